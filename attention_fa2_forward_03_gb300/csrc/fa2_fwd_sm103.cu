@@ -14,6 +14,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <utility>
 
@@ -22,6 +23,7 @@
 #include "fa2_fwd_fp8_sm103.cuh"
 #include "fa2_fwd_sm103.cuh"
 #include "fa2_fwd_d64_sm103.cuh"
+#include "fa2_kv4_sm103.cuh"
 
 // ==================================================================== host
 
@@ -56,8 +58,9 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
-// backward dQ 14-17, d = 64 equal-length forward 18-19.
-constexpr int kKernelSlots = 20;
+// backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
+// 4-bit cache 20-31.
+constexpr int kKernelSlots = 32;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -616,6 +619,251 @@ fa2_status fa2_bwd_noalloc(const void* q, const void* k, const void* v, const vo
     // read, so nothing left from an earlier call needs clearing.
     return bwd_launch(dev, q, k, v, o, lse, dout, dq, dk, dv, static_cast<float*>(ptr), B, H_q, H_kv, N, d, scale,
                       causal, dtype, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the paged 4-bit KV cache
+
+namespace {
+
+int log2_of(int x) {
+    int n = 0;
+    while ((1 << n) < x) ++n;
+    return n;
+}
+
+// Sizes that every cache entry point shares (INVALID_ARG before UNSUPPORTED).
+constexpr long long kMaxTokens = 0x7FFFFFFFLL - 256;
+fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
+    if (page_size <= 0 || num_pages <= 0 || max_pages <= 0) return FA2_ERR_INVALID_ARG;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FA2_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_pages) * page_size > kMaxTokens ||
+        static_cast<long long>(max_pages) * page_size > kMaxTokens)
+        return FA2_ERR_UNSUPPORTED;
+    return FA2_OK;
+}
+
+// Row blocks of 8, 16 or 32 query rows share one pass over the keys.
+int kv4_blocks_of_8(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+int64_t kv4_workspace(long long rows, int d) {
+    const int nr = kv4_blocks_of_8(static_cast<int>(std::min<long long>(rows, 64)));
+    return 2LL * fa2::kv4::kMaxCtas * 8 * nr * (d + 2) * static_cast<long long>(sizeof(float));
+}
+
+template <int D, int NR, bool kBf16>
+fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
+    constexpr int kSmem = static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, NR>));
+    auto kern = fa2::kv4::fa2_kv4_fwd_kernel<D, NR, kBf16>;
+    const int slot = 20 + (D == 128 ? 0 : 6) + (NR == 1 ? 0 : NR == 2 ? 2 : 4) + (kBf16 ? 0 : 1);
+    fa2_status st = set_smem(dev, slot, kern, kSmem);
+    p.rblocks = (p.rows + 8 * NR - 1) / (8 * NR);
+    p.ctas = std::min(sm_count(dev) * (NR == 1 ? 4 : 2), fa2::kv4::kMaxCtas);
+    p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
+    const dim3 grid(static_cast<unsigned>(p.ctas));
+    if (st == FA2_OK) st = launch_kernel(kern, grid, fa2::kv4::kFwdThreads, kSmem, stream, p);
+    if (st == FA2_OK)
+        st = launch_kernel(fa2::kv4::fa2_kv4_join_kernel<D, NR, kBf16>, grid, fa2::kv4::kFwdThreads, 0, stream, p);
+    return st;
+}
+
+template <int D, bool kBf16>
+fa2_status kv4_launch_rows(int dev, const fa2::kv4::FwdParams& p, cudaStream_t stream) {
+    switch (kv4_blocks_of_8(p.rows)) {
+        case 1: return kv4_launch<D, 1, kBf16>(dev, p, stream);
+        case 2: return kv4_launch<D, 2, kBf16>(dev, p, stream);
+        default: return kv4_launch<D, 4, kBf16>(dev, p, stream);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                        int32_t* free_pages, const int32_t* free_state, int32_t* seq_lens_out,
+                        int32_t* accepted, int32_t* slots, int32_t* free_state_out, int B, int N,
+                        int max_pages, int page_size, int num_pages, cudaStream_t stream) {
+    const void* ptrs[] = {seq_lens, new_lens, block_table, free_pages, free_state, seq_lens_out, accepted, slots,
+                          free_state_out};
+    for (const void* x : ptrs)
+        if (!x || !aligned4(x)) return FA2_ERR_INVALID_ARG;
+    if (B <= 0 || N <= 0) return FA2_ERR_INVALID_ARG;
+    fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
+    if (st != FA2_OK) return st;
+    if (static_cast<long long>(B) * N > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::kv4::PlanParams p{};
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.block_table = block_table;
+    p.free_pages = free_pages;
+    p.free_state = free_state;
+    p.seq_lens_out = seq_lens_out;
+    p.accepted = accepted;
+    p.slots = slots;
+    p.free_state_out = free_state_out;
+    p.B = B;
+    p.n = N;
+    p.max_pages = max_pages;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.num_pages = num_pages;
+    st = launch_kernel(fa2::kv4::fa2_kv4_plan_kernel, dim3(1), fa2::kv4::kPlanThreads, 0, stream, p);
+    if (st != FA2_OK) return st;
+    const long long n = static_cast<long long>(B) * N;
+    return launch_kernel(fa2::kv4::fa2_kv4_slots_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream,
+                         p);
+}
+
+fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, void* cache,
+                          const float* k_descale, const float* v_descale, int B, int H_kv, int N, int d,
+                          int64_t k_stride_b, int64_t k_stride_h, int64_t k_stride_n, int64_t v_stride_b,
+                          int64_t v_stride_h, int64_t v_stride_n, int page_size, int num_pages,
+                          fa2_dtype dtype, cudaStream_t stream) {
+    if (!k || !v || !slots || !cache || !k_descale || !v_descale) return FA2_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return FA2_ERR_INVALID_ARG;
+    if (!aligned4(slots) || !aligned4(k_descale) || !aligned4(v_descale)) return FA2_ERR_INVALID_ARG;
+    if (B <= 0 || H_kv <= 0 || N <= 0 || d <= 0) return FA2_ERR_INVALID_ARG;
+    for (int64_t s : {k_stride_b, k_stride_h, k_stride_n, v_stride_b, v_stride_h, v_stride_n})
+        if (s < 0 || s % 8 != 0) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_BF16 && dtype != FA2_FP16) return FA2_ERR_INVALID_ARG;
+    fa2_status st = kv4_check_pages(page_size, num_pages, 1);
+    if (st != FA2_OK) return st;
+    if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    const long long rows = static_cast<long long>(B) * H_kv;
+    if (rows > 0x7FFFFFFFLL / N) return FA2_ERR_UNSUPPORTED;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::kv4::AppendParams p{};
+    p.x[0] = k;
+    p.x[1] = v;
+    p.sb[0] = k_stride_b;
+    p.sh[0] = k_stride_h;
+    p.sn[0] = k_stride_n;
+    p.sb[1] = v_stride_b;
+    p.sh[1] = v_stride_h;
+    p.sn[1] = v_stride_n;
+    p.descale[0] = k_descale;
+    p.descale[1] = v_descale;
+    p.slots = slots;
+    p.cache = static_cast<uint8_t*>(cache);
+    p.rows = static_cast<int>(rows * N);
+    p.hkv = H_kv;
+    p.n = N;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.num_slots = num_pages * page_size;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.rows) * (d / 16) + 255) / 256));
+    const bool bf = dtype == FA2_BF16;
+    using namespace fa2::kv4;
+    if (d == 128)
+        return bf ? launch_kernel(fa2_kv4_append_kernel<128, true>, grid, 256, 0, stream, p)
+                  : launch_kernel(fa2_kv4_append_kernel<128, false>, grid, 256, 0, stream, p);
+    return bf ? launch_kernel(fa2_kv4_append_kernel<64, true>, grid, 256, 0, stream, p)
+              : launch_kernel(fa2_kv4_append_kernel<64, false>, grid, 256, 0, stream, p);
+}
+
+fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* starts, const float* k_descale, const float* v_descale, void* k,
+                          void* v, int B, int H_kv, int N, int d, int max_pages, int page_size, int num_pages,
+                          fa2_dtype dtype, cudaStream_t stream) {
+    if (!cache || !block_table || !seq_lens || !k_descale || !v_descale || !k || !v) return FA2_ERR_INVALID_ARG;
+    if (!aligned16(cache) || !aligned16(k) || !aligned16(v)) return FA2_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(starts) || !aligned4(k_descale) ||
+        !aligned4(v_descale))
+        return FA2_ERR_INVALID_ARG;
+    if (B <= 0 || H_kv <= 0 || N <= 0 || d <= 0) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_BF16 && dtype != FA2_FP16) return FA2_ERR_INVALID_ARG;
+    fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
+    if (st != FA2_OK) return st;
+    if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    const long long rows = static_cast<long long>(B) * H_kv;
+    if (rows > 0x7FFFFFFFLL / N) return FA2_ERR_UNSUPPORTED;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::kv4::GatherParams p{};
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.starts = starts;
+    p.descale[0] = k_descale;
+    p.descale[1] = v_descale;
+    p.out[0] = k;
+    p.out[1] = v;
+    p.rows = static_cast<int>(rows * N);
+    p.hkv = H_kv;
+    p.n = N;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.rows) * (d / 16) + 255) / 256));
+    const bool bf = dtype == FA2_BF16;
+    using namespace fa2::kv4;
+    if (d == 128)
+        return bf ? launch_kernel(fa2_kv4_gather_kernel<128, true>, grid, 256, 0, stream, p)
+                  : launch_kernel(fa2_kv4_gather_kernel<128, false>, grid, 256, 0, stream, p);
+    return bf ? launch_kernel(fa2_kv4_gather_kernel<64, true>, grid, 256, 0, stream, p)
+              : launch_kernel(fa2_kv4_gather_kernel<64, false>, grid, 256, 0, stream, p);
+}
+
+int64_t fa2_fwd_kv4_workspace(int H_q, int H_kv, int N_q, int d) {
+    if (H_q <= 0 || H_kv <= 0 || N_q <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128)) return -1;
+    return kv4_workspace(static_cast<long long>(H_q / H_kv) * N_q, d);
+}
+
+fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                       const float* k_descale, const float* v_descale, void* o, float* lse, void* workspace,
+                       int64_t workspace_bytes, int B, int H_q, int H_kv, int N_q, int d, int max_pages,
+                       int page_size, int num_pages, float scale, int causal, fa2_dtype dtype,
+                       cudaStream_t stream) {
+    if (!q || !cache || !block_table || !seq_lens || !k_descale || !v_descale || !o || !lse || !workspace)
+        return FA2_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace))
+        return FA2_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(k_descale) || !aligned4(v_descale))
+        return FA2_ERR_INVALID_ARG;
+    if (B <= 0 || H_q <= 0 || H_kv <= 0 || N_q <= 0 || d <= 0) return FA2_ERR_INVALID_ARG;
+    if (H_q % H_kv != 0) return FA2_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.0f)) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_BF16 && dtype != FA2_FP16) return FA2_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FA2_ERR_INVALID_ARG;
+    fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
+    if (st != FA2_OK) return st;
+    if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    const long long heads = static_cast<long long>(B) * H_q;
+    if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit
+    if (workspace_bytes < fa2_fwd_kv4_workspace(H_q, H_kv, N_q, d)) return FA2_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::kv4::FwdParams p{};
+    p.q = q;
+    p.cache = static_cast<const uint8_t*>(cache);
+    p.k_descale = k_descale;
+    p.v_descale = v_descale;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.o = o;
+    p.lse = lse;
+    p.part_o = static_cast<float*>(workspace);
+    p.B = B;
+    p.hkv = H_kv;
+    p.nq = N_q;
+    p.rows = H_q / H_kv * N_q;
+    p.max_pages = max_pages;
+    p.max_tokens = max_pages * page_size;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.num_pages = num_pages;
+    p.causal = causal;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    const bool bf = dtype == FA2_BF16;
+    if (d == 128)
+        return bf ? kv4_launch_rows<128, true>(dev, p, stream) : kv4_launch_rows<128, false>(dev, p, stream);
+    return bf ? kv4_launch_rows<64, true>(dev, p, stream) : kv4_launch_rows<64, false>(dev, p, stream);
 }
 
 fa2_status fa2_check_status(cudaStream_t stream) {

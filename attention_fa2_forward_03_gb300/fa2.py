@@ -20,11 +20,12 @@ FA2_ERR_INVALID_ARG = 1
 FA2_ERR_UNSUPPORTED = 2
 FA2_ERR_CUDA = 3
 FA2_ERR_TIMEOUT = 4
-FA2_ERR_BOUNDS = 5   # debug builds only: a device-side bounds check failed
+FA2_ERR_BOUNDS = 5   # a device-side bounds check failed (KV cache: every build; others: debug builds)
 
 # symbols declared in include/fa2.h
-EXPORTS = ("fa2_fwd", "fa2_fwd_gqa", "fa2_fwd_ex", "fa2_fwd_fp8", "fa2_fwd_fp8_ex", "fa2_bwd", "fa2_bwd_noalloc", "fa2_check_status",
-           "fa2_status_string",
+EXPORTS = ("fa2_fwd", "fa2_fwd_gqa", "fa2_fwd_ex", "fa2_fwd_fp8", "fa2_fwd_fp8_ex", "fa2_bwd", "fa2_bwd_noalloc",
+           "fa2_kv4_plan", "fa2_kv4_append", "fa2_kv4_gather", "fa2_fwd_kv4", "fa2_fwd_kv4_workspace",
+           "fa2_check_status", "fa2_status_string",
            "fa2_set_wait_limit_ns", "fa2_set_debug_flags", "fa2_set_tile_config", "fa2_version")
 
 _lib = None
@@ -60,6 +61,17 @@ def load(path: str = LIB_PATH):
     lib.fa2_bwd.restype = i
     lib.fa2_bwd_noalloc.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, f, i, i, p]
     lib.fa2_bwd_noalloc.restype = i
+    ll = ctypes.c_int64
+    lib.fa2_kv4_plan.argtypes = [p, p, p, p, p, p, p, p, p, i, i, i, i, i, p]
+    lib.fa2_kv4_plan.restype = i
+    lib.fa2_kv4_append.argtypes = [p, p, p, p, p, p, i, i, i, i, ll, ll, ll, ll, ll, ll, i, i, i, p]
+    lib.fa2_kv4_append.restype = i
+    lib.fa2_kv4_gather.argtypes = [p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, i, p]
+    lib.fa2_kv4_gather.restype = i
+    lib.fa2_fwd_kv4.argtypes = [p, p, p, p, p, p, p, p, p, ll, i, i, i, i, i, i, i, i, f, i, i, p]
+    lib.fa2_fwd_kv4.restype = i
+    lib.fa2_fwd_kv4_workspace.argtypes = [i, i, i, i]
+    lib.fa2_fwd_kv4_workspace.restype = ll
     lib.fa2_check_status.argtypes = [p]
     lib.fa2_check_status.restype = i
     lib.fa2_status_string.argtypes = [i]
@@ -127,6 +139,41 @@ def fa2_bwd_noalloc_ptr(q, k, v, o, lse, dout, dq, dk, dv, B, H_q, H_kv, N, d, s
     memory (at most 2**20 query rows). Returns the status code."""
     return load().fa2_bwd_noalloc(q, k, v, o, lse, dout, dq, dk, dv, B, H_q, H_kv, N, d, float(scale),
                                   int(causal), int(dtype), stream or None)
+
+
+def fa2_kv4_plan_ptr(seq_lens, new_lens, block_table, free_pages, free_state, seq_lens_out, accepted, slots,
+                     free_state_out, B, N, max_pages, page_size, num_pages, stream=0) -> int:
+    """fa2_kv4_plan on raw device addresses (ints); returns the status code."""
+    return load().fa2_kv4_plan(seq_lens, new_lens, block_table, free_pages, free_state, seq_lens_out, accepted,
+                               slots, free_state_out, B, N, max_pages, page_size, num_pages, stream or None)
+
+
+def fa2_kv4_append_ptr(k, v, slots, cache, k_descale, v_descale, B, H_kv, N, d, k_strides, v_strides, page_size,
+                       num_pages, dtype, stream=0) -> int:
+    """fa2_kv4_append on raw device addresses (ints), strides (request, head,
+    token) in elements; returns the status code."""
+    return load().fa2_kv4_append(k, v, slots, cache, k_descale, v_descale, B, H_kv, N, d, *k_strides, *v_strides,
+                                 page_size, num_pages, int(dtype), stream or None)
+
+
+def fa2_kv4_gather_ptr(cache, block_table, seq_lens, starts, k_descale, v_descale, k, v, B, H_kv, N, d, max_pages,
+                       page_size, num_pages, dtype, stream=0) -> int:
+    """fa2_kv4_gather on raw device addresses (ints; starts may be 0); returns the status code."""
+    return load().fa2_kv4_gather(cache, block_table, seq_lens, starts or None, k_descale, v_descale, k, v, B, H_kv,
+                                 N, d, max_pages, page_size, num_pages, int(dtype), stream or None)
+
+
+def fa2_fwd_kv4_ptr(q, cache, block_table, seq_lens, k_descale, v_descale, o, lse, workspace, workspace_bytes, B,
+                    H_q, H_kv, N_q, d, max_pages, page_size, num_pages, scale, causal, dtype, stream=0) -> int:
+    """fa2_fwd_kv4 on raw device addresses (ints); returns the status code."""
+    return load().fa2_fwd_kv4(q, cache, block_table, seq_lens, k_descale, v_descale, o, lse, workspace,
+                              workspace_bytes, B, H_q, H_kv, N_q, d, max_pages, page_size, num_pages, float(scale),
+                              int(causal), int(dtype), stream or None)
+
+
+def fa2_fwd_kv4_workspace(H_q: int, H_kv: int, N_q: int, d: int) -> int:
+    """Bytes of workspace that fa2_fwd_kv4 needs, -1 for sizes that it does not take."""
+    return load().fa2_fwd_kv4_workspace(H_q, H_kv, N_q, d)
 
 
 def fa2_check_status(stream=0) -> int:
@@ -342,3 +389,187 @@ def fa2_fwd(q, k, v, o=None, lse=None, scale=None, stream=None):
     if q.shape[1] != k.shape[1]:
         raise ValueError("fa2_fwd needs equal head counts; use fa2_fwd_gqa")
     return fa2_fwd_gqa(q, k, v, o, lse, scale, stream)
+
+
+# ------------------------------------------------------------------ the paged 4-bit KV cache
+
+def fa2_kv4_cache_shape(num_pages: int, H_kv: int, page_size: int, d: int) -> tuple:
+    """Shape of the uint8 cache tensor (layout: include/fa2.h)."""
+    return (num_pages, H_kv, 2, page_size * (d // 2 + d // 16))
+
+
+def _kv4_call(fn, device, stream, *args):
+    """Runs a C entry point with `device` current (the library launches on
+    the current device)."""
+    import torch
+
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return fn(*args, _stream_handle(stream, device))
+    return fn(*args, _stream_handle(stream, device))
+
+
+def _kv4_same_device(device, *tensors):
+    for t in tensors:
+        if t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+
+
+def _kv4_ints(name, t, shape):
+    import torch
+
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _kv4_cache(cache, k_descale, v_descale, H_kv, d):
+    """Checks the cache and its descales; returns (num_pages, page_size)."""
+    import torch
+
+    token = max(1, d // 2 + d // 16)
+    if (cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_cuda or not cache.is_contiguous()
+            or cache.shape[1] != H_kv or cache.shape[2] != 2 or cache.shape[3] == 0 or cache.shape[3] % token):
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [num_pages, H_kv, 2, page_size*(d/2+d/16)]")
+    for t in (k_descale, v_descale):
+        if t.dtype != torch.float32 or t.shape != (H_kv,) or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("descales must be contiguous fp32 CUDA tensors [H_kv]")
+    return cache.shape[0], cache.shape[3] // token
+
+
+def fa2_kv4_plan(seq_lens, new_lens, block_table, free_pages, free_state, page_size, N, seq_lens_out=None,
+                 accepted=None, slots=None, free_state_out=None, stream=None):
+    """Pages and slots of one scheduling step (include/fa2.h).
+
+    seq_lens, new_lens [B], block_table [B, max_pages] (updated), free_pages
+    [num_pages] (a ring, updated), free_state [2]: int32 CUDA tensors; N: the
+    most tokens a request may add. seq_lens_out and free_state_out may be
+    seq_lens and free_state themselves. Returns (seq_lens_out [B],
+    accepted [B], slots [B, N], free_state_out [2])."""
+    import torch
+
+    if seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("seq_lens must be [B], block_table [B, max_pages], free_pages [num_pages]")
+    B, W = block_table.shape
+    dev = seq_lens.device
+    seq_lens_out = torch.empty_like(seq_lens) if seq_lens_out is None else seq_lens_out
+    accepted = torch.empty_like(seq_lens) if accepted is None else accepted
+    slots = torch.empty((B, N), dtype=torch.int32, device=dev) if slots is None else slots
+    free_state_out = torch.empty_like(free_state) if free_state_out is None else free_state_out
+    for name, t, shape in (("seq_lens", seq_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("block_table", block_table, (B, W)), ("free_pages", free_pages, free_pages.shape),
+                           ("free_state", free_state, (2,)), ("seq_lens_out", seq_lens_out, (B,)),
+                           ("accepted", accepted, (B,)), ("slots", slots, (B, N)),
+                           ("free_state_out", free_state_out, (2,))):
+        _kv4_ints(name, t, shape)
+    _kv4_same_device(dev, new_lens, block_table, free_pages, free_state, seq_lens_out, accepted, slots,
+                     free_state_out)
+    rc = _kv4_call(fa2_kv4_plan_ptr, dev, stream, seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                   free_pages.data_ptr(), free_state.data_ptr(), seq_lens_out.data_ptr(), accepted.data_ptr(),
+                   slots.data_ptr(), free_state_out.data_ptr(), B, N, W, page_size, free_pages.shape[0])
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_kv4_plan")
+    return seq_lens_out, accepted, slots, free_state_out
+
+
+def fa2_kv4_append(k, v, slots, cache, k_descale, v_descale, stream=None):
+    """Quantises k, v [B, Hkv, N, d] (any strides that are multiples of 8
+    elements, rows of adjacent elements) into the slots [B, N] of the cache; negative slots
+    are skipped. Returns the cache."""
+    if k.dim() != 4 or k.shape != v.shape:
+        raise ValueError("k and v must be 4-D [B, H_kv, N, d] of one shape")
+    B, Hkv, N, d = k.shape
+    if k.dtype != v.dtype:
+        raise TypeError("k and v must share one dtype")
+    for t in (k, v):
+        if not t.is_cuda or t.stride(3) != 1:
+            raise ValueError("k and v must be CUDA tensors whose rows are adjacent elements")
+    num_pages, page_size = _kv4_cache(cache, k_descale, v_descale, Hkv, d)
+    _kv4_ints("slots", slots, (B, N))
+    _kv4_same_device(k.device, v, slots, cache, k_descale, v_descale)
+    # the stride of an axis of length 1 is never used and may be anything
+    ks, vs = (tuple(s if n > 1 else 0 for s, n in zip(t.stride(), t.shape))[:3] for t in (k, v))
+    rc = _kv4_call(fa2_kv4_append_ptr, k.device, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
+                   cache.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), B, Hkv, N, d, ks, vs, page_size,
+                   num_pages, _dtype_code(k))
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_kv4_append")
+    return cache
+
+
+def fa2_kv4_gather(cache, block_table, seq_lens, k_descale, v_descale, N, d, starts=None, dtype=None, k=None, v=None,
+                   stream=None):
+    """Reads cached tokens back: k, v [B, Hkv, N, d] of `dtype` (bf16 by
+    default, or k's), row i of request b its position starts[b] + i (starts
+    None: i); rows at or past seq_lens[b] are zeros. Returns (k, v)."""
+    import torch
+
+    if block_table.dim() != 2 or cache.dim() != 4:
+        raise ValueError("block_table must be [B, max_pages], cache [num_pages, H_kv, 2, page_size*(d/2+d/16)]")
+    (B, W), Hkv = block_table.shape, cache.shape[1]
+    num_pages, page_size = _kv4_cache(cache, k_descale, v_descale, Hkv, d)
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
+    k = torch.empty((B, Hkv, N, d), dtype=dtype, device=cache.device) if k is None else k
+    v = torch.empty((B, Hkv, N, d), dtype=dtype, device=cache.device) if v is None else v
+    for t in (k, v):
+        if t.shape != (B, Hkv, N, d) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise ValueError("k and v must be contiguous CUDA tensors [B, H_kv, N, d] of one dtype")
+    _kv4_ints("block_table", block_table, (B, W))
+    _kv4_ints("seq_lens", seq_lens, (B,))
+    _kv4_same_device(cache.device, block_table, seq_lens, k_descale, v_descale, k, v)
+    if starts is not None:
+        _kv4_ints("starts", starts, (B,))
+        _kv4_same_device(cache.device, starts)
+    rc = _kv4_call(fa2_kv4_gather_ptr, cache.device, stream, cache.data_ptr(), block_table.data_ptr(),
+                   seq_lens.data_ptr(), 0 if starts is None else starts.data_ptr(), k_descale.data_ptr(),
+                   v_descale.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, N, d, W, page_size, num_pages,
+                   _dtype_code(k))
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_kv4_gather")
+    return k, v
+
+
+def fa2_fwd_kv4(q, cache, block_table, seq_lens, k_descale, v_descale, o=None, lse=None, workspace=None, scale=None,
+                causal=False, stream=None):
+    """Attention of the newest N_q tokens of each request, q [B, Hq, Nq, d],
+    over its seq_lens[b] cached tokens. `workspace`: a uint8 CUDA tensor of
+    fa2_fwd_kv4_workspace(Hq, Hkv, Nq, d) bytes that no other call in flight
+    uses; allocated with torch when not given, as o and lse are. Returns
+    (o [B, Hq, Nq, d], lse fp32 [B, Hq, Nq])."""
+    import torch
+
+    if q.dim() != 4 or cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [B, H_q, N_q, d], cache 4-D and block_table [B, max_pages]")
+    B, Hq, Nq, d = q.shape
+    Hkv, W = cache.shape[1], block_table.shape[1]
+    if not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA tensor")
+    num_pages, page_size = _kv4_cache(cache, k_descale, v_descale, Hkv, d)
+    _kv4_ints("block_table", block_table, (B, W))
+    _kv4_ints("seq_lens", seq_lens, (B,))
+    dev = q.device
+    if o is None:
+        o = torch.empty_like(q)
+    elif o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
+        raise ValueError("o must be a contiguous tensor like q")
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    elif lse.shape != (B, Hq, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, H_q, N_q]")
+    if workspace is None:
+        workspace = torch.empty(max(fa2_fwd_kv4_workspace(Hq, Hkv, Nq, d), 16), dtype=torch.uint8, device=dev)
+        if stream is not None:   # freed below while `stream` may still use it
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _kv4_same_device(dev, cache, block_table, seq_lens, k_descale, v_descale, o, lse, workspace)
+    if scale is None:
+        scale = d ** -0.5
+    rc = _kv4_call(fa2_fwd_kv4_ptr, dev, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
+                   seq_lens.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, Hq, Hkv, Nq, d, W,
+                   page_size, num_pages, scale, bool(causal), _dtype_code(q))
+    if rc != FA2_OK:
+        raise FA2Error(rc, "fa2_fwd_kv4")
+    return o, lse

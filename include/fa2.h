@@ -66,9 +66,10 @@ typedef enum {
                                  compute capability 10.3 */
     FA2_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed */
     FA2_ERR_TIMEOUT = 4,      /* the kernel's watchdog gave up on a wait */
-    FA2_ERR_BOUNDS = 5        /* debug builds only (libfa2_debug.so, compiled
-                                 with FA2_DEBUG): a device-side bounds check
-                                 failed and the access was skipped */
+    FA2_ERR_BOUNDS = 5        /* a device-side bounds check failed and the access
+                                 was skipped: a page id, slot or length of the KV
+                                 cache entry points, or anything in the debug
+                                 build (libfa2_debug.so, compiled with FA2_DEBUG) */
 } fa2_status;
 
 /*
@@ -231,11 +232,125 @@ fa2_status fa2_bwd_noalloc(const void* q, const void* k, const void* v, const vo
                            fa2_dtype dtype, cudaStream_t stream);
 
 /*
+ * A paged KV cache held in 4 bits, for serving. (The source pages leave the
+ * KV cache out; these four entry points extend the library.) The cache is the
+ * caller's device memory, one block of bytes
+ *     cache : [num_pages, H_kv, 2, page_size * (d/2 + d/16)]
+ * Part 0 of a (page, KV head) holds the keys of page_size tokens, part 1 the
+ * values: first the e2m1 codes [page_size, d/2] (OCP FP4 E2M1; element 2i of
+ * a token in the low four bits of byte i), then an OCP FP8 E4M3 scale for each
+ * 16 elements [page_size, d/16]. An element stands for
+ *     code * scale * descale[h]
+ * with k_descale, v_descale : [H_kv] fp32, device, finite and > 0 (a head's
+ * largest magnitude over 6 * 448 uses the whole range). That is 4.5 bits an
+ * element. A token's place is its slot, page * page_size + offset; request b's
+ * position i lies in page block_table[b, i / page_size] at offset
+ * i % page_size. Table entries behind a request's last page are never read.
+ *   d         : 64 or 128
+ *   page_size : 16, 32, 64 or 128; num_pages * page_size < 2^31 - 256
+ *   block_table : [B, max_pages] int32, max_pages * page_size < 2^31 - 256
+ * Page ids, slots and lengths come from device memory: one that points outside
+ * the cache or the table is skipped on the device in every build and reported
+ * by fa2_check_status as FA2_ERR_BOUNDS. Pointers: cache, tensors and
+ * workspace 16-byte aligned, int32 and descale arrays 4-byte aligned. Errors
+ * otherwise as fa2_fwd_gqa; nothing is allocated.
+ */
+
+/*
+ * Pages and slots of one scheduling step, from the request lengths.
+ *   seq_lens  : [B] int32, tokens that request b has in the cache
+ *   new_lens  : [B] int32, tokens this step adds (0 .. N), or negative: the
+ *               request ends and gives its pages back
+ *   block_table : [B, max_pages] int32, in and out: the entries of new pages
+ *               are written, all others stay as they were
+ *   free_pages, free_state : a ring of free page ids [num_pages] int32 and
+ *               {index of the first, how many} int32. New pages are taken from
+ *               its front; pages given back are written behind its end and are
+ *               handed out from the next call on
+ *   seq_lens_out : [B] int32, the lengths after the step (may be seq_lens)
+ *   accepted  : [B] int32, new_lens[b] if the request got its pages, else 0
+ *   slots     : [B, N] int32, the slots of the accepted tokens, -1 in the
+ *               other places
+ *   free_state_out : [2] int32 (may be free_state)
+ * Requests are served in order. One that needs pages gets them iff the pages
+ * wanted by the requests up to and including it are free; one that needs none
+ * (its last page has room) always gets its slots. new_lens[b] > N, or a length
+ * that its table row cannot hold, is not accepted and wants no page. A length
+ * below 0 or above max_pages * page_size counts as 0 and is reported, and so
+ * is a ring that is not one. A page that two requests share must be given back
+ * once only. One or two launches; calls that share a ring must be ordered.
+ */
+fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                        int32_t* free_pages, const int32_t* free_state, int32_t* seq_lens_out,
+                        int32_t* accepted, int32_t* slots, int32_t* free_state_out, int B, int N,
+                        int max_pages, int page_size, int num_pages, cudaStream_t stream);
+
+/*
+ * Quantises new keys and values and writes them into their slots.
+ *   k, v   : [B, H_kv, N, d] bf16 or fp16, elements of a row adjacent; the
+ *            strides of request, head and token are given in elements
+ *            (multiples of 8, >= 0) so that views of a projection's output need no copy
+ *   slots  : [B, N] int32; a negative slot is skipped. A slot named twice in
+ *            one call holds, 16 elements by 16 elements, either token
+ * For each 16 elements x: scale = e4m3(max|x| / (6 descale)), t = scale *
+ * descale in fp32, code = e2m1(x / t), every rounding to nearest, ties to
+ * even, limited to the format's largest value; t = 0 gives codes 0. 16
+ * elements that hold a NaN or an infinity read back as NaN.
+ */
+fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, void* cache,
+                          const float* k_descale, const float* v_descale, int B, int H_kv, int N, int d,
+                          int64_t k_stride_b, int64_t k_stride_h, int64_t k_stride_n, int64_t v_stride_b,
+                          int64_t v_stride_h, int64_t v_stride_n, int page_size, int num_pages,
+                          fa2_dtype dtype, cudaStream_t stream);
+
+/*
+ * Reads cached tokens back as 16-bit tensors, for instance the context of a
+ * prompt's next chunk, for fa2_fwd_ex.
+ *   starts : [B] int32 or NULL (all 0): the position of row 0
+ *   k, v   : [B, H_kv, N, d] (output); row i is position starts[b] + i, each
+ *            value code * (scale * descale) in fp32, rounded once. Rows at or
+ *            past seq_lens[b], before position 0 or on a bad page are zeros
+ */
+fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* starts, const float* k_descale, const float* v_descale, void* k,
+                          void* v, int B, int H_kv, int N, int d, int max_pages, int page_size, int num_pages,
+                          fa2_dtype dtype, cudaStream_t stream);
+
+/*
+ * Attention of the N_q newest tokens of each request over its cached tokens
+ * (their own keys and values included, if they were appended).
+ *   q, o : [B, H_q, N_q, d] 16-bit; lse : [B, H_q, N_q] fp32
+ *   seq_lens : [B] int32, cached tokens of each request; 0 for an idle row
+ *   causal   : 0 or 1. With 1, query row i attends position
+ *              j < seq_lens[b] + i + 1 - N_q, as fa2_fwd_ex. A row with no
+ *              allowed key gets O = 0 and LSE = -inf
+ *   workspace : device, fa2_fwd_kv4_workspace(...) bytes, contents irrelevant
+ *              before and after; calls that may overlap need their own
+ * Any N_q >= 1 is right; the kernel is made for few rows a KV head
+ * (H_q / H_kv * N_q up to 32 read the cache once, every 32 more once again).
+ * Prompts and their chunks are faster by fa2_kv4_gather and fa2_fwd_ex.
+ * Query rows hold no precision less than q's own; the softmax weights are
+ * rounded to fp16 (2^-11), sums are fp32. A row of q that is not finite
+ * affects no other row. A NaN in the cache affects the rows that see it.
+ * B * H_q * N_q < 2^31 - 64. Two launches in stream order.
+ */
+fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                       const float* k_descale, const float* v_descale, void* o, float* lse, void* workspace,
+                       int64_t workspace_bytes, int B, int H_q, int H_kv, int N_q, int d, int max_pages,
+                       int page_size, int num_pages, float scale, int causal, fa2_dtype dtype,
+                       cudaStream_t stream);
+
+/* Bytes of workspace that fa2_fwd_kv4 needs for these sizes, whatever B and
+ * the lengths; -1 for sizes that it does not take. */
+int64_t fa2_fwd_kv4_workspace(int H_q, int H_kv, int N_q, int d);
+
+/*
  * Synchronises `stream`, then reads and clears the status word of the device
  * that `stream` belongs to (the current device is switched to it for the
  * read and restored afterwards). Returns FA2_ERR_TIMEOUT if a kernel since
  * the last check abandoned a wait (its outputs are then undefined),
- * FA2_ERR_BOUNDS if (debug builds only) a device-side bounds check failed,
+ * FA2_ERR_BOUNDS if a device-side bounds check failed (the KV cache's checks
+ * are in every build, all others in debug builds only),
  * FA2_ERR_CUDA if the stream reported an error, FA2_OK otherwise.
  * There is one status word per device, shared by every stream and host
  * thread that uses the device: a timeout of a kernel on another stream is
