@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -59,8 +60,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
-// 4-bit cache 20-31.
-constexpr int kKernelSlots = 32;
+// 4-bit cache 20-35.
+constexpr int kKernelSlots = 36;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -644,35 +645,59 @@ fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
     return FA2_OK;
 }
 
-// Row blocks of 8, 16 or 32 query rows share one pass over the keys.
-int kv4_blocks_of_8(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// A pass over the keys serves a row block of 8 NR query rows, NR <= 4 (what
+// the registers hold); more rows are cut into blocks of about equal size.
+int kv4_nr(long long rows) {
+    const long long blocks = (rows + 31) / 32;
+    return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
+}
 
+// Workspace: two partial results a CTA, then a counter a CTA.
+int64_t kv4_part_floats(int nr, int d) { return 2LL * fa2::kv4::kMaxCtas * 8 * nr * (d + 2); }
 int64_t kv4_workspace(long long rows, int d) {
-    const int nr = kv4_blocks_of_8(static_cast<int>(std::min<long long>(rows, 64)));
-    return 2LL * fa2::kv4::kMaxCtas * 8 * nr * (d + 2) * static_cast<long long>(sizeof(float));
+    return kv4_part_floats(kv4_nr(rows), d) * static_cast<int64_t>(sizeof(float)) +
+           fa2::kv4::kMaxCtas * static_cast<int64_t>(sizeof(unsigned long long));
+}
+
+// A number that no other launch of this process has, and that memory left
+// by anything else holds only by a chance of 2^-48; low 16 bits 0.
+unsigned long long kv4_nonce() {
+    static const unsigned long long seed =
+        static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count()) * 0x9E3779B97F4A7C15ULL ^
+        reinterpret_cast<uintptr_t>(&g_mu) * 0xD1B54A32D192ED03ULL;
+    static std::atomic<unsigned long long> calls{seed};
+    unsigned long long n = 0;
+    while (n == 0) n = (calls.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4A7C15ULL) << 16;
+    return n;
 }
 
 template <int D, int NR, bool kBf16>
 fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
     constexpr int kSmem = static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, NR>));
+    using Shape = fa2::kv4::Shape<NR>;
+    static_assert(Shape::kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory budget");
     auto kern = fa2::kv4::fa2_kv4_fwd_kernel<D, NR, kBf16>;
-    const int slot = 20 + (D == 128 ? 0 : 6) + (NR == 1 ? 0 : NR == 2 ? 2 : 4) + (kBf16 ? 0 : 1);
-    fa2_status st = set_smem(dev, slot, kern, kSmem);
+    const int slot = 20 + (D == 128 ? 0 : 8) + 2 * (NR - 1) + (kBf16 ? 0 : 1);
+    const fa2_status st = set_smem(dev, slot, kern, kSmem);
+    if (st != FA2_OK) return st;
     p.rblocks = (p.rows + 8 * NR - 1) / (8 * NR);
-    p.ctas = std::min(sm_count(dev) * (NR == 1 ? 4 : 2), fa2::kv4::kMaxCtas);
-    p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
-    const dim3 grid(static_cast<unsigned>(p.ctas));
-    if (st == FA2_OK) st = launch_kernel(kern, grid, fa2::kv4::kFwdThreads, kSmem, stream, p);
-    if (st == FA2_OK)
-        st = launch_kernel(fa2::kv4::fa2_kv4_join_kernel<D, NR, kBf16>, grid, fa2::kv4::kFwdThreads, 0, stream, p);
-    return st;
+    p.ctas = std::min(sm_count(dev) * Shape::kCtas, fa2::kv4::kMaxCtas);
+    // units of the line are 32-bit, and padding can double them
+    if (static_cast<long long>(p.B) * p.hkv * p.rblocks * ((p.max_tokens + fa2::kv4::kTile - 1LL) / fa2::kv4::kTile) >
+        (1LL << 30))
+        return FA2_ERR_UNSUPPORTED;
+    p.part_ml = p.part_o + 2LL * fa2::kv4::kMaxCtas * 8 * NR * D;
+    p.arrived = reinterpret_cast<unsigned long long*>(p.part_o + kv4_part_floats(NR, D));
+    p.nonce = kv4_nonce();
+    return launch_kernel(kern, dim3(static_cast<unsigned>(p.ctas)), Shape::kThreads, kSmem, stream, p);
 }
 
 template <int D, bool kBf16>
 fa2_status kv4_launch_rows(int dev, const fa2::kv4::FwdParams& p, cudaStream_t stream) {
-    switch (kv4_blocks_of_8(p.rows)) {
+    switch (kv4_nr(p.rows)) {
         case 1: return kv4_launch<D, 1, kBf16>(dev, p, stream);
         case 2: return kv4_launch<D, 2, kBf16>(dev, p, stream);
+        case 3: return kv4_launch<D, 3, kBf16>(dev, p, stream);
         default: return kv4_launch<D, 4, kBf16>(dev, p, stream);
     }
 }
@@ -835,7 +860,8 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     if (st != FA2_OK) return st;
     if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
     const long long heads = static_cast<long long>(B) * H_q;
-    if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit
+    if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit,
+    if (H_kv > 65535 / 2) return FA2_ERR_UNSUPPORTED;                    // and a page's bytes
     if (workspace_bytes < fa2_fwd_kv4_workspace(H_q, H_kv, N_q, d)) return FA2_ERR_INVALID_ARG;
     int dev = 0;
     if ((st = check_device(&dev)) != FA2_OK) return st;
@@ -858,6 +884,8 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
+    p.part = page_size * (d / 2 + d / 16);
+    p.page_bytes = H_kv * 2 * p.part;
     p.causal = causal;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     const bool bf = dtype == FA2_BF16;

@@ -348,9 +348,17 @@ __global__ void __launch_bounds__(256) fa2_kv4_slots_kernel(const PlanParams p) 
 // ------------------------------------------------------------------ attention
 
 constexpr int kTile = 32;      // tokens a warp takes at a time
-constexpr int kWarps = 4;
-constexpr int kFwdThreads = 32 * kWarps;
-constexpr int kMaxCtas = 640;  // workspace is sized for this many
+constexpr int kMaxCtas = 320;  // workspace is sized for this many
+constexpr int kMinRun = 16;    // tiles a CTA's run has at least
+
+// Warps a CTA and CTAs an SM by the rows a pass over the keys serves: what
+// the accumulators leave room for in the registers.
+template <int NR>
+struct Shape {
+    static constexpr int kWarps = NR == 2 || NR == 3 ? 12 : 8;
+    static constexpr int kCtas = NR == 1 ? 2 : 1;
+    static constexpr int kThreads = 32 * kWarps;
+};
 
 struct FwdParams {
     const void* q;             // [B, H_q, N_q, D]: `rows` contiguous rows a KV head
@@ -363,8 +371,11 @@ struct FwdParams {
     float* lse;
     float* part_o;             // [2 * ctas, 8 NR, D]
     float* part_ml;            // [2 * ctas, 8 NR, 2]
+    unsigned long long* arrived;  // [ctas]
+    unsigned long long nonce;  // of this launch, low 16 bits 0
     int B, hkv, nq, rows, rblocks;   // rows = group * N_q; rblocks = ceil(rows / (8 NR))
     int max_pages, max_tokens, page, log2_page, num_pages;
+    int part, page_bytes;      // bytes of keys (or values) of a head's page, of a page of all heads
     int causal;
     int ctas;                  // CTAs that take work
     float scale_log2;
@@ -379,6 +390,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same into accumulators that were zero.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The transpose of an 8 x 8 matrix of 16-bit elements held two a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
@@ -386,97 +406,203 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return r;
 }
 
-// The work: the tiles of every (request, KV head, row block), in that order,
-// as one line of units cut into equal runs, one a CTA. A run may end inside a
-// segment (the tiles of one row block); its CTAs then leave partial results.
-struct Cursor {
-    long long u, end;          // next unit, end of the run
-    int b, hr, tile, tiles;    // request, head * rblocks + row block, next tile of the segment, its tiles
-};
-
-__device__ __forceinline__ int tiles_of(const FwdParams& p, int b) {
-    const int len = min(max(p.seq_lens[b], 0), p.max_tokens);
-    return (len >> 5) + ((len & 31) != 0);
+// Shared-memory loads at 32-bit addresses.
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
 }
 
-// Finds unit `u` of the line for the caller's whole block: per = units a CTA,
-// total = all units. Uses shared memory `sm` (kFwdThreads / 32 + 4 values).
-// first_run: u = blockIdx.x * per, else u = (blockIdx.x + 1) * per - 1.
-__device__ __forceinline__ bool locate(const FwdParams& p, bool last, long long* sm, long long& per, long long& total,
-                                       Cursor& cur) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    const int chunk = (p.B + nt - 1) / nt;
-    const int b0 = min(tid * chunk, p.B), b1 = min(b0 + chunk, p.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(p, b);
-    long long inc = mine;
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The work: the tiles of every (request, KV head, row block), in that order,
+// as one line of units cut into equal runs, one a CTA: every CTA has the same
+// amount whatever the lengths, which only the device knows. A run may end
+// inside a segment (the tiles of one row block); its CTAs then leave partial
+// results, and the last of them to finish joins them. Where the segments are
+// so few that each CTA can begin one at its own run's start, the segments are
+// padded to whole runs (`pad` = per, else 1), so that no CTA has two.
+struct Cursor {
+    int u, end;                // first unit of the segment's part in this run, end of the run
+    int b, hr, tile;           // request, head * rblocks + row block, first tile of the part
+    int len, tiles;            // the request's tokens and tiles
+};
+
+__device__ __forceinline__ int length_of(const FwdParams& p, int b) { return min(max(p.seq_lens[b], 0), p.max_tokens); }
+__device__ __forceinline__ int tiles_in(int len) { return (len >> 5) + ((len & 31) != 0); }
+__device__ __forceinline__ int padded(int tiles, int pad) { return (tiles + pad - 1) / pad * pad; }
+
+// Exclusive prefix sum over the block's threads of `mine`, and the total.
+template <int W>
+__device__ __forceinline__ int scan_units(int mine, int& total, int* sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(~0u, inc, o);
-        if ((tid & 31) >= o) inc += t;
+        const int t = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += t;
     }
-    if ((tid & 31) == 31) sm[tid >> 5] = inc;
-    if (tid == 0) sm[nt / 32] = -1;
+    if (lane == 31) sm[warp] = inc;
     __syncthreads();
-    long long before = 0;
+    int before = 0;
     total = 0;
-    for (int w = 0; w < nt / 32; ++w) {
-        if (w == (tid >> 5)) before = total;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w == warp) before = total;
         total += sm[w];
     }
+    return before + inc - mine;
+}
+
+// The start of this CTA's run; false if it has none. `sm`: 2 W + 3 ints.
+template <int W>
+__device__ __forceinline__ bool locate(const FwdParams& p, int* sm, Cursor& cur, int& per, int& pad) {
+    const int tid = threadIdx.x;
+    const int chunk = (p.B + 32 * W - 1) / (32 * W);
+    const int b0 = min(tid * chunk, p.B), b1 = min(b0 + chunk, p.B);
     const int hrs = p.hkv * p.rblocks;
+    int mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += tiles_in(length_of(p, b));
+    int at = scan_units<W>(mine, total, sm) * hrs;
     total *= hrs;
-    per = (total + p.ctas - 1) / p.ctas;
-    per = (per + kWarps - 1) / kWarps * kWarps;
-    const long long u = last ? (blockIdx.x + 1) * per - 1 : blockIdx.x * per;
-    long long at = (before + inc - mine) * hrs;   // first unit of request b0
-    if (u < total && u >= at && u < at + mine * hrs) {
-        int b = b0;
-        long long t = tiles_of(p, b) * static_cast<long long>(hrs);
+    if (total == 0) return false;
+    per = max((total + p.ctas - 1) / p.ctas, kMinRun);
+    per = (per + W - 1) / W * W;
+    pad = 1;
+    if (p.B * hrs <= p.ctas) {
+        int mine_p = 0, total_p;
+        for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in(length_of(p, b)), per);
+        const int at_p = scan_units<W>(mine_p, total_p, sm + W) * hrs;
+        if (total_p * hrs <= p.ctas * per) {
+            pad = per;
+            total = total_p * hrs;
+            at = at_p;
+            mine = mine_p;
+        }
+    }
+    const int u = static_cast<int>(blockIdx.x) * per;
+    if (u >= total) return false;
+    if (u >= at && u < at + mine * hrs) {
+        int b = b0, len = length_of(p, b), t = padded(tiles_in(len), pad) * hrs;
         while (u >= at + t) {
             at += t;
-            ++b;
-            t = tiles_of(p, b) * static_cast<long long>(hrs);
+            len = length_of(p, ++b);
+            t = padded(tiles_in(len), pad) * hrs;
         }
-        sm[nt / 32] = b;
-        sm[nt / 32 + 1] = u - at;
+        sm[2 * W] = b;
+        sm[2 * W + 1] = u - at;
+        sm[2 * W + 2] = len;
     }
     __syncthreads();
-    if (u >= total) return false;
     cur.u = u;
     cur.end = min(total, u + per);
-    cur.b = static_cast<int>(sm[nt / 32]);
-    cur.tiles = tiles_of(p, cur.b);
-    const long long rem = sm[nt / 32 + 1];
-    cur.hr = static_cast<int>(rem / cur.tiles);
-    cur.tile = static_cast<int>(rem - static_cast<long long>(cur.hr) * cur.tiles);
+    cur.b = sm[2 * W];
+    cur.len = sm[2 * W + 2];
+    cur.tiles = tiles_in(cur.len);
+    const int rem = sm[2 * W + 1], seg = padded(cur.tiles, pad);
+    cur.hr = rem / seg;
+    cur.tile = rem - cur.hr * seg;
     return true;
 }
 
-// Past the current segment's tiles of this run.
-__device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c, int n) {
-    c.u += n;
+// Units and tiles of the cursor's part of its segment.
+__device__ __forceinline__ int part_units(const Cursor& c, int pad) {
+    return min(c.end - c.u, (pad == 1 ? c.tiles : padded(c.tiles, pad)) - c.tile);
+}
+__device__ __forceinline__ int part_tiles(const Cursor& c) { return min(c.end - c.u, c.tiles - c.tile); }
+
+// To the next segment of the run; at its end, to a place without tiles.
+__device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c, int pad) {
+    c.u += part_units(c, pad);
     c.tile = 0;
     if (c.u >= c.end) return;
     if (++c.hr == p.hkv * p.rblocks) {
         c.hr = 0;
         do {
-            ++c.b;
-            c.tiles = tiles_of(p, c.b);
-        } while (c.tiles == 0);
+            c.len = length_of(p, ++c.b);
+        } while (c.len == 0);
+        c.tiles = tiles_in(c.len);
     }
 }
 
+// A tile of 32 tokens in shared memory: key codes, value codes, key scales,
+// value scales. Rows of value codes are placed so that the four rows two
+// apart that a warp reads at once (values of tokens 2t, t = 0 .. 3) lie in
+// different banks: rows in natural order would put all of them into the same.
+template <int D>
+struct Tile {
+    static constexpr int kCodes = kTile * D / 2, kScales = kTile * D / 16;
+    static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales;
+    static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+    // Place of 16-byte piece c of value row r.
+    static __device__ __forceinline__ int v_at(int r, int c) {
+        if constexpr (D == 128) {
+            const int line = r >> 1;
+            return line * 128 + (((r & 1) ^ (line & 1)) * 64) + ((c ^ (line & 2)) * 16);
+        } else {
+            const int line = r >> 2;
+            return line * 128 + (((r & 3) ^ (line & 1)) * 32) + c * 16;
+        }
+    }
+};
+
 template <int D, int NR>
 struct FwdSmem {
+    static constexpr int kWarps = Shape<NR>::kWarps;
     static constexpr int kRows = 8 * NR;
+    static constexpr int kStages = NR == 1 ? 2 : 3;
     static constexpr int kStride = D + 4;    // floats a row of the merge buffer
+    alignas(16) uint8_t ring[kWarps][kStages][Tile<D>::kBytes];
+    float o[kWarps][8 * kStride];            // eight rows of every warp's result; the join's weights
+    uint4 raw[kRows][D / 8 + 1];             // the next segment's rows of q, as they are; padded against bank conflicts
     uint2 q[D / 16][NR][32];                 // B fragments of q
     float c[kRows];                          // log2(e) * scale * descale, with q's power of two taken out
-    float o[kWarps][kRows * kStride];
+    int off[kRows];                          // keys at the sequence's end that the row may not see
     float ml[kWarps][kRows][2];
-    long long scan[kFwdThreads / 32 + 4];
+    float row_ml[kRows][2];
+    int scan[2 * kWarps + 3];
+    int last;
 };
+
+// Queues the copy of a segment's rows of q (rows that do not exist: zeros).
+template <int D, int NR>
+__device__ __forceinline__ void load_q(const FwdParams& p, FwdSmem<D, NR>& sm, int b, int hr) {
+    const int h = hr / p.rblocks, r0 = (hr - h * p.rblocks) * 8 * NR;
+    const uint8_t* src = static_cast<const uint8_t*>(p.q) + ((static_cast<long long>(b) * p.hkv + h) * p.rows + r0) * (2 * D);
+    for (int i = threadIdx.x; i < 8 * NR * (D / 8); i += Shape<NR>::kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        if (r0 + r < p.rows) copy16(ptx::smem_addr(&sm.raw[r][c]), src + r * (2 * D) + c * 16);
+        else sm.raw[r][c] = make_uint4(0, 0, 0, 0);
+    }
+}
 
 // Rows of q as B fragments of Q^T (k = d, n = row), in fp16. A bf16 row is
 // scaled by the power of two that brings its largest magnitude into
@@ -485,48 +611,61 @@ struct FwdSmem {
 // [t D/4, (t + 1) D/4): the order of d inside a product is free, and this one
 // lets a thread read a key's codes as one piece.
 template <int D, int NR, bool kBf16>
-__device__ __forceinline__ void stage_q(const FwdParams& p, FwdSmem<D, NR>& sm, int b, int hr) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int h = hr / p.rblocks, rb = hr - h * p.rblocks;
-    const float c0 = p.scale_log2 * p.k_descale[h];
-    for (int nr = warp; nr < NR; nr += kWarps) {
-        const int r = (rb * NR + nr) * 8 + g;
-        uint32_t w[D / 8];
-        if (r < p.rows) {
-            const uint16_t* src = static_cast<const uint16_t*>(p.q) +
-                                  ((static_cast<long long>(b) * p.hkv + h) * p.rows + r) * D + t * (D / 4);
+__device__ __forceinline__ void stage_q(const FwdParams& p, FwdSmem<D, NR>& sm, int hr, float k_descale) {
+    const int nr = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (nr >= NR) return;
+    uint32_t w[D / 8];
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                const uint4 v = reinterpret_cast<const uint4*>(src)[j];
-                w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
-            }
-        } else {
+    for (int j = 0; j < D / 32; ++j) {
+        const uint4 v = sm.raw[nr * 8 + g][t * (D / 32) + j];
+        w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+    }
+    float c = p.scale_log2 * k_descale;
+    if constexpr (kBf16) {
+        uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) w[j] = 0;
+        for (int j = 0; j < D / 8; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(~0u, top, 1));
+        top = max(top, __shfl_xor_sync(~0u, top, 2));
+        const int e = static_cast<int>(top >> 7);   // biased exponent of the largest magnitude
+        const int k = e == 255 ? 0 : min(14 + 127 - e, 126);
+        const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+        c *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+            float lo, hi;
+            ptx::unpack2<true>(w[j], lo, hi);
+            w[j] = ptx::pack2<false>(lo * f, hi * f);
         }
-        float c = c0;
-        if constexpr (kBf16) {
-            uint32_t top = 0;
+    }
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const int e = static_cast<int>(top >> 7);   // biased exponent of the largest magnitude
-            const int k = e == 255 ? 0 : min(14 + 127 - e, 126);
-            const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-            c *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-                float lo, hi;
-                ptx::unpack2<true>(w[j], lo, hi);
-                w[j] = ptx::pack2<false>(lo * f, hi * f);
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) sm.q[s][nr][lane] = make_uint2(w[2 * s], w[2 * s + 1]);
-        if (t == 0) sm.c[nr * 8 + g] = c;
+    for (int s = 0; s < D / 16; ++s) sm.q[s][nr][lane] = make_uint2(w[2 * s], w[2 * s + 1]);
+    if (t == 0) {
+        const int row = hr % p.rblocks * 8 * NR + nr * 8 + g;
+        sm.c[nr * 8 + g] = c;
+        sm.off[nr * 8 + g] = p.causal && row < p.rows ? p.nq - 1 - row % p.nq : 0;
     }
 }
+
+// Where a thread (g, t) finds its pieces of a tile: byte offsets of keys g,
+// values 2t and 2t + 1 and their scales, each with those of the other tokens
+// a fixed distance away; and the addresses of its q fragments and row factors.
+template <int D>
+struct Lane {
+    uint32_t k, ks, v[2], vs, q, c;
+    template <int NR>
+    __device__ __forceinline__ void set(const FwdSmem<D, NR>& sm) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        k = g * (D / 2) + t * (D / 8);
+        ks = Tile<D>::kKs + g * (D / 16) + t * (D / 64);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            v[x] = Tile<D>::kV + Tile<D>::v_at(2 * t + x, g * (D / 16) / 16) + g * (D / 16) % 16;
+        vs = Tile<D>::kVs + 2 * t * (D / 16) + (D == 128 ? g : g / 2);
+        q = ptx::smem_addr(&sm.q[0][0][lane]);
+        c = ptx::smem_addr(&sm.c[2 * t]);
+    }
+};
 
 // What a warp carries along a segment: unnormalised O^T as accumulators
 // (thread (g, t): d in [g D/8, (g + 1) D/8), rows 2t and 2t + 1 of each eight)
@@ -534,59 +673,42 @@ __device__ __forceinline__ void stage_q(const FwdParams& p, FwdSmem<D, NR>& sm, 
 template <int D, int NR>
 struct Acc {
     float o[NR][D / 16][4];
-    float m[NR][2];        // running maximum of the raw scores, -inf before the first
-    float thr[NR][2];      // a score above this moves the reference
-    float ref[NR][2];      // exponentials are 2^(s c - ref)
+    float ref[NR][2];      // exponentials are 2^(s c - ref); -inf before the first score
     float l[NR][2];        // this thread's part of the row sums
-    float c[NR][2];
-    int lim[NR][2];        // first key the row may not see
 };
 
-// Exponentials reach 2^15 at most (fp16 holds 65504): 2^7 at the running
-// maximum, and scores may pass that by 2^8 before the reference moves, which
+// Exponentials reach 2^15 at most (fp16 holds 65504): 2^7 at the maximum that
+// set the reference, and scores may pass that by 2^8 before it moves, which
 // spares most tiles the exchange of maxima and the rescaling.
-constexpr float kLift = 7.0f, kSlack = 8.0f;
+constexpr float kLift = 7.0f, kTop = 15.0f;
 
-// 32 tokens from `tok0`: kc[u], ks[u], vc[u], vs[u] point at the codes and
-// scales of the 16 tokens of half u. `kMask`: some row may not see all of
-// them, or half u is past the sequence or on a bad page (n_ok[u] < 16 tokens
-// of it are usable).
-//
-// Token order inside a half: position kk of a product is token (kk >> 1) +
-// 4 (kk & 1) + (kk & 8), so a warp reads four neighbouring tokens at once.
+// One tile of 32 tokens from `tok0`, in shared memory at `tile`. kMask: some
+// row may not see all of them, or a half's tokens are not all usable (it ends
+// behind the sequence or lies on a bad page): n_ok[u] of its 16 are.
 template <int D, int NR, bool kMask>
-__device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR][32], const uint8_t* const (&kc)[2],
-                                          const uint8_t* const (&ks)[2], const uint8_t* const (&vc)[2],
-                                          const uint8_t* const (&vs)[2], int tok0, const int (&n_ok)[2]) {
+__device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const FwdSmem<D, NR>& sm, const Lane<D>& ln, uint32_t tile,
+                                          int tok0, int len, const int (&n_ok)[2]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int tg = (g >> 1) + 4 * (g & 1);
     float s[NR][2][4];
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nr][u][e] = 0.0f;
 
     // S^T = K Q^T
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        uint32_t w[2][D / 32];   // codes of tokens tg and 8 + tg, elements [t D/4, (t+1) D/4)
+        uint32_t w[2][D / 32];   // codes of tokens g and 8 + g, elements [t D/4, (t+1) D/4)
         uint32_t sc[2][2];       // their scales, twice each
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const uint8_t* src = kc[u] + (tg + 8 * x) * (D / 2) + t * (D / 8);
-            const uint8_t* ss = ks[u] + (tg + 8 * x) * (D / 16) + t * (D / 64);
+            const uint32_t at = tile + ln.k + (16 * u + 8 * x) * (D / 2), sat = tile + ln.ks + (16 * u + 8 * x) * (D / 16);
             if constexpr (D == 128) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src);
+                const uint4 v = lds128(at);
                 w[x][0] = v.x; w[x][1] = v.y; w[x][2] = v.z; w[x][3] = v.w;
-                const uint32_t two = e4m3_to_f16(*reinterpret_cast<const uint16_t*>(ss));
+                const uint32_t two = e4m3_to_f16(lds16(sat));
                 sc[x][0] = __byte_perm(two, 0, 0x1010);
                 sc[x][1] = __byte_perm(two, 0, 0x3232);
             } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                const uint2 v = lds64(at);
                 w[x][0] = v.x; w[x][1] = v.y;
-                sc[x][0] = sc[x][1] = e4m3_to_f16(*ss * 0x0101u);
+                sc[x][0] = sc[x][1] = e4m3_to_f16(__byte_perm(lds8(sat), 0, 0x4400));
             }
         }
 #pragma unroll
@@ -602,35 +724,38 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
-                    const uint2 q = qs[2 * i + y][nr][lane];
-                    mma_f16(s[nr][u], a[0][2 * y], a[1][2 * y], a[0][2 * y + 1], a[1][2 * y + 1], q.x, q.y);
+                    const uint2 q = lds64(ln.q + ((2 * i + y) * NR + nr) * 256);
+                    if (i == 0 && y == 0)
+                        mma_f16_first(s[nr][u], a[0][0], a[1][0], a[0][1], a[1][1], q.x, q.y);
+                    else
+                        mma_f16(s[nr][u], a[0][2 * y], a[1][2 * y], a[0][2 * y + 1], a[1][2 * y + 1], q.x, q.y);
                 }
         }
     }
 
-    if constexpr (kMask) {
+    // Exponents; the reference moves only when some score passes it by too much.
+    float c[NR][2];
+    bool hide[NR][2][4];
+    float top = -INFINITY;
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+    for (int nr = 0; nr < NR; ++nr) {
+        const uint2 two = lds64(ln.c + nr * 32);
+        c[nr][0] = __uint_as_float(two.x);
+        c[nr][1] = __uint_as_float(two.y);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = tg + 4 * (e & 2);
-                    if (j >= n_ok[u] || tok0 + 16 * u + j >= acc.lim[nr][e & 1]) s[nr][u][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kMask) {
+                    const int j = g + 4 * (e & 2);
+                    hide[nr][u][e] = j >= n_ok[u] || tok0 + 16 * u + j >= len - sm.off[nr * 8 + 2 * t + (e & 1)];
+                    if (hide[nr][u][e]) s[nr][u][e] = -INFINITY;
                 }
+                const float x = fmaf(s[nr][u][e], c[nr][e & 1], -acc.ref[nr][e & 1]);
+                if (!kMask || !hide[nr][u][e]) top = fmaxf(top, x);
+            }
     }
-
-    // Running maximum: exchanged and moved only when some score passes its
-    // row's threshold.
-    bool up = false;
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float mx = fmaxf(fmaxf(s[nr][0][r], s[nr][0][r + 2]), fmaxf(s[nr][1][r], s[nr][1][r + 2]));
-            up = up || mx > acc.thr[nr][r];
-        }
-    if (__any_sync(~0u, up)) {
+    if (__any_sync(~0u, top > kTop)) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             float alpha[2];
@@ -640,12 +765,10 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-                mx = fmaxf(mx, acc.m[nr][r]);
-                const float ref = mx == -INFINITY ? 0.0f : mx * acc.c[nr][r] - kLift;
+                const float old = acc.ref[nr][r];
+                const float ref = mx == -INFINITY ? old : fmaxf(old, fmaf(mx, c[nr][r], -kLift));
                 // before a row's first score o and l are 0 and have no reference
-                alpha[r] = acc.m[nr][r] == -INFINITY ? 1.0f : ptx::ex2_approx(acc.ref[nr][r] - ref);
-                acc.m[nr][r] = mx;
-                acc.thr[nr][r] = mx == -INFINITY ? -INFINITY : mx + kSlack / acc.c[nr][r];
+                alpha[r] = old == -INFINITY ? 1.0f : ptx::ex2_approx(old - ref);
                 acc.ref[nr][r] = ref;
                 acc.l[nr][r] *= alpha[r];
             }
@@ -664,8 +787,8 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
             float pr[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                pr[e] = ptx::ex2_approx(fmaf(s[nr][u][e], acc.c[nr][e & 1], -acc.ref[nr][e & 1]));
-                if (kMask && s[nr][u][e] == -INFINITY) pr[e] = 0.0f;
+                pr[e] = ptx::ex2_approx(fmaf(s[nr][u][e], c[nr][e & 1], -acc.ref[nr][e & 1]));
+                if (kMask && hide[nr][u][e]) pr[e] = 0.0f;
                 acc.l[nr][e & 1] += pr[e];
             }
             pb[nr][u][0] = transpose8(ptx::pack2<false>(pr[0], pr[1]));
@@ -675,18 +798,18 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
     // O^T += V^T P^T
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        uint32_t w[4][D / 64];   // codes of tokens t, 4 + t, 8 + t, 12 + t, elements [g D/8, (g+1) D/8)
+        uint32_t w[4][D / 64];   // codes of tokens 2t, 2t + 1, 2t + 8, 2t + 9, elements [g D/8, (g+1) D/8)
         uint32_t sb[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const uint8_t* src = vc[u] + (t + 4 * x) * (D / 2) + g * (D / 16);
+            const uint32_t at = tile + ln.v[x & 1] + (16 * u + 8 * (x >> 1)) * (D / 2);
             if constexpr (D == 128) {
-                const uint2 v = *reinterpret_cast<const uint2*>(src);
+                const uint2 v = lds64(at);
                 w[x][0] = v.x; w[x][1] = v.y;
             } else {
-                w[x][0] = *reinterpret_cast<const uint32_t*>(src);
+                w[x][0] = lds32(at);
             }
-            sb[x] = vs[u][(t + 4 * x) * (D / 16) + (D == 128 ? g : g / 2)];
+            sb[x] = lds8(tile + ln.vs + (16 * u + 8 * (x >> 1) + (x & 1)) * (D / 16));
         }
         if constexpr (kMask) {
             // Whatever lies behind the sequence must not enter the product,
@@ -695,9 +818,10 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
             uint32_t nan = 0;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                if (t + 4 * x >= n_ok[u]) sb[x] = 0;
+                const int j = 8 * (x >> 1) + 2 * t + (x & 1);
+                if (j >= n_ok[u]) sb[x] = 0;
                 if ((sb[x] & 0x7F) == 0x7F) {
-                    nan |= 1u << (t + 4 * x);
+                    nan |= 1u << j;
                     sb[x] = 0;
                 }
             }
@@ -711,10 +835,10 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
                     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (first < acc.lim[nr][e & 1]) acc.o[nr][i][e] = NAN;
+                            if (first < len - sm.off[nr * 8 + 2 * t + (e & 1)]) acc.o[nr][i][e] = NAN;
             }
         }
-        const uint32_t s01 = e4m3_to_f16(sb[0] | sb[1] << 8), s23 = e4m3_to_f16(sb[2] | sb[3] << 8);
+        const uint32_t s01 = e4m3_to_f16(__byte_perm(sb[0], sb[1], 0x5540)), s23 = e4m3_to_f16(__byte_perm(sb[2], sb[3], 0x5540));
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
             // Pairs of tokens side by side: even elements, then odd ones.
@@ -735,192 +859,322 @@ __device__ __forceinline__ void tile_step(Acc<D, NR>& acc, const uint2 (*qs)[NR]
     }
 }
 
-// Writes a row's result: o / l * descale and the natural-log sum.
+// Writes four elements of a row's result, o / l * descale, and the
+// natural-log sum.
 template <int D, bool kBf16>
-__device__ __forceinline__ void store_row8(const FwdParams& p, long long row, int d0, const float (&o)[8], float m,
-                                           float l, float v_descale) {
-    const float f = l == 0.0f ? 0.0f : v_descale / l;
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = l == 0.0f ? 0u : ptx::pack2<kBf16>(o[2 * j] * f, o[2 * j + 1] * f);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + d0) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (d0 == 0)
-        p.lse[row] = l == 0.0f ? -INFINITY
-                               : static_cast<float>((static_cast<double>(m) + static_cast<double>(log2f(l))) * 0.69314718055994530942);
+__device__ __forceinline__ void store_row4(const FwdParams& p, long long row, int d0, const float4& o, float m, float l,
+                                           float v_descale) {
+    const float f = v_descale / l;
+    uint2 w = make_uint2(0, 0);
+    if (l != 0.0f) w = make_uint2(ptx::pack2<kBf16>(o.x * f, o.y * f), ptx::pack2<kBf16>(o.z * f, o.w * f));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + d0) = w;
+    if (d0 == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int D, int NR, bool kBf16>
-__global__ void __launch_bounds__(kFwdThreads, NR == 1 ? 4 : 2) fa2_kv4_fwd_kernel(const FwdParams p) {
-    extern __shared__ __align__(16) uint8_t raw[];
-    FwdSmem<D, NR>& sm = *reinterpret_cast<FwdSmem<D, NR>*>(raw);
-    constexpr int kRows = 8 * NR;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+__device__ __forceinline__ void axpy4(float4& y, float a, const float4& x) {
+    y.x = fmaf(a, x.x, y.x);
+    y.y = fmaf(a, x.y, y.y);
+    y.z = fmaf(a, x.z, y.z);
+    y.w = fmaf(a, x.w, y.w);
+}
 
-    // Requests without a key: O = 0, LSE = -inf.
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (p.seq_lens[b] <= 0) {
-            const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
-            const float none[8] = {};
-            for (int i = tid; i < p.hkv * p.rows * (D / 8); i += kFwdThreads)
-                store_row8<D, kBf16>(p, r0 + i / (D / 8), i % (D / 8) * 8, none, 0.0f, 0.0f, 0.0f);
-        } else if (p.seq_lens[b] > p.max_tokens && tid == 0) {
-            report(kSiteLength);
+// A warp's tiles of a segment, loaded ahead of the computation into its own
+// ring; the first of the next segment are on their way while the results of
+// one are joined. Page ids are read one tile ahead of the copies that need
+// them. A copy's lanes take neighbouring 16-byte pieces; the addresses of a
+// half's 16 tokens differ by constants.
+template <int D, int W>
+struct Loader {
+    const uint8_t* codes;      // cache + the head's offset inside a page + the lane's piece of its codes
+    const uint8_t* scales;     // the same for the piece of scales that the lane copies
+    const int* table;          // the request's row
+    uint32_t k_dst, v_dst, s_dst;   // places of the lane's pieces in a tile
+    int tile, end, len;        // the warp's next tile, end of the part, the request's tokens
+    int pg[2];                 // pages of its halves
+
+    static constexpr int kEach = Tile<D>::kScales / 16;   // pieces of a tile's key scales
+
+    __device__ __forceinline__ void start() {
+        const int lane = threadIdx.x & 31;
+        constexpr int kPieces = D / 32;   // of a token's codes
+        k_dst = lane * 16;
+        v_dst = Tile<D>::kV + Tile<D>::v_at(lane / kPieces, lane % kPieces);
+        s_dst = Tile<D>::kKs + lane * 16;
+    }
+
+    __device__ __forceinline__ void enter(const FwdParams& p, const Cursor& c) {
+        const int lane = threadIdx.x & 31;
+        codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
+        scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;
+        codes += lane * 16;
+        table = p.block_table + static_cast<long long>(c.b) * p.max_pages;
+        len = c.len;
+        tile = c.tile + (threadIdx.x >> 5);
+        end = c.tile + part_tiles(c);
+        look(p);
+    }
+
+    __device__ __forceinline__ void look(const FwdParams& p) {
+        if (tile < end) {
+            const int at = tile * kTile;
+            pg[0] = table[at >> p.log2_page];
+            if (p.page < kTile) pg[1] = at + 16 < len ? table[(at + 16) >> p.log2_page] : -1;
         }
+    }
 
-    long long per, total;
-    Cursor cur;
-    if (!locate(p, false, sm.scan, per, total, cur)) return;
-
-    while (cur.u < cur.end) {
-        const int n = static_cast<int>(min(cur.end - cur.u, static_cast<long long>(cur.tiles - cur.tile)));
-        const int h = cur.hr / p.rblocks, rb = cur.hr - h * p.rblocks;
-        const int len = min(p.seq_lens[cur.b], p.max_tokens);
-        stage_q<D, NR, kBf16>(p, sm, cur.b, cur.hr);
-        __syncthreads();
-
-        Acc<D, NR> acc;
-        int low = len;   // the first key that some row may not see
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc.o[nr][i][e] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                acc.m[nr][r] = acc.thr[nr][r] = -INFINITY;
-                acc.ref[nr][r] = acc.l[nr][r] = 0.0f;
-                acc.c[nr][r] = sm.c[nr * 8 + 2 * t + r];
-                const int row = rb * kRows + nr * 8 + 2 * t + r;
-                acc.lim[nr][r] = p.causal && row < p.rows ? len - p.nq + row % p.nq + 1 : len;
-                low = min(low, acc.lim[nr][r]);
+    // Queues the copies of the next tile (none behind the last) and closes
+    // the group. Returns one bit a half whose page can be used; the others
+    // take some page's bytes, which nobody uses. With pages of 32 tokens or
+    // more both halves lie in one page.
+    __device__ __forceinline__ int issue(const FwdParams& p, uint32_t dst) {
+        int ok = 0;
+        if (tile < end) {
+            constexpr int kHalf = 16 * (D / 2), kIts = kHalf / 512;   // bytes of a half's codes, copies for them
+            const int lane = threadIdx.x & 31;
+            const int at = (tile * kTile) & (p.page - 1);
+            const bool ok0 = static_cast<unsigned>(pg[0]) < static_cast<unsigned>(p.num_pages);
+            const long long page0 = static_cast<long long>(ok0 ? pg[0] : 0) * p.page_bytes;
+            const uint8_t* from = codes + page0 + at * (D / 2);
+            const uint8_t* from_v = from + p.part;
+            const uint8_t* from_s = scales + page0 + at * (D / 16);
+            ok = ok0 ? 3 : 0;
+            long long more = 0;   // from where the second half would follow the first to where it is
+            if (p.page < kTile) {
+                const bool ok1 = static_cast<unsigned>(pg[1]) < static_cast<unsigned>(p.num_pages);
+                ok = (ok0 ? 1 : 0) | (ok1 ? 2 : 0);
+                more = static_cast<long long>(ok1 ? pg[1] : 0) * p.page_bytes - page0;
+                if (lane % kEach >= kEach / 2) from_s += more - kHalf / 8;
+                more -= kHalf;
+                if (!ok1 && tile * kTile + 16 < len) report(kSitePage);
             }
-        }
-        low = __reduce_min_sync(~0u, low);
-
-        const int* table = p.block_table + static_cast<long long>(cur.b) * p.max_pages;
-        for (int i = warp; i < n; i += kWarps) {
-            const int tok0 = (cur.tile + i) * kTile;
-            const uint8_t *kc[2], *ks[2], *vc[2], *vs[2];
-            int n_ok[2];
-            bool whole = tok0 + kTile <= low;
+            if (!ok0) report(kSitePage);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int tok = tok0 + 16 * u;
-                int pg = -1;
-                n_ok[u] = min(16, len - tok);
-                if (n_ok[u] > 0) {
-                    pg = table[tok >> p.log2_page];
-                    if (pg < 0 || pg >= p.num_pages) {
-                        report(kSitePage);
-                        pg = -1;
-                    }
+#pragma unroll
+                for (int it = 0; it < kIts; ++it) {
+                    copy16(dst + k_dst + u * kHalf + it * 512, from + u * kHalf + it * 512);
+                    copy16(dst + v_dst + u * kHalf + it * 512, from_v + u * kHalf + it * 512);
                 }
-                if (pg < 0) {   // read some page's bytes instead, and use none of them
-                    n_ok[u] = 0;
-                    whole = false;
-                    pg = 0;
-                }
-                const int at = tok & (p.page - 1);
-                kc[u] = p.cache + (static_cast<long long>(pg) * p.hkv + h) * 2 * part_bytes<D>(p.page) + at * (D / 2);
-                ks[u] = kc[u] - at * (D / 2) + p.page * (D / 2) + at * (D / 16);
-                vc[u] = kc[u] + part_bytes<D>(p.page);
-                vs[u] = ks[u] + part_bytes<D>(p.page);
+                from += more;
+                from_v += more;
             }
-            if (whole) tile_step<D, NR, false>(acc, sm.q, kc, ks, vc, vs, tok0, n_ok);
-            else tile_step<D, NR, true>(acc, sm.q, kc, ks, vc, vs, tok0, n_ok);
+            if (D == 128 || lane < 2 * kEach) copy16(dst + s_dst, from_s);
+            tile += W;
+            look(p);
         }
-
-        // Join the warps' results.
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float l = acc.l[nr][r];
-                l += __shfl_xor_sync(~0u, l, 4);
-                l += __shfl_xor_sync(~0u, l, 8);
-                l += __shfl_xor_sync(~0u, l, 16);
-                const int row = nr * 8 + 2 * t + r;
-                if (g == 0) {
-                    sm.ml[warp][row][0] = l == 0.0f ? -INFINITY : isnan(acc.ref[nr][r]) ? 0.0f : acc.ref[nr][r];
-                    sm.ml[warp][row][1] = l;
-                }
-                float* dst = &sm.o[warp][row * FwdSmem<D, NR>::kStride + g * (D / 8)];
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc.o[nr][i][r], acc.o[nr][i][r + 2]);
-            }
-        __syncthreads();
-        const bool starts = cur.tile == 0, ends = cur.tile + n == cur.tiles;
-        const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
-        for (int i = tid; i < kRows * (D / 8); i += kFwdThreads) {
-            const int row = i / (D / 8), d0 = i % (D / 8) * 8;
-            float m = -INFINITY, l = 0.0f, o[8] = {};
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm.ml[w][row][0]);
-            if (m != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ptx::ex2_approx(sm.ml[w][row][0] - m);
-                    l += f * sm.ml[w][row][1];
-                    const float* src = &sm.o[w][row * FwdSmem<D, NR>::kStride + d0];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = fmaf(f, src[j], o[j]);
-                }
-            }
-            const int r = rb * kRows + row;
-            if (starts && ends) {
-                if (r < p.rows)
-                    store_row8<D, kBf16>(p, (static_cast<long long>(cur.b) * p.hkv + h) * p.rows + r, d0, o, m, l,
-                                         p.v_descale[h]);
-            } else {
-                float* dst = p.part_o + (static_cast<long long>(slot) * kRows + row) * D + d0;
-                *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
-                if (d0 == 0)
-                    *reinterpret_cast<float2*>(p.part_ml + (static_cast<long long>(slot) * kRows + row) * 2) =
-                        make_float2(m, l);
-            }
-        }
-        __syncthreads();
-        next_segment(p, cur, n);
+        copy_commit();
+        return ok;
     }
+};
+
+// The counter of a segment that several CTAs share counts those that are
+// done. It needs no clearing beforehand: a word that does not carry this
+// launch's nonce is replaced by the nonce before anyone counts on it, and the
+// last CTA leaves 0, so that a replayed launch finds none of its own.
+__device__ __forceinline__ void open_counter(unsigned long long* word, unsigned long long nonce) {
+    const unsigned long long old = *static_cast<volatile unsigned long long*>(word);
+    if ((old & ~0xFFFFULL) != nonce) atomicCAS(word, old, nonce);
+}
+__device__ __forceinline__ int count_in(unsigned long long* word) {
+    unsigned long long old;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
+    return static_cast<int>(old & 0xFFFF) + 1;
 }
 
-// Joins the partial results of the segments that several CTAs took: block c
-// does the segment that starts in CTA c's run and goes on behind its end.
 template <int D, int NR, bool kBf16>
-__global__ void __launch_bounds__(kFwdThreads) fa2_kv4_join_kernel(const FwdParams p) {
-    __shared__ long long scan[kFwdThreads / 32 + 4];
-    constexpr int kRows = 8 * NR;
-    long long per, total;
-    Cursor cur;   // at the last unit of CTA blockIdx.x's run
-    if (!locate(p, true, scan, per, total, cur)) return;
-    const long long seg0 = cur.u - cur.tile, seg1 = seg0 + cur.tiles;
-    const long long run0 = blockIdx.x * per;
-    if (seg0 < run0 || seg1 <= run0 + per) return;
-    const int c1 = static_cast<int>((seg1 - 1) / per);
-    const int h = cur.hr / p.rblocks, rb = cur.hr - h * p.rblocks;
-    for (int i = threadIdx.x; i < kRows * (D / 8); i += kFwdThreads) {
-        const int row = i / (D / 8), d0 = i % (D / 8) * 8, r = rb * kRows + row;
-        if (r >= p.rows) continue;
-        float m = -INFINITY, l = 0.0f, o[8] = {};
-        for (int c = blockIdx.x; c <= c1; ++c) {
-            const int slot = 2 * c + (c == static_cast<int>(blockIdx.x) ? 1 : 0);
-            m = fmaxf(m, p.part_ml[(static_cast<long long>(slot) * kRows + row) * 2]);
-        }
-        if (m != -INFINITY) {
-            for (int c = blockIdx.x; c <= c1; ++c) {
-                const int slot = 2 * c + (c == static_cast<int>(blockIdx.x) ? 1 : 0);
-                const float* ml = p.part_ml + (static_cast<long long>(slot) * kRows + row) * 2;
-                const float f = ptx::ex2_approx(ml[0] - m);
-                l += f * ml[1];
-                const float* src = p.part_o + (static_cast<long long>(slot) * kRows + row) * D + d0;
+__global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4_fwd_kernel(const FwdParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    using Smem = FwdSmem<D, NR>;
+    Smem& sm = *reinterpret_cast<Smem*>(smem);
+    constexpr int W = Shape<NR>::kWarps, T = Shape<NR>::kThreads;
+    constexpr int kRows = 8 * NR, kStages = Smem::kStages, kStride = Smem::kStride;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+    Cursor cur;
+    int per = 0, pad = 1;
+    if (locate<W>(p, sm.scan, cur, per, pad)) {
+        load_q<D, NR>(p, sm, cur.b, cur.hr);
+        float k_descale = p.k_descale[cur.hr / p.rblocks];
+        Loader<D, W> ld;
+        ld.start();
+        ld.enter(p, cur);
+        uint32_t oks = 0;   // two bits a stage
+        const uint32_t ring = ptx::smem_addr(sm.ring[warp]);
+        Lane<D> ln;
+        ln.set(sm);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(f, src[j], o[j]);
+        for (int st = 0; st < kStages - 1; ++st) oks |= ld.issue(p, ring + st * Tile<D>::kBytes) << (2 * st);
+        copy_wait<kStages - 2>();   // q went with the first tile
+        __syncthreads();
+        stage_q<D, NR, kBf16>(p, sm, cur.hr, k_descale);
+        __syncthreads();
+
+        int st = 0;
+        while (true) {
+            const int n = part_tiles(cur), units = part_units(cur, pad);
+            const int h = cur.hr / p.rblocks, rb = cur.hr - h * p.rblocks;
+            const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
+            const bool split = seg0 < static_cast<int>(blockIdx.x) * per || seg1 > cur.end;
+            const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
+            if (split && tid == 0) open_counter(p.arrived + c0, p.nonce);
+            const float v_descale = p.v_descale[h];
+            Cursor nxt = cur;
+            next_segment(p, nxt, pad);
+            const bool more = nxt.u < nxt.end;
+            if (more) {
+                load_q<D, NR>(p, sm, nxt.b, nxt.hr);
+                k_descale = p.k_descale[nxt.hr / p.rblocks];
             }
+
+            Acc<D, NR> acc;
+            const int low = p.causal ? cur.len - p.nq + 1 : cur.len;   // keys before it are seen by every row
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc.o[nr][i][e] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    acc.ref[nr][r] = -INFINITY;
+                    acc.l[nr][r] = 0.0f;
+                }
+            }
+
+            for (int i = warp; i < n; i += W) {
+                copy_wait<kStages - 2>();
+                __syncwarp();   // every lane's copies of this tile have landed, and all are done with the one before
+                const int into = st == 0 ? kStages - 1 : st - 1;
+                const uint32_t ok = (oks >> (2 * st)) & 3;
+                oks = (oks & ~(3u << (2 * into))) |
+                      static_cast<uint32_t>(ld.issue(p, ring + into * Tile<D>::kBytes)) << (2 * into);
+                const int tok0 = (cur.tile + i) * kTile;
+                const int n_ok[2] = {ok & 1 ? cur.len - tok0 : 0, ok & 2 ? cur.len - tok0 - 16 : 0};
+                const uint32_t tile = ring + st * Tile<D>::kBytes;
+                if (ok == 3 && tok0 + kTile <= low) tile_step<D, NR, false>(acc, sm, ln, tile, tok0, cur.len, n_ok);
+                else tile_step<D, NR, true>(acc, sm, ln, tile, tok0, cur.len, n_ok);
+                st = st + 1 == kStages ? 0 : st + 1;
+            }
+            copy_wait_all();   // the next rows of q
+            if (more) {
+                ld.enter(p, nxt);
+                oks = 0;
+                st = 0;
+#pragma unroll
+                for (int i = 0; i < kStages - 1; ++i) oks |= ld.issue(p, ring + i * Tile<D>::kBytes) << (2 * i);
+            }
+
+            // Join the warps' results, eight rows at a time.
+            const long long row0 = (static_cast<long long>(cur.b) * p.hkv + h) * p.rows + rb * kRows;
+            const int rows = min(kRows, p.rows - rb * kRows);
+            const int slot = 2 * blockIdx.x + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                if (nr > 0) __syncthreads();
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float l = acc.l[nr][r];
+                    l += __shfl_xor_sync(~0u, l, 4);
+                    l += __shfl_xor_sync(~0u, l, 8);
+                    l += __shfl_xor_sync(~0u, l, 16);
+                    const int row = 2 * t + r;
+                    if (g == 0) {
+                        sm.ml[warp][nr * 8 + row][0] = l == 0.0f ? -INFINITY : acc.ref[nr][r] == -INFINITY ? 0.0f : acc.ref[nr][r];
+                        sm.ml[warp][nr * 8 + row][1] = l;
+                    }
+                    float* dst = &sm.o[warp][row * kStride + g * (D / 8)];
+#pragma unroll
+                    for (int i = 0; i < D / 16; i += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(acc.o[nr][i][r], acc.o[nr][i][r + 2],
+                                                                              acc.o[nr][i + 1][r], acc.o[nr][i + 1][r + 2]);
+                }
+                __syncthreads();
+                for (int i = tid; i < min(8, rows - nr * 8) * (D / 4); i += T) {
+                    const int in = i / (D / 4), row = nr * 8 + in, d0 = i % (D / 4) * 4;
+                    float m = -INFINITY, l = 0.0f;
+                    float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) m = fmaxf(m, sm.ml[w][row][0]);
+                    if (m != -INFINITY) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            const float f = ptx::ex2_approx(sm.ml[w][row][0] - m);
+                            l = fmaf(f, sm.ml[w][row][1], l);
+                            axpy4(o, f, *reinterpret_cast<const float4*>(&sm.o[w][in * kStride + d0]));
+                        }
+                    }
+                    if (!split) {
+                        store_row4<D, kBf16>(p, row0 + row, d0, o, m, l, v_descale);
+                    } else {
+                        const long long at = static_cast<long long>(slot) * kRows + row;
+                        *reinterpret_cast<float4*>(p.part_o + at * D + d0) = o;
+                        if (d0 == 0) *reinterpret_cast<float2*>(p.part_ml + at * 2) = make_float2(m, l);
+                    }
+                }
+            }
+            if (more) stage_q<D, NR, kBf16>(p, sm, nxt.hr, k_descale);
+            __syncthreads();
+
+            if (split) {
+                const int parts = c1 - c0 + 1;
+                if (tid == 0) {
+                    sm.last = count_in(p.arrived + c0) == parts;
+                    if (sm.last) p.arrived[c0] = 0;
+                }
+                __syncthreads();
+                if (sm.last) {
+                    float* wt = sm.o[0];   // weights of the parts, by row
+                    for (int row = warp; row < rows; row += W) {
+                        float m = -INFINITY, l = 0.0f;
+                        for (int i = lane; i < parts; i += 32) {
+                            const long long at = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
+                            m = fmaxf(m, __ldcg(p.part_ml + at * 2));
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+                        for (int i = lane; i < parts; i += 32) {
+                            const long long at = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
+                            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml.x - m);
+                            wt[i * kRows + row] = f;
+                            l = fmaf(f, ml.y, l);
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+                        if (lane == 0) {
+                            sm.row_ml[row][0] = m;
+                            sm.row_ml[row][1] = l;
+                        }
+                    }
+                    __syncthreads();
+                    for (int i = tid; i < rows * (D / 4); i += T) {
+                        const int row = i / (D / 4), d0 = i % (D / 4) * 4;
+                        float4 o = make_float4(0, 0, 0, 0);
+                        const float* src = p.part_o + (2LL * c0 * kRows + row) * D + d0;
+                        axpy4(o, wt[row], __ldcg(reinterpret_cast<const float4*>(src + kRows * D)));
+#pragma unroll 8
+                        for (int j = 1; j < parts; ++j)
+                            axpy4(o, wt[j * kRows + row], __ldcg(reinterpret_cast<const float4*>(src + 2LL * j * kRows * D)));
+                        store_row4<D, kBf16>(p, row0 + row, d0, o, sm.row_ml[row][0], sm.row_ml[row][1], v_descale);
+                    }
+                    __syncthreads();
+                }
+            }
+            if (!more) break;
+            cur = nxt;
         }
-        store_row8<D, kBf16>(p, (static_cast<long long>(cur.b) * p.hkv + h) * p.rows + r, d0, o, m, l, p.v_descale[h]);
+    }
+
+    // Requests without a key: O = 0, LSE = -inf.
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int len = p.seq_lens[b];
+        if (len <= 0) {
+            const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
+            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += T)
+                store_row4<D, kBf16>(p, r0 + i / (D / 4), i % (D / 4) * 4, make_float4(0, 0, 0, 0), 0.0f, 0.0f, 0.0f);
+        } else if (len > p.max_tokens && tid == 0) {
+            report(kSiteLength);
+        }
     }
 }
 

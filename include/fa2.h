@@ -332,7 +332,7 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
  * Query rows hold no precision less than q's own; the softmax weights are
  * rounded to fp16 (2^-11), sums are fp32. A row of q that is not finite
  * affects no other row. A NaN in the cache affects the rows that see it.
- * B * H_q * N_q < 2^31 - 64. Two launches in stream order.
+ * B * H_q * N_q < 2^31 - 64. One launch.
  */
 fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
                        const float* k_descale, const float* v_descale, void* o, float* lse, void* workspace,
