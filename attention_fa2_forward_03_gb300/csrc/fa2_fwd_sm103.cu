@@ -628,6 +628,27 @@ fa2_status fa2_bwd_noalloc(const void* q, const void* k, const void* v, const vo
 
 namespace {
 
+// Queues one kernel that waits itself for the one before it (programmatic
+// dependent launch), in clusters of `cluster` CTAs.
+template <typename P>
+fa2_status kv4_launch_kernel(void (*kern)(P), long long grid, int threads, int smem, cudaStream_t stream, const P& p,
+                             int cluster = 1) {
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? FA2_OK : cuda_fail();
+}
+
 int log2_of(int x) {
     int n = 0;
     while ((1 << n) < x) ++n;
@@ -652,11 +673,19 @@ int kv4_nr(long long rows) {
     return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
+// The CTAs that can have work: runs have kMinRun tiles or more, and a padded
+// line has at most one run for each segment beyond those.
+long long kv4_ctas(long long B, long long hkv, long long rows, int nr, long long max_tokens, long long most) {
+    const long long segments = B * hkv * ((rows + 8 * nr - 1) / (8 * nr));
+    const long long tiles = (max_tokens + fa2::kv4::kTile - 1) / fa2::kv4::kTile;
+    if (segments >= most) return most;
+    return std::min(most, segments * (tiles / fa2::kv4::kMinRun + 1));
+}
+
 // Workspace: two partial results a CTA, then a counter a CTA.
-int64_t kv4_part_floats(int nr, int d) { return 2LL * fa2::kv4::kMaxCtas * 8 * nr * (d + 2); }
-int64_t kv4_workspace(long long rows, int d) {
-    return kv4_part_floats(kv4_nr(rows), d) * static_cast<int64_t>(sizeof(float)) +
-           fa2::kv4::kMaxCtas * static_cast<int64_t>(sizeof(unsigned long long));
+int64_t kv4_workspace(long long ctas, int nr, int d) {
+    return ctas * (2LL * 8 * nr * (d + 2) * static_cast<int64_t>(sizeof(float)) +
+                   static_cast<int64_t>(sizeof(unsigned long long)));
 }
 
 // A number that no other launch of this process has, and that memory left
@@ -681,15 +710,16 @@ fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
     const fa2_status st = set_smem(dev, slot, kern, kSmem);
     if (st != FA2_OK) return st;
     p.rblocks = (p.rows + 8 * NR - 1) / (8 * NR);
-    p.ctas = std::min(sm_count(dev) * Shape::kCtas, fa2::kv4::kMaxCtas);
     // units of the line are 32-bit, and padding can double them
     if (static_cast<long long>(p.B) * p.hkv * p.rblocks * ((p.max_tokens + fa2::kv4::kTile - 1LL) / fa2::kv4::kTile) >
         (1LL << 30))
         return FA2_ERR_UNSUPPORTED;
-    p.part_ml = p.part_o + 2LL * fa2::kv4::kMaxCtas * 8 * NR * D;
-    p.arrived = reinterpret_cast<unsigned long long*>(p.part_o + kv4_part_floats(NR, D));
+    p.ctas = static_cast<int>(kv4_ctas(p.B, p.hkv, p.rows, NR, p.max_tokens,
+                                       std::min(sm_count(dev) * Shape::kCtas, fa2::kv4::kMaxCtas)));
+    p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
+    p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * 8 * NR * 2);
     p.nonce = kv4_nonce();
-    return launch_kernel(kern, dim3(static_cast<unsigned>(p.ctas)), Shape::kThreads, kSmem, stream, p);
+    return kv4_launch_kernel(kern, p.ctas, Shape::kThreads, kSmem, stream, p);
 }
 
 template <int D, bool kBf16>
@@ -736,11 +766,10 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
-    st = launch_kernel(fa2::kv4::fa2_kv4_plan_kernel, dim3(1), fa2::kv4::kPlanThreads, 0, stream, p);
-    if (st != FA2_OK) return st;
-    const long long n = static_cast<long long>(B) * N;
-    return launch_kernel(fa2::kv4::fa2_kv4_slots_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, stream,
-                         p);
+    // One block where it has at most eight slots a thread to write, a cluster otherwise.
+    const bool many = static_cast<long long>(B) * N > 8 * fa2::kv4::kPlanThreads;
+    return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel, many ? fa2::kv4::kPlanCtas : 1, fa2::kv4::kPlanThreads, 0,
+                             stream, p, many ? fa2::kv4::kPlanCtas : 1);
 }
 
 fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, void* cache,
@@ -758,6 +787,8 @@ fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, vo
     fa2_status st = kv4_check_pages(page_size, num_pages, 1);
     if (st != FA2_OK) return st;
     if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    for (int64_t s : {k_stride_b, k_stride_h, k_stride_n, v_stride_b, v_stride_h, v_stride_n})
+        if (s > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
     const long long rows = static_cast<long long>(B) * H_kv;
     if (rows > 0x7FFFFFFFLL / N) return FA2_ERR_UNSUPPORTED;
     int dev = 0;
@@ -765,12 +796,12 @@ fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, vo
     fa2::kv4::AppendParams p{};
     p.x[0] = k;
     p.x[1] = v;
-    p.sb[0] = k_stride_b;
-    p.sh[0] = k_stride_h;
-    p.sn[0] = k_stride_n;
-    p.sb[1] = v_stride_b;
-    p.sh[1] = v_stride_h;
-    p.sn[1] = v_stride_n;
+    p.sb[0] = static_cast<int>(k_stride_b);
+    p.sh[0] = static_cast<int>(k_stride_h);
+    p.sn[0] = static_cast<int>(k_stride_n);
+    p.sb[1] = static_cast<int>(v_stride_b);
+    p.sh[1] = static_cast<int>(v_stride_h);
+    p.sn[1] = static_cast<int>(v_stride_n);
     p.descale[0] = k_descale;
     p.descale[1] = v_descale;
     p.slots = slots;
@@ -781,14 +812,15 @@ fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, vo
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_slots = num_pages * page_size;
-    const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.rows) * (d / 16) + 255) / 256));
+    const int rows_block = d == 128 ? fa2::kv4::Copy<128>::kRows : fa2::kv4::Copy<64>::kRows;
+    const long long grid = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
     const bool bf = dtype == FA2_BF16;
     using namespace fa2::kv4;
     if (d == 128)
-        return bf ? launch_kernel(fa2_kv4_append_kernel<128, true>, grid, 256, 0, stream, p)
-                  : launch_kernel(fa2_kv4_append_kernel<128, false>, grid, 256, 0, stream, p);
-    return bf ? launch_kernel(fa2_kv4_append_kernel<64, true>, grid, 256, 0, stream, p)
-              : launch_kernel(fa2_kv4_append_kernel<64, false>, grid, 256, 0, stream, p);
+        return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<128, true>, grid, 256, 0, stream, p)
+                  : kv4_launch_kernel(fa2_kv4_append_kernel<128, false>, grid, 256, 0, stream, p);
+    return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<64, true>, grid, 256, 0, stream, p)
+              : kv4_launch_kernel(fa2_kv4_append_kernel<64, false>, grid, 256, 0, stream, p);
 }
 
 fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -825,19 +857,24 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
     p.log2_page = log2_of(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;
-    const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.rows) * (d / 16) + 255) / 256));
+    const int rows_block = d == 128 ? fa2::kv4::Copy<128>::kRows : fa2::kv4::Copy<64>::kRows;
+    const long long grid = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
     const bool bf = dtype == FA2_BF16;
     using namespace fa2::kv4;
     if (d == 128)
-        return bf ? launch_kernel(fa2_kv4_gather_kernel<128, true>, grid, 256, 0, stream, p)
-                  : launch_kernel(fa2_kv4_gather_kernel<128, false>, grid, 256, 0, stream, p);
-    return bf ? launch_kernel(fa2_kv4_gather_kernel<64, true>, grid, 256, 0, stream, p)
-              : launch_kernel(fa2_kv4_gather_kernel<64, false>, grid, 256, 0, stream, p);
+        return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<128, true>, grid, 256, 0, stream, p)
+                  : kv4_launch_kernel(fa2_kv4_gather_kernel<128, false>, grid, 256, 0, stream, p);
+    return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<64, true>, grid, 256, 0, stream, p)
+              : kv4_launch_kernel(fa2_kv4_gather_kernel<64, false>, grid, 256, 0, stream, p);
 }
 
-int64_t fa2_fwd_kv4_workspace(int H_q, int H_kv, int N_q, int d) {
-    if (H_q <= 0 || H_kv <= 0 || N_q <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128)) return -1;
-    return kv4_workspace(static_cast<long long>(H_q / H_kv) * N_q, d);
+int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size) {
+    if (B <= 0 || H_q <= 0 || H_kv <= 0 || N_q <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
+        kv4_check_pages(page_size, 1, max_pages) != FA2_OK)
+        return -1;
+    const long long rows = static_cast<long long>(H_q / H_kv) * N_q;
+    const int nr = kv4_nr(rows);
+    return kv4_workspace(kv4_ctas(B, H_kv, rows, nr, static_cast<long long>(max_pages) * page_size, fa2::kv4::kMaxCtas), nr, d);
 }
 
 fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -862,7 +899,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     const long long heads = static_cast<long long>(B) * H_q;
     if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit,
     if (H_kv > 65535 / 2) return FA2_ERR_UNSUPPORTED;                    // and a page's bytes
-    if (workspace_bytes < fa2_fwd_kv4_workspace(H_q, H_kv, N_q, d)) return FA2_ERR_INVALID_ARG;
+    if (workspace_bytes < fa2_fwd_kv4_workspace(B, H_q, H_kv, N_q, d, max_pages, page_size)) return FA2_ERR_INVALID_ARG;
     int dev = 0;
     if ((st = check_device(&dev)) != FA2_OK) return st;
     fa2::kv4::FwdParams p{};

@@ -34,6 +34,14 @@ __host__ __device__ constexpr int part_bytes(int page) {
     return page * (D / 2 + D / 16);
 }
 
+// The kernels of this file are launched so that one may take its place on the
+// SMs while the one before it in the stream still runs (programmatic
+// dependent launch). Nothing of global memory is touched before that one is
+// done and its writes can be seen.
+__device__ __forceinline__ void enter_stream_order() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ conversions
 
 // Four bytes of e2m1 pairs to four fp16 pairs (low four bits of a byte in the
@@ -79,7 +87,7 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float* x) {
 
 struct AppendParams {
     const void* x[2];          // keys, values
-    long long sb[2], sh[2], sn[2];  // strides in elements: request, head, token
+    int sb[2], sh[2], sn[2];   // strides in elements: request, head, token
     const float* descale[2];   // [hkv]
     const int* slots;          // [B, N]
     uint8_t* cache;
@@ -88,69 +96,157 @@ struct AppendParams {
     int num_slots;             // num_pages * page
 };
 
-// One thread quantises 16 elements of a key and of a value: the unit of a
-// scale, 32 bytes read and 9 written for each.
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) fa2_kv4_append_kernel(const AppendParams p) {
-    constexpr int kGroups = D / 16;
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const long long row = i / kGroups;
-    const int grp = static_cast<int>(i % kGroups);
-    if (row >= p.rows) return;
-    const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.n);
-    const unsigned n = static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.n);
-    const unsigned b = bh / static_cast<unsigned>(p.hkv), h = bh - b * static_cast<unsigned>(p.hkv);
-    const int slot = p.slots[static_cast<long long>(b) * p.n + n];
-    if (slot < 0) return;
-    if (slot >= p.num_slots) {
-        report(kSiteSlot);
-        return;
+// Eight elements a lane, so that a warp's loads and stores are contiguous:
+// 16 bytes of a row, two lanes to a scale. A thread has kPasses rows of keys
+// and of values in flight.
+template <int D>
+struct Copy {
+    static constexpr int kLanes = D / 8;             // lanes of a row
+    static constexpr int kRowsPass = 256 / kLanes;
+    static constexpr int kPasses = 4;
+    static constexpr int kRows = kRowsPass * kPasses;   // rows of a block
+};
+
+// Row (b, h, n) of [B, hkv, n], and the row `k` on.
+struct Row {
+    unsigned b, h, n;
+    __device__ __forceinline__ Row(unsigned row, unsigned hkv, unsigned len) {
+        const unsigned bh = row / len;
+        n = row - bh * len;
+        b = bh / hkv;
+        h = bh - b * hkv;
     }
-    const int pg = slot >> p.log2_page, at = slot & (p.page - 1);
-    uint4 in[2][2];
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        const uint16_t* src = static_cast<const uint16_t*>(p.x[part]) + b * p.sb[part] + h * p.sh[part] +
-                              n * p.sn[part] + grp * 16;
-        in[part][0] = reinterpret_cast<const uint4*>(src)[0];
-        in[part][1] = reinterpret_cast<const uint4*>(src)[1];
-    }
-    uint8_t* blk = p.cache + (static_cast<long long>(pg) * p.hkv + h) * 2 * part_bytes<D>(p.page);
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        float x[16];
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(in[part]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ptx::unpack2<kBf16>(w[j], x[2 * j], x[2 * j + 1]);
-        // The largest magnitude by its bits, which order NaN above infinity
-        // above every finite value.
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-        const float descale = p.descale[part][h];
-        uint32_t s8 = 0x7F;   // e4m3 NaN: a block that holds a NaN or an infinity reads back as NaN
-        uint32_t codes[2] = {0, 0};
-        if (top < 0x7F800000u) {
-            const float want = __fdiv_rn(__uint_as_float(top), 6.0f * descale);
-            asm("{\n\t.reg .b16 a;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %1, %1;\n\tcvt.u32.u16 %0, a;\n\t}"
-                : "=r"(s8)
-                : "f"(want));
-            s8 &= 0xFF;
-            float s, other;
-            ptx::unpack2<false>(e4m3_to_f16(s8), s, other);
-            const float t = __fmul_rn(s, descale);
-            if (t > 0.0f) {
-                // True quotients: a tie between two codes (common, as inputs
-                // and scales have few bits) has to be seen as one.
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __fdiv_rn(x[j], t);
-                codes[0] = pack8_e2m1(x);
-                codes[1] = pack8_e2m1(x + 8);
+    __device__ __forceinline__ void step(unsigned k, unsigned hkv, unsigned len) {
+        n += k;
+        if (n >= len) {   // most rows are followed by rows of their own sequence: divisions are rare
+            const unsigned q = n / len;
+            n -= q * len;
+            h += q;
+            if (h >= hkv) {
+                const unsigned r = h / hkv;
+                h -= r * hkv;
+                b += r;
             }
         }
-        uint8_t* dst = blk + part * part_bytes<D>(p.page);
-        *reinterpret_cast<uint2*>(dst + at * (D / 2) + grp * 8) = make_uint2(codes[0], codes[1]);
-        dst[p.page * (D / 2) + at * kGroups + grp] = static_cast<uint8_t>(s8);
+    }
+};
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Quotients rounded to nearest by Markstein's correction (IBM J. Res. Dev. 34,
+// 1990): with r the nearest to 1 / t, q the nearest to x r, and the remainder
+// x - q t, which an fma gives exactly, q + remainder * r rounds to the nearest
+// of x / t. A tie between two codes (or scales) is common, as inputs and scales
+// have few bits, and has to be seen as one. It holds where no step leaves the
+// normal numbers: `plain` says so for a divisor and the largest numerator of
+// its block, smaller ones giving codes near 0, far from a tie. The divider
+// takes the rest.
+__device__ __forceinline__ bool plain(float t, float top) {
+    return t > 1e-18f && t < 1e18f && top > 1e-18f && top < 1e18f;
+}
+__device__ __forceinline__ float quotient(float x, float t, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, t, x), r, q);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256, 4) fa2_kv4_append_kernel(const AppendParams p) {
+    enter_stream_order();
+    using C = Copy<D>;
+    const int lane = threadIdx.x % C::kLanes;
+    const long long row0 = static_cast<long long>(blockIdx.x) * C::kRows + threadIdx.x / C::kLanes;
+    uint4 in[C::kPasses][2];
+    int slot[C::kPasses];
+    unsigned head[C::kPasses];
+    long long at[C::kPasses][2];
+    Row r(static_cast<unsigned>(row0), p.hkv, p.n);
+#pragma unroll
+    for (int i = 0; i < C::kPasses; ++i) {
+        slot[i] = -1;
+        if (row0 + i * C::kRowsPass < p.rows) slot[i] = p.slots[static_cast<long long>(r.b) * p.n + r.n];
+        head[i] = r.h;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+            at[i][part] = static_cast<long long>(static_cast<int>(r.b)) * p.sb[part] +
+                          static_cast<long long>(static_cast<int>(r.h)) * p.sh[part] +
+                          static_cast<long long>(static_cast<int>(r.n)) * p.sn[part] + lane * 8;
+        r.step(C::kRowsPass, p.hkv, p.n);
+    }
+#pragma unroll
+    for (int i = 0; i < C::kPasses; ++i) {
+        if (slot[i] >= p.num_slots) {
+            if (lane == 0) report(kSiteSlot);
+            slot[i] = -1;
+        }
+        in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
+        if (slot[i] >= 0)
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+                in[i][part] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[part]) + at[i][part]);
+    }
+    float scales[2], six[2], six_r[2];   // of the head at hand: descale, 6 descale and its reciprocal
+    unsigned at_head = ~0u;
+#pragma unroll
+    for (int i = 0; i < C::kPasses; ++i) {
+        if (slot[i] >= 0 && head[i] != at_head) {
+            at_head = head[i];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                scales[part] = p.descale[part][at_head];
+                six[part] = 6.0f * scales[part];
+                six_r[part] = __frcp_rn(six[part]);
+            }
+        }
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint4 w = in[i][part];
+            // The largest magnitude by its bits, which order NaN above
+            // infinity above every finite value.
+            uint32_t pair = max_u16x2(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                      max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+            pair = max_u16x2(pair, __shfl_xor_sync(~0u, pair, 1));
+            if (slot[i] < 0) continue;
+            float lo, hi;
+            ptx::unpack2<kBf16>(pair, lo, hi);
+            const float top = __uint_as_float(max(__float_as_uint(lo), __float_as_uint(hi)));
+            const float descale = scales[part];
+            uint32_t s8 = 0x7F;   // e4m3 NaN: 16 elements that hold a NaN or an infinity read back as NaN
+            uint32_t codes = 0;
+            if (__float_as_uint(top) < 0x7F800000u) {
+                const float want = plain(six[part], top) ? quotient(top, six[part], six_r[part]) : __fdiv_rn(top, six[part]);
+                asm("{\n\t.reg .b16 a;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %1, %1;\n\tcvt.u32.u16 %0, a;\n\t}"
+                    : "=r"(s8)
+                    : "f"(want));
+                s8 &= 0xFF;
+                float s, other;
+                ptx::unpack2<false>(e4m3_to_f16(s8), s, other);
+                const float t = __fmul_rn(s, descale);
+                if (t > 0.0f) {
+                    float x[8];
+                    ptx::unpack2<kBf16>(w.x, x[0], x[1]);
+                    ptx::unpack2<kBf16>(w.y, x[2], x[3]);
+                    ptx::unpack2<kBf16>(w.z, x[4], x[5]);
+                    ptx::unpack2<kBf16>(w.w, x[6], x[7]);
+                    if (plain(t, top)) {
+                        const float r = __frcp_rn(t);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = quotient(x[j], t, r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], t);
+                    }
+                    codes = pack8_e2m1(x);
+                }
+            }
+            const int pg = slot[i] >> p.log2_page, off = slot[i] & (p.page - 1);
+            uint8_t* dst = p.cache + ((static_cast<long long>(pg) * p.hkv + head[i]) * 2 + part) * part_bytes<D>(p.page);
+            *reinterpret_cast<uint32_t*>(dst + off * (D / 2) + lane * 4) = codes;
+            if (lane % 2 == 0) dst[p.page * (D / 2) + off * (D / 16) + lane / 2] = static_cast<uint8_t>(s8);
+        }
     }
 }
 
@@ -167,54 +263,60 @@ struct GatherParams {
     int hkv, n, page, log2_page, max_pages, num_pages;
 };
 
-// One thread reads 16 elements of a key and of a value: 9 bytes read and 32
-// written for each. Rows at or past a request's length are zeros.
+// Rows at or past a request's length are zeros.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherParams p) {
-    constexpr int kGroups = D / 16;
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    const long long row = i / kGroups;
-    const int grp = static_cast<int>(i % kGroups);
-    if (row >= p.rows) return;
-    const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.n);
-    const unsigned n = static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.n);
-    const unsigned b = bh / static_cast<unsigned>(p.hkv), h = bh - b * static_cast<unsigned>(p.hkv);
-    const long long pos = static_cast<long long>(p.starts ? p.starts[b] : 0) + n;
-    const uint8_t* blk = nullptr;
-    int at = 0;
-    if (pos >= 0 && pos < p.seq_lens[b]) {
+    enter_stream_order();
+    using C = Copy<D>;
+    const int lane = threadIdx.x % C::kLanes;
+    const long long row0 = static_cast<long long>(blockIdx.x) * C::kRows + threadIdx.x / C::kLanes;
+    uint32_t codes[C::kPasses][2], scale[C::kPasses][2];
+    unsigned head[C::kPasses];
+    Row next(static_cast<unsigned>(row0), p.hkv, p.n);
+#pragma unroll
+    for (int i = 0; i < C::kPasses; ++i) {
+        const Row r = next;
+        next.step(C::kRowsPass, p.hkv, p.n);
+        codes[i][0] = codes[i][1] = scale[i][0] = scale[i][1] = 0;   // reads as zeros
+        head[i] = r.h;
+        if (row0 + i * C::kRowsPass >= p.rows) continue;
+        const long long pos = static_cast<long long>(p.starts ? p.starts[r.b] : 0) + r.n;
+        if (pos < 0 || pos >= p.seq_lens[r.b]) continue;
         const long long entry = pos >> p.log2_page;
-        const int pg = entry < p.max_pages ? p.block_table[static_cast<long long>(b) * p.max_pages + entry] : -1;
-        at = static_cast<int>(pos & (p.page - 1));
-        if (pg >= 0 && pg < p.num_pages)
-            blk = p.cache + (static_cast<long long>(pg) * p.hkv + h) * 2 * part_bytes<D>(p.page);
-        else
-            report(kSitePage);
+        const int pg = entry < p.max_pages ? p.block_table[static_cast<long long>(r.b) * p.max_pages + entry] : -1;
+        if (pg < 0 || pg >= p.num_pages) {
+            if (lane == 0) report(kSitePage);
+            continue;
+        }
+        const int at = static_cast<int>(pos & (p.page - 1));
+        const uint8_t* src = p.cache + (static_cast<long long>(pg) * p.hkv + r.h) * 2 * part_bytes<D>(p.page);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            codes[i][part] = *reinterpret_cast<const uint32_t*>(src + at * (D / 2) + lane * 4);
+            scale[i][part] = src[p.page * (D / 2) + at * (D / 16) + lane / 2];
+            src += part_bytes<D>(p.page);
+        }
     }
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-        uint32_t out[8] = {};
-        if (blk) {
-            const uint8_t* src = blk + part * part_bytes<D>(p.page);
-            const uint2 codes = *reinterpret_cast<const uint2*>(src + at * (D / 2) + grp * 8);
+    for (int i = 0; i < C::kPasses; ++i) {
+        const long long row = row0 + i * C::kRowsPass;
+        if (row >= p.rows) break;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
             float s, other;
-            ptx::unpack2<false>(e4m3_to_f16(src[p.page * (D / 2) + at * kGroups + grp]), s, other);
-            const float t = __fmul_rn(s, p.descale[part][h]);
+            ptx::unpack2<false>(e4m3_to_f16(scale[i][part]), s, other);
+            const float t = __fmul_rn(s, p.descale[part][min(head[i], static_cast<unsigned>(p.hkv) - 1)]);
+            uint32_t c[4], out[4];
+            e2m1_to_f16(codes[i][part], c);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t c[4];
-                e2m1_to_f16(j ? codes.y : codes.x, c);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float lo, hi;
-                    ptx::unpack2<false>(c[e], lo, hi);
-                    out[4 * j + e] = ptx::pack2<kBf16>(__fmul_rn(lo, t), __fmul_rn(hi, t));
-                }
+            for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                ptx::unpack2<false>(c[e], lo, hi);
+                out[e] = ptx::pack2<kBf16>(__fmul_rn(lo, t), __fmul_rn(hi, t));
             }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[part]) + row * D + lane * 8) =
+                make_uint4(out[0], out[1], out[2], out[3]);
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out[part]) + row * D + grp * 16);
-        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
 }
 
@@ -234,6 +336,7 @@ struct PlanParams {
 };
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanCtas = 8;   // of a cluster, where there is much to write
 
 // Exclusive prefix sums of (a, r) over the block's threads, and the totals.
 __device__ __forceinline__ void block_scan2(long long& a, long long& r, long long& a_all, long long& r_all,
@@ -248,114 +351,175 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& r, long lon
             ir += tr;
         }
     }
-    __syncthreads();
     if (lane == 31) {
         sm[0][warp] = ia;
         sm[1][warp] = ir;
     }
     __syncthreads();
-    long long ba = 0, br = 0;
-    a_all = r_all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w == warp) {
-            ba = a_all;
-            br = r_all;
+    // every warp scans the warps' sums for itself
+    const long long wa = sm[0][lane], wr = sm[1][lane];
+    long long sa = wa, sr = wr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long ta = __shfl_up_sync(~0u, sa, o), tr = __shfl_up_sync(~0u, sr, o);
+        if (lane >= o) {
+            sa += ta;
+            sr += tr;
         }
-        a_all += sm[0][w];
-        r_all += sm[1][w];
     }
-    a = ba + ia - a;
-    r = br + ir - r;
+    a_all = __shfl_sync(~0u, sa, 31);
+    r_all = __shfl_sync(~0u, sr, 31);
+    a = __shfl_sync(~0u, sa - wa, warp) + ia - a;
+    r = __shfl_sync(~0u, sr - wr, warp) + ir - r;
 }
 
-// Pages, lengths and the free ring, by one block: a scan over the requests in
-// order, 1024 at a time. A request gets its pages iff the pages wanted up to
-// and including it are free (or it needs none); pages of requests that end
-// join the ring behind its last page and are not handed out by this call.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// One cluster. Every CTA scans the requests in order, 1024 at a time, so that
+// each knows where every request's pages lie in the ring; behind a barrier
+// (the outputs may be the inputs) they share the writing. A request gets its
+// pages iff the pages wanted up to and including it are free (or it needs
+// none); pages of requests that end join the ring behind its last page and are
+// not handed out by this call. Bound by latency: three dependent reads.
 __global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanParams p) {
     __shared__ long long sm[2][kPlanThreads / 32];
+    __shared__ int s_len[kPlanThreads], s_add[kPlanThreads], s_page[kPlanThreads], s_back[kPlanThreads];
+    enter_stream_order();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t rank, ranks;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     int first = p.free_state[0], count = p.free_state[1];
     if (first < 0 || first >= p.num_pages || count < 0 || count > p.num_pages) {
-        if (threadIdx.x == 0) report(kSitePool);
+        if (tid == 0 && rank == 0) report(kSitePool);
         first = 0;
         count = 0;
     }
     const long long room = static_cast<long long>(p.max_pages) << p.log2_page;
-    long long want = 0, back = 0;   // pages wanted by, and returned by, the requests before this chunk
-    long long taken = 0;            // pages this thread's requests got
+    // pages wanted by the requests before this chunk, handed out to them, and returned by them
+    long long want = 0, taken = 0, back = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-        const int b = b0 + threadIdx.x;
+        const int n = min(kPlanThreads, p.B - b0), b = b0 + tid;
         int len = 0, add = 0;
-        bool in = b < p.B, ends = false, fits = false;
+        const bool in = tid < n;
         if (in) {
             len = p.seq_lens[b];
             add = p.new_lens[b];
             if (len < 0 || len > room) {
-                report(kSiteLength);
+                if (rank == 0) report(kSiteLength);
                 len = 0;
             }
-            ends = add < 0;
-            fits = !ends && add <= p.n && static_cast<long long>(len) + add <= room;
         }
+        const bool ends = in && add < 0;
+        const bool fits = in && !ends && add <= p.n && static_cast<long long>(len) + add <= room;
         const int have = (len + p.page - 1) >> p.log2_page;
-        const int need = fits ? static_cast<int>(((static_cast<long long>(len) + add + p.page - 1) >> p.log2_page) - have) : 0;
-        const int rel = in && ends ? have : 0;
-        long long a = need, r = rel, a_all, r_all;
+        const int need = fits ? static_cast<int>((static_cast<long long>(len) + add + p.page - 1) >> p.log2_page) - have : 0;
+        long long a = need, r = ends ? have : 0, a_all, r_all;
         block_scan2(a, r, a_all, r_all, sm);
         const bool granted = fits && (need == 0 || want + a + need <= count);
-        if (in) {
-            int* row = p.block_table + static_cast<long long>(b) * p.max_pages;
-            if (granted) {
-                taken += need;
-                for (int j = 0; j < need; ++j) row[have + j] = p.free_pages[(first + want + a + j) % p.num_pages];
-            }
-            for (int j = 0; j < rel; ++j) p.free_pages[(first + static_cast<long long>(count) + back + r + j) % p.num_pages] = row[j];
-            p.seq_lens_out[b] = ends ? 0 : len + (granted ? add : 0);
-            p.accepted[b] = granted ? add : 0;
+        s_len[tid] = len;
+        s_add[tid] = ends ? -1 : granted ? add : 0;
+        s_page[tid] = granted ? static_cast<int>(first + want + a) : 0;   // of its first new page in the ring; < 2 num_pages if it has one
+        s_back[tid] = static_cast<int>((first + static_cast<long long>(count) + back + r) % p.num_pages);
+        // those that got pages are the first of those that wanted any
+        taken = want + a_all <= count ? want + a_all : taken;
+        const bool cut = want <= count && want + a_all > count;
+        if (cut) {
+            long long got = granted ? need : 0, none = 0, unused;
+            __syncthreads();
+            block_scan2(got, none, taken, unused, sm);
+            taken += want;
         }
         want += a_all;
         back += r_all;
+        __syncthreads();
+        cluster_sync();
+
+        if (rank == 0 && in) {
+            p.seq_lens_out[b] = ends ? 0 : len + (granted ? add : 0);
+            p.accepted[b] = granted ? add : 0;
+        }
+        // slots, and the table entries of the pages that begin among them
+        auto slot_of = [&](int rb, int i) {
+            if (i >= s_add[rb]) return -1;
+            const int l = s_len[rb], pos = l + i, had = (l + p.page - 1) >> p.log2_page;
+            const int entry = pos >> p.log2_page;
+            int* at = p.block_table + static_cast<long long>(b0 + rb) * p.max_pages + entry;
+            int pg;
+            if (entry < had) {
+                pg = *at;
+            } else {
+                int k = s_page[rb] + entry - had;
+                if (k >= p.num_pages) k -= p.num_pages;
+                pg = p.free_pages[k];
+                if ((pos & (p.page - 1)) == 0) *at = pg;
+            }
+            if (pg >= 0 && pg < p.num_pages) return (pg << p.log2_page) + (pos & (p.page - 1));
+            report(kSitePage);
+            return -1;
+        };
+        int* slots = p.slots + static_cast<long long>(b0) * p.n;
+        if (p.n >= 256) {
+            // long rows: a warp takes 256 slots of one request, whose facts stay in registers
+            const unsigned pieces = (p.n + 255) / 256, all = n * pieces;
+            for (unsigned q = rank * (kPlanThreads / 32) + warp; q < all; q += ranks * (kPlanThreads / 32)) {
+                const int rb = q / pieces, i0 = (q - rb * pieces) * 256;
+                int* to = slots + static_cast<long long>(rb) * p.n;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = i0 + j * 32 + lane;
+                    if (i < p.n) to[i] = slot_of(rb, i);
+                }
+            }
+        } else {
+            const unsigned total = static_cast<unsigned>(n) * static_cast<unsigned>(p.n);
+            const unsigned stride = ranks * kPlanThreads, sb = stride / p.n, si = stride - sb * p.n;
+            unsigned e = rank * kPlanThreads + tid, rb = e / p.n, i = e - rb * p.n;
+            for (; e < total; e += stride) {
+                slots[e] = slot_of(rb, i);
+                rb += sb;
+                i += si;
+                if (i >= static_cast<unsigned>(p.n)) {
+                    i -= p.n;
+                    ++rb;
+                }
+            }
+        }
+        // pages of requests that end, a warp each
+        if (r_all > 0)
+            for (int q = rank * (kPlanThreads / 32) + warp; q < n; q += ranks * (kPlanThreads / 32))
+                if (s_add[q] < 0) {
+                    const int* row = p.block_table + static_cast<long long>(b0 + q) * p.max_pages;
+                    for (int j = lane; j < (s_len[q] + p.page - 1) >> p.log2_page; j += 32)
+                        p.free_pages[(static_cast<long long>(s_back[q]) + j) % p.num_pages] = row[j];
+                }
+        __syncthreads();
     }
-    long long zero = 0, all, unused;
-    block_scan2(taken, zero, all, unused, sm);
-    if (threadIdx.x == 0) {
-        long long left = count - all + back;
+    if (tid == 0 && rank == 0) {
+        long long left = count - taken + back;
         if (left > p.num_pages) {   // more pages came back than were out
             report(kSitePool);
             left = p.num_pages;
         }
-        p.free_state_out[0] = static_cast<int>((first + all) % p.num_pages);
+        p.free_state_out[0] = static_cast<int>((first + taken) % p.num_pages);
         p.free_state_out[1] = static_cast<int>(left);
     }
-}
-
-// Slots of the accepted tokens, -1 in the other places.
-__global__ void __launch_bounds__(256) fa2_kv4_slots_kernel(const PlanParams p) {
-    const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= static_cast<long long>(p.B) * p.n) return;
-    const int b = static_cast<int>(i / p.n), j = static_cast<int>(i - static_cast<long long>(b) * p.n);
-    const int add = p.accepted[b];
-    int slot = -1;
-    if (j < add) {
-        const int pos = p.seq_lens_out[b] - add + j;
-        const int pg = p.block_table[static_cast<long long>(b) * p.max_pages + (pos >> p.log2_page)];
-        if (pg >= 0 && pg < p.num_pages) slot = (pg << p.log2_page) + (pos & (p.page - 1));
-        else report(kSitePage);
-    }
-    p.slots[i] = slot;
 }
 
 // ------------------------------------------------------------------ attention
 
 constexpr int kTile = 32;      // tokens a warp takes at a time
 constexpr int kMaxCtas = 320;  // workspace is sized for this many
-constexpr int kMinRun = 16;    // tiles a CTA's run has at least
+constexpr int kMinRun = 32;    // tiles a CTA's run has at least
+constexpr int kSpare = 40;     // tiles by which a run may grow so that no segment is split
 
 // Warps a CTA and CTAs an SM by the rows a pass over the keys serves: what
 // the accumulators leave room for in the registers.
 template <int NR>
 struct Shape {
-    static constexpr int kWarps = NR == 2 || NR == 3 ? 12 : 8;
+    static constexpr int kWarps = 8;
     static constexpr int kCtas = NR == 1 ? 2 : 1;
     static constexpr int kThreads = 32 * kWarps;
 };
@@ -460,9 +624,10 @@ __device__ __forceinline__ int length_of(const FwdParams& p, int b) { return min
 __device__ __forceinline__ int tiles_in(int len) { return (len >> 5) + ((len & 31) != 0); }
 __device__ __forceinline__ int padded(int tiles, int pad) { return (tiles + pad - 1) / pad * pad; }
 
-// Exclusive prefix sum over the block's threads of `mine`, and the total.
+// Exclusive prefix sum over the block's threads of `mine`, and the total; the
+// largest `top`. `sm`: 2 W ints.
 template <int W>
-__device__ __forceinline__ int scan_units(int mine, int& total, int* sm) {
+__device__ __forceinline__ int scan_units(int mine, int& total, int& top, int* sm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int inc = mine;
 #pragma unroll
@@ -470,7 +635,11 @@ __device__ __forceinline__ int scan_units(int mine, int& total, int* sm) {
         const int t = __shfl_up_sync(~0u, inc, o);
         if (lane >= o) inc += t;
     }
-    if (lane == 31) sm[warp] = inc;
+    top = __reduce_max_sync(~0u, top);
+    if (lane == 31) {
+        sm[warp] = inc;
+        sm[W + warp] = top;
+    }
     __syncthreads();
     int before = 0;
     total = 0;
@@ -478,29 +647,37 @@ __device__ __forceinline__ int scan_units(int mine, int& total, int* sm) {
     for (int w = 0; w < W; ++w) {
         if (w == warp) before = total;
         total += sm[w];
+        top = max(top, sm[W + w]);
     }
     return before + inc - mine;
 }
 
-// The start of this CTA's run; false if it has none. `sm`: 2 W + 3 ints.
+// The start of this CTA's run; false if it has none. `sm`: 4 W + 3 ints.
 template <int W>
 __device__ __forceinline__ bool locate(const FwdParams& p, int* sm, Cursor& cur, int& per, int& pad) {
     const int tid = threadIdx.x;
     const int chunk = (p.B + 32 * W - 1) / (32 * W);
     const int b0 = min(tid * chunk, p.B), b1 = min(b0 + chunk, p.B);
     const int hrs = p.hkv * p.rblocks;
-    int mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += tiles_in(length_of(p, b));
-    int at = scan_units<W>(mine, total, sm) * hrs;
+    int mine = 0, total, longest = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int t = tiles_in(length_of(p, b));
+        mine += t;
+        longest = max(longest, t);
+    }
+    int at = scan_units<W>(mine, total, longest, sm) * hrs;
     total *= hrs;
     if (total == 0) return false;
     per = max((total + p.ctas - 1) / p.ctas, kMinRun);
     per = (per + W - 1) / W * W;
     pad = 1;
     if (p.B * hrs <= p.ctas) {
-        int mine_p = 0, total_p;
+        // Every segment could have a CTA of its own, which is worth a
+        // somewhat longer run: nothing to join, no second segment.
+        if (longest <= per + kSpare) per = max(per, (longest + W - 1) / W * W);
+        int mine_p = 0, total_p, unused = 0;
         for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in(length_of(p, b)), per);
-        const int at_p = scan_units<W>(mine_p, total_p, sm + W) * hrs;
+        const int at_p = scan_units<W>(mine_p, total_p, unused, sm + 2 * W) * hrs;
         if (total_p * hrs <= p.ctas * per) {
             pad = per;
             total = total_p * hrs;
@@ -517,17 +694,17 @@ __device__ __forceinline__ bool locate(const FwdParams& p, int* sm, Cursor& cur,
             len = length_of(p, ++b);
             t = padded(tiles_in(len), pad) * hrs;
         }
-        sm[2 * W] = b;
-        sm[2 * W + 1] = u - at;
-        sm[2 * W + 2] = len;
+        sm[4 * W] = b;
+        sm[4 * W + 1] = u - at;
+        sm[4 * W + 2] = len;
     }
     __syncthreads();
     cur.u = u;
     cur.end = min(total, u + per);
-    cur.b = sm[2 * W];
-    cur.len = sm[2 * W + 2];
+    cur.b = sm[4 * W];
+    cur.len = sm[4 * W + 2];
     cur.tiles = tiles_in(cur.len);
-    const int rem = sm[2 * W + 1], seg = padded(cur.tiles, pad);
+    const int rem = sm[4 * W + 1], seg = padded(cur.tiles, pad);
     cur.hr = rem / seg;
     cur.tile = rem - cur.hr * seg;
     return true;
@@ -588,7 +765,7 @@ struct FwdSmem {
     int off[kRows];                          // keys at the sequence's end that the row may not see
     float ml[kWarps][kRows][2];
     float row_ml[kRows][2];
-    int scan[2 * kWarps + 3];
+    int scan[4 * kWarps + 3];
     int last;
 };
 
@@ -990,6 +1167,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
     constexpr int kRows = 8 * NR, kStages = Smem::kStages, kStride = Smem::kStride;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
 
+    enter_stream_order();
     Cursor cur;
     int per = 0, pad = 1;
     if (locate<W>(p, sm.scan, cur, per, pad)) {

@@ -278,7 +278,7 @@ fa2_status fa2_bwd_noalloc(const void* q, const void* k, const void* v, const vo
  * that its table row cannot hold, is not accepted and wants no page. A length
  * below 0 or above max_pages * page_size counts as 0 and is reported, and so
  * is a ring that is not one. A page that two requests share must be given back
- * once only. One or two launches; calls that share a ring must be ordered.
+ * once only. One launch; calls that share a ring must be ordered.
  */
 fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
                         int32_t* free_pages, const int32_t* free_state, int32_t* seq_lens_out,
@@ -289,7 +289,8 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
  * Quantises new keys and values and writes them into their slots.
  *   k, v   : [B, H_kv, N, d] bf16 or fp16, elements of a row adjacent; the
  *            strides of request, head and token are given in elements
- *            (multiples of 8, >= 0) so that views of a projection's output need no copy
+ *            (multiples of 8, 0 .. 2^31 - 8) so that views of a
+ *            projection's output need no copy
  *   slots  : [B, N] int32; a negative slot is skipped. A slot named twice in
  *            one call holds, 16 elements by 16 elements, either token
  * For each 16 elements x: scale = e4m3(max|x| / (6 descale)), t = scale *
@@ -340,9 +341,10 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
                        int page_size, int num_pages, float scale, int causal, fa2_dtype dtype,
                        cudaStream_t stream);
 
-/* Bytes of workspace that fa2_fwd_kv4 needs for these sizes, whatever B and
- * the lengths; -1 for sizes that it does not take. */
-int64_t fa2_fwd_kv4_workspace(int H_q, int H_kv, int N_q, int d);
+/* Bytes of workspace that fa2_fwd_kv4 needs for these sizes, whatever the
+ * lengths; -1 for sizes that it does not take. Not more for a smaller B,
+ * max_pages or page_size. */
+int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size);
 
 /*
  * Synchronises `stream`, then reads and clears the status word of the device

@@ -79,11 +79,13 @@ def test_forward_host_validation(i, x, want):
 
 def test_workspace_is_checked_exactly():
     for Hq, Hkv, Nq, d in ((32, 8, 1, 128), (32, 8, 5, 128), (8, 1, 2, 64), (16, 16, 700, 64)):
-        n = fa2.fa2_fwd_kv4_workspace(Hq, Hkv, Nq, d)
+        n = fa2.fa2_fwd_kv4_workspace(2, Hq, Hkv, Nq, d, 10, 64)
         args = FWD[:]
         args[9:15] = [n - 1, 2, Hq, Hkv, Nq, d]
         assert n > 0 and fa2.fa2_fwd_kv4_ptr(*args) == BAD
-    for bad in ((0, 8, 1, 128), (32, 0, 1, 128), (32, 5, 1, 128), (32, 8, 0, 128), (32, 8, 1, 96)):
+    for bad in ((2, 0, 8, 1, 128, 10, 64), (2, 32, 0, 1, 128, 10, 64), (2, 32, 5, 1, 128, 10, 64),
+                (2, 32, 8, 0, 128, 10, 64), (2, 32, 8, 1, 96, 10, 64), (0, 32, 8, 1, 128, 10, 64),
+                (2, 32, 8, 1, 128, 0, 64), (2, 32, 8, 1, 128, 10, 48)):
         assert fa2.fa2_fwd_kv4_workspace(*bad) == -1
 
 

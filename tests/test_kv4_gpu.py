@@ -558,7 +558,7 @@ def test_captured_step_replays_with_new_lengths(gpu_lib):
     k, v, q = torch.empty_like(toks[0, 0]), torch.empty_like(toks[0, 1]), torch.empty_like(qs[0])
     new = i32([1, 1, 1])
     acc, slots = torch.empty_like(new), torch.empty((B, 1), dtype=torch.int32, device=dev)
-    ws = torch.empty(fa2.fa2_fwd_kv4_workspace(Hq, Hkv, 1, d), dtype=torch.uint8, device=dev)
+    ws = torch.empty(fa2.fa2_fwd_kv4_workspace(B, Hq, Hkv, 1, d, W, page), dtype=torch.uint8, device=dev)
     o, lse = torch.empty_like(q), torch.empty((B, Hq, 1), device=dev)
 
     def step(s):
@@ -666,7 +666,7 @@ def test_refusals_on_the_device(gpu_lib):
         with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
             fa2.fa2_fwd_kv4(*args)
     with pytest.raises(fa2.FA2Error):
-        fa2.fa2_fwd_kv4(*good, workspace=torch.empty(1024, dtype=torch.uint8, device=dev))
+        fa2.fa2_fwd_kv4(*good, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
     with pytest.raises(ValueError):
         fa2.fa2_fwd_kv4(*good, o=torch.empty(1, 4, 1, 64, device=dev))
     k = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16, device=dev)
