@@ -7,6 +7,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +21,10 @@ SOURCES = [os.path.join(CSRC, "fa2_fwd_sm103.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "ptx_sm103.cuh"), os.path.join(CSRC, "fa2_fwd_sm103.cuh"), os.path.join(CSRC, "fa2_bwd_sm103.cuh"), os.path.join(CSRC, "fa2_fwd_fp8_sm103.cuh"),
                      os.path.join(CSRC, "fa2_fwd_d64_sm103.cuh"), os.path.join(CSRC, "fa2_kv4_sm103.cuh"),
                      os.path.join(INCLUDE, "fa2.h")]
+# The extension that passes torch tensors to the KV cache entry points (host code only).
+TORCH_LIB = os.path.join(PKG, "_kv4_torch.so")
+TORCH_SOURCES = [os.path.join(CSRC, "kv4_torch.cpp")]
+TORCH_DEPENDS = TORCH_SOURCES + [os.path.join(INCLUDE, "fa2.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,13 +37,30 @@ def needs_build(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    return any(os.path.getmtime(f) > t for f in DEPENDS)
+    return any(os.path.getmtime(f) > t for f in (TORCH_DEPENDS if lib == TORCH_LIB else DEPENDS))
+
+
+def torch_command(out: str) -> list:
+    """g++ command of the extension, against the installed torch."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I",
+            os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
+            sysconfig.get_paths()["include"], "-o", out, *TORCH_SOURCES, "-L", os.path.join(root, "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libfa2.so and libfa2_debug.so next to this file (in parallel)
-    if they are missing or stale; returns the release library's path."""
+    """Compile libfa2.so, libfa2_debug.so and the torch extension next to this
+    file (in parallel) if they are missing or stale; returns the release
+    library's path."""
     jobs = []
+    if force or needs_build(TORCH_LIB):
+        tmp = TORCH_LIB + f".tmp{os.getpid()}"
+        cmd = torch_command(tmp)
+        jobs.append((subprocess.Popen(cmd), tmp, TORCH_LIB, cmd))
     for lib, extra in ((LIB, []), (DEBUG_LIB, ["-DFA2_DEBUG"])):
         if not force and not needs_build(lib):
             continue

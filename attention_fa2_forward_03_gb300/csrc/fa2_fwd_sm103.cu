@@ -673,6 +673,8 @@ int kv4_nr(long long rows) {
     return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
 }
 
+constexpr int kv4_ctas_per_sm(int nr) { return nr == 1 ? 2 : 1; }
+
 // The CTAs that can have work: runs have kMinRun tiles or more, and a padded
 // line has at most one run for each segment beyond those.
 long long kv4_ctas(long long B, long long hkv, long long rows, int nr, long long max_tokens, long long most) {
@@ -682,10 +684,18 @@ long long kv4_ctas(long long B, long long hkv, long long rows, int nr, long long
     return std::min(most, segments * (tiles / fa2::kv4::kMinRun + 1));
 }
 
-// Workspace: two partial results a CTA, then a counter a CTA.
-int64_t kv4_workspace(long long ctas, int nr, int d) {
-    return ctas * (2LL * 8 * nr * (d + 2) * static_cast<int64_t>(sizeof(float)) +
-                   static_cast<int64_t>(sizeof(unsigned long long)));
+// Workspace: two partial results a CTA, then a counter a CTA; nothing where
+// no segment can be split: each gets a CTA of its own (`locate`).
+int64_t kv4_workspace(long long B, long long hkv, long long rows, int d, long long max_tokens) {
+    const int nr = kv4_nr(rows);
+    const long long most = 128 * kv4_ctas_per_sm(nr);   // CTAs that a whole device runs at once
+    const long long segments = B * hkv * ((rows + 8 * nr - 1) / (8 * nr));
+    if (segments <= most &&
+        (max_tokens + fa2::kv4::kTile - 1) / fa2::kv4::kTile <= fa2::kv4::kMinRun + fa2::kv4::kSpare)
+        return 0;
+    return kv4_ctas(B, hkv, rows, nr, max_tokens, fa2::kv4::kMaxCtas) *
+           (2LL * 8 * nr * (d + 2) * static_cast<int64_t>(sizeof(float)) +
+            static_cast<int64_t>(sizeof(unsigned long long)));
 }
 
 // A number that no other launch of this process has, and that memory left
@@ -704,6 +714,7 @@ template <int D, int NR, bool kBf16>
 fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
     constexpr int kSmem = static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, NR>));
     using Shape = fa2::kv4::Shape<NR>;
+    static_assert(Shape::kCtas == kv4_ctas_per_sm(NR), "CTAs an SM");
     static_assert(Shape::kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory budget");
     auto kern = fa2::kv4::fa2_kv4_fwd_kernel<D, NR, kBf16>;
     const int slot = 20 + (D == 128 ? 0 : 8) + 2 * (NR - 1) + (kBf16 ? 0 : 1);
@@ -716,8 +727,12 @@ fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
         return FA2_ERR_UNSUPPORTED;
     p.ctas = static_cast<int>(kv4_ctas(p.B, p.hkv, p.rows, NR, p.max_tokens,
                                        std::min(sm_count(dev) * Shape::kCtas, fa2::kv4::kMaxCtas)));
-    p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
-    p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * 8 * NR * 2);
+    // Without a workspace every segment needs a CTA, also where they run in waves.
+    if (!p.part_o) p.ctas = std::max(p.ctas, p.B * p.hkv * p.rblocks);
+    if (p.part_o) {
+        p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
+        p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * 8 * NR * 2);
+    }
     p.nonce = kv4_nonce();
     return kv4_launch_kernel(kern, p.ctas, Shape::kThreads, kSmem, stream, p);
 }
@@ -872,9 +887,8 @@ int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_
     if (B <= 0 || H_q <= 0 || H_kv <= 0 || N_q <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
         kv4_check_pages(page_size, 1, max_pages) != FA2_OK)
         return -1;
-    const long long rows = static_cast<long long>(H_q / H_kv) * N_q;
-    const int nr = kv4_nr(rows);
-    return kv4_workspace(kv4_ctas(B, H_kv, rows, nr, static_cast<long long>(max_pages) * page_size, fa2::kv4::kMaxCtas), nr, d);
+    return kv4_workspace(B, H_kv, static_cast<long long>(H_q / H_kv) * N_q, d,
+                         static_cast<long long>(max_pages) * page_size);
 }
 
 fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -882,8 +896,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
                        int64_t workspace_bytes, int B, int H_q, int H_kv, int N_q, int d, int max_pages,
                        int page_size, int num_pages, float scale, int causal, fa2_dtype dtype,
                        cudaStream_t stream) {
-    if (!q || !cache || !block_table || !seq_lens || !k_descale || !v_descale || !o || !lse || !workspace)
-        return FA2_ERR_INVALID_ARG;
+    if (!q || !cache || !block_table || !seq_lens || !k_descale || !v_descale || !o || !lse) return FA2_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace))
         return FA2_ERR_INVALID_ARG;
     if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(k_descale) || !aligned4(v_descale))
@@ -899,7 +912,8 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     const long long heads = static_cast<long long>(B) * H_q;
     if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit,
     if (H_kv > 65535 / 2) return FA2_ERR_UNSUPPORTED;                    // and a page's bytes
-    if (workspace_bytes < fa2_fwd_kv4_workspace(B, H_q, H_kv, N_q, d, max_pages, page_size)) return FA2_ERR_INVALID_ARG;
+    const int64_t need = fa2_fwd_kv4_workspace(B, H_q, H_kv, N_q, d, max_pages, page_size);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FA2_ERR_INVALID_ARG;
     int dev = 0;
     if ((st = check_device(&dev)) != FA2_OK) return st;
     fa2::kv4::FwdParams p{};
@@ -911,7 +925,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     p.block_table = block_table;
     p.o = o;
     p.lse = lse;
-    p.part_o = static_cast<float*>(workspace);
+    p.part_o = need > 0 ? static_cast<float*>(workspace) : nullptr;
     p.B = B;
     p.hkv = H_kv;
     p.nq = N_q;

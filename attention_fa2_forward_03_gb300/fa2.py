@@ -399,52 +399,36 @@ def fa2_kv4_cache_shape(num_pages: int, H_kv: int, page_size: int, d: int) -> tu
     return (num_pages, H_kv, 2, page_size * (d // 2 + d // 16))
 
 
-# These wrappers run once a layer and decoding step, so each checks its
-# arguments in one pass of cheap comparisons; the helpers below find out what
-# is wrong once that pass has failed.
+# Arguments are checked, outputs allocated and the C entry points called in
+# csrc/kv4_torch.cpp: these calls run once a layer and decoding step, and in
+# Python that would take longer than their kernels.
 
-def _kv4_call(fn, index, stream, *args):
-    """Runs a C entry point with device `index` current (the library launches
-    on the current device) on `stream` (None: that device's current stream)."""
-    import torch
-
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return fn(*args, int(stream))
-    return fn(*args, stream)
+KV4_TORCH_LIB = os.path.join(PKG, "_kv4_torch.so")
+_kv4_mod = None
 
 
-def _kv4_same_device(index, **tensors):
-    for name, t in tensors.items():
-        if t.get_device() != index or index < 0:
-            raise ValueError(f"all tensors must be on one CUDA device, {name} is on {t.device}")
+def _kv4():
+    """The extension that passes torch tensors to the C entry points (built by
+    ``__graft_entry__.build()``); raises if absent."""
+    global _kv4_mod
+    if _kv4_mod is None:
+        import importlib.machinery
+        import importlib.util
 
+        import torch  # before the extension, which resolves against its libraries
 
-def _kv4_ints(name, t, shape):
-    import torch
-
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-def _kv4_refuse_cache(index, cache, k_descale, v_descale, H_kv, d, what):
-    """Says what is wrong with a cache or its descales (or, if nothing is,
-    with `what`)."""
-    import torch
-
-    _kv4_same_device(index, cache=cache, k_descale=k_descale, v_descale=v_descale)
-    token = max(1, d // 2 + d // 16)
-    if (cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous()
-            or cache.shape[1] != H_kv or cache.shape[2] != 2 or cache.shape[3] == 0 or cache.shape[3] % token):
-        raise ValueError("cache must be a contiguous uint8 CUDA tensor [num_pages, H_kv, 2, page_size*(d/2+d/16)]")
-    for t in (k_descale, v_descale):
-        if t.dtype != torch.float32 or t.shape != (H_kv,) or not t.is_contiguous():
-            raise ValueError("descales must be contiguous fp32 CUDA tensors [H_kv]")
-    raise ValueError(what)
+        lib = load()
+        if not os.path.exists(KV4_TORCH_LIB):
+            raise ImportError(f"extension {KV4_TORCH_LIB} is missing: run __graft_entry__.build() "
+                              "(python -m attention_fa2_forward_03_gb300.build)")
+        loader = importlib.machinery.ExtensionFileLoader("_kv4_torch", KV4_TORCH_LIB)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kv4_torch", loader))
+        loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.fa2_kv4_plan, lib.fa2_kv4_append, lib.fa2_kv4_gather, lib.fa2_fwd_kv4, lib.fa2_fwd_kv4_workspace)),
+                 torch.OutOfMemoryError)
+        _kv4_mod = mod
+    return _kv4_mod
 
 
 def fa2_kv4_plan(seq_lens, new_lens, block_table, free_pages, free_state, page_size, N, seq_lens_out=None,
@@ -456,177 +440,44 @@ def fa2_kv4_plan(seq_lens, new_lens, block_table, free_pages, free_state, page_s
     most tokens a request may add. seq_lens_out and free_state_out may be
     seq_lens and free_state themselves. Returns (seq_lens_out [B],
     accepted [B], slots [B, N], free_state_out [2])."""
-    import torch
-
-    if seq_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("seq_lens must be [B], block_table [B, max_pages], free_pages [num_pages]")
-    B, W = block_table.shape
-    dev, index = seq_lens.device, seq_lens.get_device()
-    if seq_lens_out is None:
-        seq_lens_out = torch.empty_like(seq_lens)
-    if accepted is None:
-        accepted = torch.empty_like(seq_lens)
-    if slots is None:
-        slots = torch.empty((B, N), dtype=torch.int32, device=dev)
-    if free_state_out is None:
-        free_state_out = torch.empty_like(free_state)
-    i32, row, two = torch.int32, (B,), (2,)
-    for t, shape in ((seq_lens, row), (new_lens, row), (block_table, (B, W)), (free_pages, None), (free_state, two),
-                     (seq_lens_out, row), (accepted, row), (slots, (B, N)), (free_state_out, two)):
-        if (t.dtype is not i32 or t.get_device() != index or not t.is_contiguous() or index < 0
-                or (shape is not None and t.shape != shape)):
-            tensors = {"seq_lens": seq_lens, "new_lens": new_lens, "block_table": block_table,
-                       "free_pages": free_pages, "free_state": free_state, "seq_lens_out": seq_lens_out,
-                       "accepted": accepted, "slots": slots, "free_state_out": free_state_out}
-            _kv4_same_device(index, **tensors)
-            for name, x in tensors.items():
-                _kv4_ints(name, x, {"block_table": (B, W), "free_pages": x.shape, "free_state": two, "slots": (B, N),
-                                    "free_state_out": two}.get(name, row))
-    rc = _kv4_call(load().fa2_kv4_plan, index, stream, seq_lens.data_ptr(), new_lens.data_ptr(),
-                   block_table.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(), seq_lens_out.data_ptr(),
-                   accepted.data_ptr(), slots.data_ptr(), free_state_out.data_ptr(), B, N, W, page_size,
-                   free_pages.shape[0])
-    if rc != FA2_OK:
-        raise FA2Error(rc, "fa2_kv4_plan")
-    return seq_lens_out, accepted, slots, free_state_out
+    out = (_kv4_mod or _kv4()).plan(seq_lens, new_lens, block_table, free_pages, free_state, page_size, N,
+                                    seq_lens_out, accepted, slots, free_state_out, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_kv4_plan")
+    return out
 
 
 def fa2_kv4_append(k, v, slots, cache, k_descale, v_descale, stream=None):
     """Quantises k, v [B, Hkv, N, d] (any strides that are multiples of 8
     elements, rows of adjacent elements) into the slots [B, N] of the cache;
     negative slots are skipped. Returns the cache."""
-    import torch
-
-    if k.dim() != 4 or k.shape != v.shape or cache.dim() != 4:
-        raise ValueError("k and v must be 4-D [B, H_kv, N, d] of one shape, cache 4-D")
-    B, Hkv, N, d = k.shape
-    num_pages, heads, two, size = cache.shape
-    index, token = k.get_device(), (d // 2 + d // 16) or 1
-    if k.dtype != v.dtype:
-        raise TypeError("k and v must share one dtype")
-    (kb, kh, kn, ke), (vb, vh, vn, ve) = k.stride(), v.stride()
-    if not (index >= 0 and v.get_device() == index and slots.get_device() == index and cache.get_device() == index
-            and k_descale.get_device() == index and v_descale.get_device() == index and ke == 1 and ve == 1
-            and heads == Hkv and two == 2 and size % token == 0 and cache.dtype is torch.uint8
-            and slots.dtype is torch.int32 and k_descale.dtype is torch.float32 and v_descale.dtype is torch.float32
-            and slots.shape == (B, N) and k_descale.shape == (Hkv,) and v_descale.shape == (Hkv,)
-            and cache.is_contiguous() and slots.is_contiguous() and k_descale.is_contiguous()
-            and v_descale.is_contiguous()):
-        _kv4_same_device(index, k=k, v=v, slots=slots)
-        _kv4_ints("slots", slots, (B, N))
-        _kv4_refuse_cache(index, cache, k_descale, v_descale, Hkv, d, "the rows of k and v must be adjacent elements")
-    # the stride of an axis of length 1 is never used and may be anything
-    if B == 1:
-        kb = vb = 0
-    if Hkv == 1:
-        kh = vh = 0
-    if N == 1:
-        kn = vn = 0
-    rc = _kv4_call(load().fa2_kv4_append, index, stream, k.data_ptr(), v.data_ptr(), slots.data_ptr(),
-                   cache.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), B, Hkv, N, d, kb, kh, kn, vb, vh, vn,
-                   size // token, num_pages, _dtype_code(k))
-    if rc != FA2_OK:
-        raise FA2Error(rc, "fa2_kv4_append")
-    return cache
+    out = (_kv4_mod or _kv4()).append(k, v, slots, cache, k_descale, v_descale, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_kv4_append")
+    return out
 
 
 def fa2_kv4_gather(cache, block_table, seq_lens, k_descale, v_descale, N, d, starts=None, dtype=None, k=None, v=None,
                    stream=None):
-    """Reads cached tokens back: k, v [B, Hkv, N, d] of `dtype` (bf16 by
-    default, or k's), row i of request b its position starts[b] + i (starts
-    None: i); rows at or past seq_lens[b] are zeros. Returns (k, v)."""
-    import torch
-
-    if block_table.dim() != 2 or cache.dim() != 4:
-        raise ValueError("block_table must be [B, max_pages], cache [num_pages, H_kv, 2, page_size*(d/2+d/16)]")
-    B, W = block_table.shape
-    num_pages, Hkv, two, size = cache.shape
-    index, token = cache.get_device(), (d // 2 + d // 16) or 1
-    if not (index >= 0 and block_table.get_device() == index and seq_lens.get_device() == index
-            and k_descale.get_device() == index and v_descale.get_device() == index and two == 2
-            and size % token == 0 and cache.dtype is torch.uint8 and block_table.dtype is torch.int32
-            and seq_lens.dtype is torch.int32 and k_descale.dtype is torch.float32
-            and v_descale.dtype is torch.float32 and seq_lens.shape == (B,) and k_descale.shape == (Hkv,)
-            and v_descale.shape == (Hkv,) and cache.is_contiguous() and block_table.is_contiguous()
-            and seq_lens.is_contiguous() and k_descale.is_contiguous() and v_descale.is_contiguous()
-            and (starts is None or (starts.get_device() == index and starts.dtype is torch.int32
-                                    and starts.shape == (B,) and starts.is_contiguous()))):
-        _kv4_same_device(index, block_table=block_table, seq_lens=seq_lens)
-        _kv4_ints("block_table", block_table, (B, W))
-        _kv4_ints("seq_lens", seq_lens, (B,))
-        _kv4_refuse_cache(index, cache, k_descale, v_descale, Hkv, d,
-                          "starts must be a contiguous int32 CUDA tensor [B] on the cache's device")
-    if dtype is None:
-        dtype = torch.bfloat16 if k is None else k.dtype
-    shape = (B, Hkv, N, d)
-    if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.device)
-    elif k.shape != shape or k.dtype != dtype or k.get_device() != index or not k.is_contiguous():
-        raise ValueError("k must be a contiguous tensor [B, H_kv, N, d] of `dtype` on the cache's device")
-    if v is None:
-        v = torch.empty_like(k)
-    elif v.shape != shape or v.dtype != dtype or v.get_device() != index or not v.is_contiguous():
-        raise ValueError("v must be a contiguous tensor [B, H_kv, N, d] of `dtype` on the cache's device")
-    rc = _kv4_call(load().fa2_kv4_gather, index, stream, cache.data_ptr(), block_table.data_ptr(),
-                   seq_lens.data_ptr(), None if starts is None else starts.data_ptr(), k_descale.data_ptr(),
-                   v_descale.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, N, d, W, size // token, num_pages,
-                   _dtype_code(k))
-    if rc != FA2_OK:
-        raise FA2Error(rc, "fa2_kv4_gather")
-    return k, v
+    """Reads cached tokens back: k, v [B, Hkv, N, d] of `dtype` (k's by
+    default, bf16 without a k), row i of request b its position starts[b] + i
+    (starts None: i); rows at or past seq_lens[b] are zeros. Returns (k, v)."""
+    out = (_kv4_mod or _kv4()).gather(cache, block_table, seq_lens, k_descale, v_descale, N, d, starts, dtype, k, v,
+                                      stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_kv4_gather")
+    return out
 
 
 def fa2_fwd_kv4(q, cache, block_table, seq_lens, k_descale, v_descale, o=None, lse=None, workspace=None, scale=None,
                 causal=False, stream=None):
     """Attention of the newest N_q tokens of each request, q [B, Hq, Nq, d],
-    over its seq_lens[b] cached tokens. `workspace`: a uint8 CUDA tensor of
-    fa2_fwd_kv4_workspace(...) bytes that no other call in flight uses;
-    allocated with torch when not given, as o and lse are. Returns
+    over its seq_lens[b] cached tokens. `workspace`: a CUDA tensor of
+    fa2_fwd_kv4_workspace(...) bytes (none for 0) that no other call in flight
+    uses; allocated with torch when not given, as o and lse are. Returns
     (o [B, Hq, Nq, d], lse fp32 [B, Hq, Nq])."""
-    import torch
-
-    if q.dim() != 4 or cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q must be [B, H_q, N_q, d], cache 4-D and block_table [B, max_pages]")
-    B, Hq, Nq, d = q.shape
-    num_pages, Hkv, two, size = cache.shape
-    rows, W = block_table.shape
-    index, token = q.get_device(), (d // 2 + d // 16) or 1
-    if not (index >= 0 and cache.get_device() == index and block_table.get_device() == index
-            and seq_lens.get_device() == index and k_descale.get_device() == index and v_descale.get_device() == index
-            and rows == B and two == 2 and size % token == 0 and cache.dtype is torch.uint8
-            and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32
-            and k_descale.dtype is torch.float32 and v_descale.dtype is torch.float32 and seq_lens.shape == (B,)
-            and k_descale.shape == (Hkv,) and v_descale.shape == (Hkv,) and q.is_contiguous()
-            and cache.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()
-            and k_descale.is_contiguous() and v_descale.is_contiguous()):
-        _kv4_same_device(index, q=q, block_table=block_table, seq_lens=seq_lens)
-        _kv4_ints("block_table", block_table, (B, W))
-        _kv4_ints("seq_lens", seq_lens, (B,))
-        _kv4_refuse_cache(index, cache, k_descale, v_descale, Hkv, d, "q must be contiguous")
-    page_size = size // token
-    if o is None:
-        o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype != q.dtype or o.get_device() != index or not o.is_contiguous():
-        raise ValueError("o must be a contiguous tensor like q")
-    if lse is None:
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-    elif (lse.shape != (B, Hq, Nq) or lse.dtype != torch.float32 or lse.get_device() != index
-          or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 tensor [B, H_q, N_q] on q's device")
-    lib = load()
-    if workspace is None:
-        nbytes = max(lib.fa2_fwd_kv4_workspace(B, Hq, Hkv, Nq, d, W, page_size), 16)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        if stream is not None:   # freed below while `stream` may still use it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on q's device")
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    rc = _kv4_call(lib.fa2_fwd_kv4, index, stream, q.data_ptr(), cache.data_ptr(), block_table.data_ptr(),
-                   seq_lens.data_ptr(), k_descale.data_ptr(), v_descale.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                   workspace.data_ptr(), nbytes, B, Hq, Hkv, Nq, d, W, page_size, num_pages,
-                   d ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(q))
-    if rc != FA2_OK:
-        raise FA2Error(rc, "fa2_fwd_kv4")
-    return o, lse
+    out = (_kv4_mod or _kv4()).fwd(q, cache, block_table, seq_lens, k_descale, v_descale, o, lse, workspace, scale,
+                                   causal, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_fwd_kv4")
+    return out

@@ -325,8 +325,9 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
  *   causal   : 0 or 1. With 1, query row i attends position
  *              j < seq_lens[b] + i + 1 - N_q, as fa2_fwd_ex. A row with no
  *              allowed key gets O = 0 and LSE = -inf
- *   workspace : device, fa2_fwd_kv4_workspace(...) bytes, contents irrelevant
- *              before and after; calls that may overlap need their own
+ *   workspace : device, fa2_fwd_kv4_workspace(...) bytes (may be NULL for 0),
+ *              contents irrelevant before and after; calls that may overlap
+ *              need their own
  * Any N_q >= 1 is right; the kernel is made for few rows a KV head
  * (H_q / H_kv * N_q up to 32 read the cache once, every 32 more once again).
  * Prompts and their chunks are faster by fa2_kv4_gather and fa2_fwd_ex.

@@ -62,7 +62,7 @@ def test_gather_host_validation(i, x, want):
     assert fa2.fa2_kv4_gather_ptr(*swap(GATHER, i, x)) == want
 
 
-FWD = [A] * 9 + [1 << 40, 2, 32, 8, 1, 128, 10, 64, 100, 0.1, 0, 0]
+FWD = [A] * 9 + [1 << 40, 2, 32, 8, 1, 128, 99, 64, 100, 0.1, 0, 0]
 
 
 @pytest.mark.parametrize("i,x,want", [
@@ -79,10 +79,13 @@ def test_forward_host_validation(i, x, want):
 
 def test_workspace_is_checked_exactly():
     for Hq, Hkv, Nq, d in ((32, 8, 1, 128), (32, 8, 5, 128), (8, 1, 2, 64), (16, 16, 700, 64)):
-        n = fa2.fa2_fwd_kv4_workspace(2, Hq, Hkv, Nq, d, 10, 64)
+        n = fa2.fa2_fwd_kv4_workspace(2, Hq, Hkv, Nq, d, 99, 64)
         args = FWD[:]
         args[9:15] = [n - 1, 2, Hq, Hkv, Nq, d]
         assert n > 0 and fa2.fa2_fwd_kv4_ptr(*args) == BAD
+    # short sequences are never split: no workspace, and none is asked for
+    assert fa2.fa2_fwd_kv4_workspace(2, 32, 8, 1, 128, 36, 64) == 0 < fa2.fa2_fwd_kv4_workspace(2, 32, 8, 1, 128, 37, 64)
+    assert fa2.fa2_fwd_kv4_workspace(32, 32, 8, 1, 128, 36, 64) == 0 < fa2.fa2_fwd_kv4_workspace(33, 32, 8, 1, 128, 36, 64)
     for bad in ((2, 0, 8, 1, 128, 10, 64), (2, 32, 0, 1, 128, 10, 64), (2, 32, 5, 1, 128, 10, 64),
                 (2, 32, 8, 0, 128, 10, 64), (2, 32, 8, 1, 96, 10, 64), (0, 32, 8, 1, 128, 10, 64),
                 (2, 32, 8, 1, 128, 0, 64), (2, 32, 8, 1, 128, 10, 48)):

@@ -665,8 +665,11 @@ def test_refusals_on_the_device(gpu_lib):
         args[i] = bad
         with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
             fa2.fa2_fwd_kv4(*args)
+    wide = list(good)
+    wide[2] = i32(np.zeros((1, 400)))
     with pytest.raises(fa2.FA2Error):
-        fa2.fa2_fwd_kv4(*good, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
+        fa2.fa2_fwd_kv4(*wide, workspace=torch.empty(64, dtype=torch.uint8, device=dev))
+    fa2.fa2_fwd_kv4(*wide)
     with pytest.raises(ValueError):
         fa2.fa2_fwd_kv4(*good, o=torch.empty(1, 4, 1, 64, device=dev))
     k = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16, device=dev)
