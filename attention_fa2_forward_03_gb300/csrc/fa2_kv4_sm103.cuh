@@ -622,89 +622,86 @@ struct Cursor {
 
 __device__ __forceinline__ int length_of(const FwdParams& p, int b) { return min(max(p.seq_lens[b], 0), p.max_tokens); }
 __device__ __forceinline__ int tiles_in(int len) { return (len >> 5) + ((len & 31) != 0); }
+// `tiles` rounded up to whole runs of `pad`, of which there are fewer than
+// 2^20; inv = 1 / pad.
+__device__ __forceinline__ int padded(int tiles, int pad, float inv) {
+    if (pad == 1) return tiles;
+    int n = static_cast<int>(static_cast<float>(tiles) * inv);   // off by one at most
+    n += n * pad < tiles;
+    n -= (n - 1) * pad >= tiles;
+    return n * pad;
+}
 __device__ __forceinline__ int padded(int tiles, int pad) { return (tiles + pad - 1) / pad * pad; }
 
-// Exclusive prefix sum over the block's threads of `mine`, and the total; the
-// largest `top`. `sm`: 2 W ints.
-template <int W>
-__device__ __forceinline__ int scan_units(int mine, int& total, int& top, int* sm) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = mine;
+__device__ __forceinline__ int warp_scan(int x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(~0u, inc, o);
-        if (lane >= o) inc += t;
+        const int y = __shfl_up_sync(~0u, x, o);
+        if ((threadIdx.x & 31) >= o) x += y;
     }
-    top = __reduce_max_sync(~0u, top);
-    if (lane == 31) {
-        sm[warp] = inc;
-        sm[W + warp] = top;
-    }
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w == warp) before = total;
-        total += sm[w];
-        top = max(top, sm[W + w]);
-    }
-    return before + inc - mine;
+    return x;
 }
 
-// The start of this CTA's run; false if it has none. `sm`: 4 W + 3 ints.
+// The start of this CTA's run; false if it has none. Every warp finds it for
+// itself, a lane looking at its share of the requests: no barrier.
 template <int W>
-__device__ __forceinline__ bool locate(const FwdParams& p, int* sm, Cursor& cur, int& per, int& pad) {
-    const int tid = threadIdx.x;
-    const int chunk = (p.B + 32 * W - 1) / (32 * W);
-    const int b0 = min(tid * chunk, p.B), b1 = min(b0 + chunk, p.B);
+__device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per, int& pad) {
+    const int lane = threadIdx.x & 31;
+    const int chunk = (p.B + 31) >> 5;
+    const int b0 = min(lane * chunk, p.B), b1 = min(b0 + chunk, p.B);
     const int hrs = p.hkv * p.rblocks;
-    int mine = 0, total, longest = 0;
+    int mine = 0, longest = 0;
+#pragma unroll 4
     for (int b = b0; b < b1; ++b) {
         const int t = tiles_in(length_of(p, b));
         mine += t;
         longest = max(longest, t);
     }
-    int at = scan_units<W>(mine, total, longest, sm) * hrs;
-    total *= hrs;
+    int to = warp_scan(mine);
+    int total = __shfl_sync(~0u, to, 31) * hrs;
     if (total == 0) return false;
+    longest = __reduce_max_sync(~0u, longest);
     per = max((total + p.ctas - 1) / p.ctas, kMinRun);
     per = (per + W - 1) / W * W;
     pad = 1;
+    float inv = 1.0f;
     if (p.B * hrs <= p.ctas) {
         // Every segment could have a CTA of its own, which is worth a
         // somewhat longer run: nothing to join, no second segment.
         if (longest <= per + kSpare) per = max(per, (longest + W - 1) / W * W);
-        int mine_p = 0, total_p, unused = 0;
-        for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in(length_of(p, b)), per);
-        const int at_p = scan_units<W>(mine_p, total_p, unused, sm + 2 * W) * hrs;
-        if (total_p * hrs <= p.ctas * per) {
+        inv = 1.0f / static_cast<float>(per);
+        int mine_p = 0;
+        for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in(length_of(p, b)), per, inv);
+        const int to_p = warp_scan(mine_p), total_p = __shfl_sync(~0u, to_p, 31) * hrs;
+        if (total_p <= p.ctas * per) {
             pad = per;
-            total = total_p * hrs;
-            at = at_p;
+            total = total_p;
+            to = to_p;
             mine = mine_p;
+        } else {
+            inv = 1.0f;
         }
     }
     const int u = static_cast<int>(blockIdx.x) * per;
     if (u >= total) return false;
-    if (u >= at && u < at + mine * hrs) {
-        int b = b0, len = length_of(p, b), t = padded(tiles_in(len), pad) * hrs;
-        while (u >= at + t) {
+    int at = (to - mine) * hrs, b = b0, len = 0;   // the lane's first unit
+    const bool here = u >= at && u < to * hrs;
+    if (here) {
+        while (true) {
+            len = length_of(p, b);
+            const int t = padded(tiles_in(len), pad, inv) * hrs;
+            if (u < at + t) break;
             at += t;
-            len = length_of(p, ++b);
-            t = padded(tiles_in(len), pad) * hrs;
+            ++b;
         }
-        sm[4 * W] = b;
-        sm[4 * W + 1] = u - at;
-        sm[4 * W + 2] = len;
     }
-    __syncthreads();
+    const int from = __ffs(__ballot_sync(~0u, here)) - 1;
     cur.u = u;
     cur.end = min(total, u + per);
-    cur.b = sm[4 * W];
-    cur.len = sm[4 * W + 2];
+    cur.b = __shfl_sync(~0u, b, from);
+    cur.len = __shfl_sync(~0u, len, from);
     cur.tiles = tiles_in(cur.len);
-    const int rem = sm[4 * W + 1], seg = padded(cur.tiles, pad);
+    const int rem = u - __shfl_sync(~0u, at, from), seg = padded(cur.tiles, pad, inv);
     cur.hr = rem / seg;
     cur.tile = rem - cur.hr * seg;
     return true;
@@ -765,7 +762,7 @@ struct FwdSmem {
     int off[kRows];                          // keys at the sequence's end that the row may not see
     float ml[kWarps][kRows][2];
     float row_ml[kRows][2];
-    int scan[4 * kWarps + 3];
+    unsigned long long counter;              // the segment's, as it was when the segment began
     int last;
 };
 
@@ -1148,12 +1145,9 @@ struct Loader {
 // done. It needs no clearing beforehand: a word that does not carry this
 // launch's nonce is replaced by the nonce before anyone counts on it, and the
 // last CTA leaves 0, so that a replayed launch finds none of its own.
-__device__ __forceinline__ void open_counter(unsigned long long* word, unsigned long long nonce) {
-    const unsigned long long old = *static_cast<volatile unsigned long long*>(word);
-    if ((old & ~0xFFFFULL) != nonce) atomicCAS(word, old, nonce);
-}
-__device__ __forceinline__ int count_in(unsigned long long* word) {
+__device__ __forceinline__ int count_in(unsigned long long* word, unsigned long long seen, unsigned long long nonce) {
     unsigned long long old;
+    if ((seen & ~0xFFFFULL) != nonce) atomicCAS(word, seen, nonce);   // in vain if someone else did it since
     asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(old) : "l"(word) : "memory");
     return static_cast<int>(old & 0xFFFF) + 1;
 }
@@ -1170,7 +1164,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
     enter_stream_order();
     Cursor cur;
     int per = 0, pad = 1;
-    if (locate<W>(p, sm.scan, cur, per, pad)) {
+    if (locate<W>(p, cur, per, pad)) {
         load_q<D, NR>(p, sm, cur.b, cur.hr);
         float k_descale = p.k_descale[cur.hr / p.rblocks];
         Loader<D, W> ld;
@@ -1194,7 +1188,10 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
             const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
             const bool split = seg0 < static_cast<int>(blockIdx.x) * per || seg1 > cur.end;
             const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
-            if (split && tid == 0) open_counter(p.arrived + c0, p.nonce);
+            if (split && tid == 0)   // read ahead; in place when the tiles are done
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.counter)),
+                             "l"(p.arrived + c0)
+                             : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;
             next_segment(p, nxt, pad);
@@ -1296,7 +1293,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
             if (split) {
                 const int parts = c1 - c0 + 1;
                 if (tid == 0) {
-                    sm.last = count_in(p.arrived + c0) == parts;
+                    sm.last = count_in(p.arrived + c0, sm.counter, p.nonce) == parts;
                     if (sm.last) p.arrived[c0] = 0;
                 }
                 __syncthreads();
