@@ -17,6 +17,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "fa2.h"
@@ -649,6 +650,16 @@ fa2_status kv4_launch_kernel(void (*kern)(P), long long grid, int threads, int s
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? FA2_OK : cuda_fail();
 }
 
+// Launches a copy of `rows` rows with one row a thread where four would give
+// fewer blocks than SMs, else with four.
+template <typename F>
+fa2_status kv4_rows(int dev, int rows, int d, F&& launch) {
+    const int pass = 256 / (d / 8);
+    const long long blocks = (static_cast<long long>(rows) + 4 * pass - 1) / (4 * pass);
+    if (blocks < sm_count(dev)) return launch(std::true_type{}, (static_cast<long long>(rows) + pass - 1) / pass);
+    return launch(std::false_type{}, blocks);
+}
+
 int log2_of(int x) {
     int n = 0;
     while ((1 << n) < x) ++n;
@@ -781,10 +792,25 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
-    // One block where it has at most eight slots a thread to write, a cluster otherwise.
-    const bool many = static_cast<long long>(B) * N > 8 * fa2::kv4::kPlanThreads;
-    return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel, many ? fa2::kv4::kPlanCtas : 1, fa2::kv4::kPlanThreads, 0,
-                             stream, p, many ? fa2::kv4::kPlanCtas : 1);
+    // 256 threads for a decoding step, whose scan is the shorter one. Where
+    // there are thousands of slots, a warp for every 256 (48 prompts of 16384:
+    // 10 us; 20 by a cluster of eight CTAs, which writing in place asks for).
+    const long long all = static_cast<long long>(B) * N;
+    auto in = [](const void* a, const void* out, long long n) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(out);
+        return x < y + 4 * n && y < x + 4 * n;
+    };
+    p.in_place = 0;
+    for (const void* a : {static_cast<const void*>(seq_lens), static_cast<const void*>(new_lens)})
+        p.in_place |= in(a, seq_lens_out, B) || in(a, accepted, B);
+    p.in_place |= in(free_state, free_state_out, 2);
+    if (B <= 256 && all <= 2048) return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel<256>, 1, 256, 0, stream, p);
+    if (all <= 8192) return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel<1024>, 1, 1024, 0, stream, p);
+    if (p.in_place)
+        return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel<1024>, fa2::kv4::kPlanCtas, 1024, 0, stream, p,
+                                 fa2::kv4::kPlanCtas);
+    return kv4_launch_kernel(fa2::kv4::fa2_kv4_plan_kernel<1024>,
+                             std::min<long long>(sm_count(dev), (all + 8191) / 8192), 1024, 0, stream, p);
 }
 
 fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, void* cache,
@@ -827,15 +853,16 @@ fa2_status fa2_kv4_append(const void* k, const void* v, const int32_t* slots, vo
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_slots = num_pages * page_size;
-    const int rows_block = d == 128 ? fa2::kv4::Copy<128>::kRows : fa2::kv4::Copy<64>::kRows;
-    const long long grid = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
     const bool bf = dtype == FA2_BF16;
-    using namespace fa2::kv4;
-    if (d == 128)
-        return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<128, true>, grid, 256, 0, stream, p)
-                  : kv4_launch_kernel(fa2_kv4_append_kernel<128, false>, grid, 256, 0, stream, p);
-    return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<64, true>, grid, 256, 0, stream, p)
-              : kv4_launch_kernel(fa2_kv4_append_kernel<64, false>, grid, 256, 0, stream, p);
+    return kv4_rows(dev, p.rows, d, [&](auto few, long long grid) {
+        using namespace fa2::kv4;
+        constexpr int P = few ? 1 : 4;
+        if (d == 128)
+            return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<128, true, P>, grid, 256, 0, stream, p)
+                      : kv4_launch_kernel(fa2_kv4_append_kernel<128, false, P>, grid, 256, 0, stream, p);
+        return bf ? kv4_launch_kernel(fa2_kv4_append_kernel<64, true, P>, grid, 256, 0, stream, p)
+                  : kv4_launch_kernel(fa2_kv4_append_kernel<64, false, P>, grid, 256, 0, stream, p);
+    });
 }
 
 fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -872,15 +899,16 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
     p.log2_page = log2_of(page_size);
     p.max_pages = max_pages;
     p.num_pages = num_pages;
-    const int rows_block = d == 128 ? fa2::kv4::Copy<128>::kRows : fa2::kv4::Copy<64>::kRows;
-    const long long grid = (static_cast<long long>(p.rows) + rows_block - 1) / rows_block;
     const bool bf = dtype == FA2_BF16;
-    using namespace fa2::kv4;
-    if (d == 128)
-        return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<128, true>, grid, 256, 0, stream, p)
-                  : kv4_launch_kernel(fa2_kv4_gather_kernel<128, false>, grid, 256, 0, stream, p);
-    return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<64, true>, grid, 256, 0, stream, p)
-              : kv4_launch_kernel(fa2_kv4_gather_kernel<64, false>, grid, 256, 0, stream, p);
+    return kv4_rows(dev, p.rows, d, [&](auto few, long long grid) {
+        using namespace fa2::kv4;
+        constexpr int P = few ? 1 : 4;
+        if (d == 128)
+            return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<128, true, P>, grid, 256, 0, stream, p)
+                      : kv4_launch_kernel(fa2_kv4_gather_kernel<128, false, P>, grid, 256, 0, stream, p);
+        return bf ? kv4_launch_kernel(fa2_kv4_gather_kernel<64, true, P>, grid, 256, 0, stream, p)
+                  : kv4_launch_kernel(fa2_kv4_gather_kernel<64, false, P>, grid, 256, 0, stream, p);
+    });
 }
 
 int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size) {

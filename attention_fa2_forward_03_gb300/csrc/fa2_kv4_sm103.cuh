@@ -97,13 +97,14 @@ struct AppendParams {
 };
 
 // Eight elements a lane, so that a warp's loads and stores are contiguous:
-// 16 bytes of a row, two lanes to a scale. A thread has kPasses rows of keys
-// and of values in flight.
-template <int D>
+// 16 bytes of a row, two lanes to a scale. A thread has P rows of keys and of
+// values in flight: four where there are enough rows, one where that would
+// leave SMs idle.
+template <int D, int P>
 struct Copy {
     static constexpr int kLanes = D / 8;             // lanes of a row
     static constexpr int kRowsPass = 256 / kLanes;
-    static constexpr int kPasses = 4;
+    static constexpr int kPasses = P;
     static constexpr int kRows = kRowsPass * kPasses;   // rows of a block
 };
 
@@ -153,10 +154,10 @@ __device__ __forceinline__ float quotient(float x, float t, float r) {
     return __fmaf_rn(__fmaf_rn(-q, t, x), r, q);
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, int P>
 __global__ void __launch_bounds__(256, 4) fa2_kv4_append_kernel(const AppendParams p) {
     enter_stream_order();
-    using C = Copy<D>;
+    using C = Copy<D, P>;
     const int lane = threadIdx.x % C::kLanes;
     const long long row0 = static_cast<long long>(blockIdx.x) * C::kRows + threadIdx.x / C::kLanes;
     uint4 in[C::kPasses][2];
@@ -264,10 +265,10 @@ struct GatherParams {
 };
 
 // Rows at or past a request's length are zeros.
-template <int D, bool kBf16>
+template <int D, bool kBf16, int P>
 __global__ void __launch_bounds__(256) fa2_kv4_gather_kernel(const GatherParams p) {
     enter_stream_order();
-    using C = Copy<D>;
+    using C = Copy<D, P>;
     const int lane = threadIdx.x % C::kLanes;
     const long long row0 = static_cast<long long>(blockIdx.x) * C::kRows + threadIdx.x / C::kLanes;
     uint32_t codes[C::kPasses][2], scale[C::kPasses][2];
@@ -333,14 +334,15 @@ struct PlanParams {
     int* slots;                // [B, N]
     int* free_state_out;       // {first, count}, may be free_state
     int B, n, max_pages, page, log2_page, num_pages;
+    int in_place;              // outputs are inputs: the grid is one cluster
 };
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanCtas = 8;   // of a cluster, where there is much to write
+constexpr int kPlanCtas = 8;   // of a cluster, where there is much to write in place
 
-// Exclusive prefix sums of (a, r) over the block's threads, and the totals.
+// Exclusive prefix sums of (a, r) over the block's T threads, and the totals.
+template <int T>
 __device__ __forceinline__ void block_scan2(long long& a, long long& r, long long& a_all, long long& r_all,
-                                            long long (*sm)[kPlanThreads / 32]) {
+                                            long long (*sm)[T / 32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long ia = a, ir = r;
 #pragma unroll
@@ -357,18 +359,18 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& r, long lon
     }
     __syncthreads();
     // every warp scans the warps' sums for itself
-    const long long wa = sm[0][lane], wr = sm[1][lane];
+    const long long wa = lane < T / 32 ? sm[0][lane] : 0, wr = lane < T / 32 ? sm[1][lane] : 0;
     long long sa = wa, sr = wr;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < T / 32; o <<= 1) {
         const long long ta = __shfl_up_sync(~0u, sa, o), tr = __shfl_up_sync(~0u, sr, o);
         if (lane >= o) {
             sa += ta;
             sr += tr;
         }
     }
-    a_all = __shfl_sync(~0u, sa, 31);
-    r_all = __shfl_sync(~0u, sr, 31);
+    a_all = __shfl_sync(~0u, sa, T / 32 - 1);
+    r_all = __shfl_sync(~0u, sr, T / 32 - 1);
     a = __shfl_sync(~0u, sa - wa, warp) + ia - a;
     r = __shfl_sync(~0u, sr - wr, warp) + ir - r;
 }
@@ -377,20 +379,20 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One cluster. Every CTA scans the requests in order, 1024 at a time, so that
-// each knows where every request's pages lie in the ring; behind a barrier
-// (the outputs may be the inputs) they share the writing. A request gets its
+// Every CTA scans the requests in order, T at a time, so that
+// each knows where every request's pages lie in the ring; then they share the
+// writing. Where outputs are the inputs the CTAs are one cluster, whose barrier
+// lies between. A request gets its
 // pages iff the pages wanted up to and including it are free (or it needs
 // none); pages of requests that end join the ring behind its last page and are
 // not handed out by this call. Bound by latency: three dependent reads.
-__global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanParams p) {
-    __shared__ long long sm[2][kPlanThreads / 32];
-    __shared__ int s_len[kPlanThreads], s_add[kPlanThreads], s_page[kPlanThreads], s_back[kPlanThreads];
+template <int T>
+__global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
+    __shared__ long long sm[2][T / 32];
+    __shared__ int s_len[T], s_add[T], s_page[T], s_back[T];
     enter_stream_order();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t rank, ranks;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    const uint32_t rank = blockIdx.x, ranks = gridDim.x;
     int first = p.free_state[0], count = p.free_state[1];
     if (first < 0 || first >= p.num_pages || count < 0 || count > p.num_pages) {
         if (tid == 0 && rank == 0) report(kSitePool);
@@ -400,8 +402,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanPa
     const long long room = static_cast<long long>(p.max_pages) << p.log2_page;
     // pages wanted by the requests before this chunk, handed out to them, and returned by them
     long long want = 0, taken = 0, back = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-        const int n = min(kPlanThreads, p.B - b0), b = b0 + tid;
+    for (int b0 = 0; b0 < p.B; b0 += T) {
+        const int n = min(T, p.B - b0), b = b0 + tid;
         int len = 0, add = 0;
         const bool in = tid < n;
         if (in) {
@@ -417,68 +419,84 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanPa
         const int have = (len + p.page - 1) >> p.log2_page;
         const int need = fits ? static_cast<int>((static_cast<long long>(len) + add + p.page - 1) >> p.log2_page) - have : 0;
         long long a = need, r = ends ? have : 0, a_all, r_all;
-        block_scan2(a, r, a_all, r_all, sm);
+        block_scan2<T>(a, r, a_all, r_all, sm);
         const bool granted = fits && (need == 0 || want + a + need <= count);
         s_len[tid] = len;
         s_add[tid] = ends ? -1 : granted ? add : 0;
         s_page[tid] = granted ? static_cast<int>(first + want + a) : 0;   // of its first new page in the ring; < 2 num_pages if it has one
-        s_back[tid] = static_cast<int>((first + static_cast<long long>(count) + back + r) % p.num_pages);
+        long long behind = first + static_cast<long long>(count) + back + r;   // below 3 num_pages in a sane ring
+        if (behind >= p.num_pages) behind -= p.num_pages;
+        if (behind >= p.num_pages) behind -= p.num_pages;
+        if (behind >= p.num_pages) behind %= p.num_pages;
+        s_back[tid] = static_cast<int>(behind);
         // those that got pages are the first of those that wanted any
         taken = want + a_all <= count ? want + a_all : taken;
         const bool cut = want <= count && want + a_all > count;
         if (cut) {
             long long got = granted ? need : 0, none = 0, unused;
             __syncthreads();
-            block_scan2(got, none, taken, unused, sm);
+            block_scan2<T>(got, none, taken, unused, sm);
             taken += want;
         }
         want += a_all;
         back += r_all;
         __syncthreads();
-        cluster_sync();
+        if (p.in_place) cluster_sync();
 
         if (rank == 0 && in) {
             p.seq_lens_out[b] = ends ? 0 : len + (granted ? add : 0);
             p.accepted[b] = granted ? add : 0;
         }
-        // slots, and the table entries of the pages that begin among them
-        auto slot_of = [&](int rb, int i) {
-            if (i >= s_add[rb]) return -1;
-            const int l = s_len[rb], pos = l + i, had = (l + p.page - 1) >> p.log2_page;
-            const int entry = pos >> p.log2_page;
-            int* at = p.block_table + static_cast<long long>(b0 + rb) * p.max_pages + entry;
-            int pg;
-            if (entry < had) {
-                pg = *at;
-            } else {
-                int k = s_page[rb] + entry - had;
-                if (k >= p.num_pages) k -= p.num_pages;
-                pg = p.free_pages[k];
-                if ((pos & (p.page - 1)) == 0) *at = pg;
-            }
-            if (pg >= 0 && pg < p.num_pages) return (pg << p.log2_page) + (pos & (p.page - 1));
-            report(kSitePage);
-            return -1;
-        };
+        // Slots, and the table entries of the pages that begin among them. A
+        // slot's page comes from the table, or from the ring if it is new.
         int* slots = p.slots + static_cast<long long>(b0) * p.n;
+        auto page_at = [&](int rb, int len, int entry) -> const int* {
+            const int had = (len + p.page - 1) >> p.log2_page;
+            if (entry < had) return p.block_table + static_cast<long long>(b0 + rb) * p.max_pages + entry;
+            const int k = s_page[rb] + entry - had;
+            return p.free_pages + (k >= p.num_pages ? k - p.num_pages : k);
+        };
         if (p.n >= 256) {
-            // long rows: a warp takes 256 slots of one request, whose facts stay in registers
+            // Long rows: a warp takes 256 slots of one request. They lie in 17
+            // pages at most, whose ids the lanes read and then pass around.
             const unsigned pieces = (p.n + 255) / 256, all = n * pieces;
-            for (unsigned q = rank * (kPlanThreads / 32) + warp; q < all; q += ranks * (kPlanThreads / 32)) {
-                const int rb = q / pieces, i0 = (q - rb * pieces) * 256;
-                int* to = slots + static_cast<long long>(rb) * p.n;
+            for (unsigned q = rank * (T / 32) + warp; q < all; q += ranks * (T / 32)) {
+                const int rb = q / pieces, i0 = (q - rb * pieces) * 256, got = s_add[rb] - i0, start = s_len[rb] + i0;
+                const int entry0 = start >> p.log2_page;
+                int pg = -1;
+                if (got > 0 && entry0 + lane <= (start + min(got, 256) - 1) >> p.log2_page) {
+                    pg = *page_at(rb, s_len[rb], entry0 + lane);
+                    // a page that begins behind the cached tokens is a new one
+                    if ((entry0 + lane) << p.log2_page >= start)
+                        p.block_table[static_cast<long long>(b0 + rb) * p.max_pages + entry0 + lane] = pg;
+                    if (pg < 0 || pg >= p.num_pages) {
+                        report(kSitePage);
+                        pg = -1;
+                    }
+                }
+                int* to = slots + static_cast<long long>(rb) * p.n + i0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const int i = i0 + j * 32 + lane;
-                    if (i < p.n) to[i] = slot_of(rb, i);
+                    const int i = 32 * j + lane, pos = start + i;
+                    const int page_of = __shfl_sync(~0u, pg, ((pos >> p.log2_page) - entry0) & 31);
+                    if (i0 + i < p.n)
+                        to[i] = i < got && page_of >= 0 ? (page_of << p.log2_page) + (pos & (p.page - 1)) : -1;
                 }
             }
         } else {
             const unsigned total = static_cast<unsigned>(n) * static_cast<unsigned>(p.n);
-            const unsigned stride = ranks * kPlanThreads, sb = stride / p.n, si = stride - sb * p.n;
-            unsigned e = rank * kPlanThreads + tid, rb = e / p.n, i = e - rb * p.n;
+            const unsigned stride = ranks * T, sb = stride / p.n, si = stride - sb * p.n;
+            unsigned e = rank * T + tid, rb = e / p.n, i = e - rb * p.n;
             for (; e < total; e += stride) {
-                slots[e] = slot_of(rb, i);
+                int slot = -1;
+                if (static_cast<int>(i) < s_add[rb]) {
+                    const int pos = s_len[rb] + static_cast<int>(i), off = pos & (p.page - 1), entry = pos >> p.log2_page;
+                    const int pg = *page_at(rb, s_len[rb], entry);
+                    if (off == 0) p.block_table[static_cast<long long>(b0 + rb) * p.max_pages + entry] = pg;
+                    if (pg >= 0 && pg < p.num_pages) slot = (pg << p.log2_page) + off;
+                    else report(kSitePage);
+                }
+                slots[e] = slot;
                 rb += sb;
                 i += si;
                 if (i >= static_cast<unsigned>(p.n)) {
@@ -488,13 +506,32 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanPa
             }
         }
         // pages of requests that end, a warp each
-        if (r_all > 0)
-            for (int q = rank * (kPlanThreads / 32) + warp; q < n; q += ranks * (kPlanThreads / 32))
-                if (s_add[q] < 0) {
+        if (r_all > 0) {
+            unsigned seen = 0, turn = rank * (T / 32) + warp;   // requests that end, so far; the next that is this warp's
+            for (int q0 = 0; q0 < n; q0 += 32) {
+                unsigned who = __ballot_sync(~0u, q0 + lane < n && s_add[min(q0 + lane, T - 1)] < 0);
+                for (; who; who &= who - 1, ++seen) {
+                    if (seen != turn) continue;
+                    turn += ranks * (T / 32);
+                    const int q = q0 + __ffs(who) - 1, have_q = (s_len[q] + p.page - 1) >> p.log2_page;
                     const int* row = p.block_table + static_cast<long long>(b0 + q) * p.max_pages;
-                    for (int j = lane; j < (s_len[q] + p.page - 1) >> p.log2_page; j += 32)
-                        p.free_pages[(static_cast<long long>(s_back[q]) + j) % p.num_pages] = row[j];
+                    for (int j0 = lane; j0 < have_q; j0 += 128) {
+                        int pg[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j0 + 32 * j < have_q) pg[j] = row[j0 + 32 * j];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j0 + 32 * j < have_q) {
+                                int k = s_back[q] + j0 + 32 * j;
+                                if (k >= p.num_pages) k -= p.num_pages;
+                                if (k >= p.num_pages) k %= p.num_pages;   // more pages than there are
+                                p.free_pages[k] = pg[j];
+                            }
+                    }
                 }
+            }
+        }
         __syncthreads();
     }
     if (tid == 0 && rank == 0) {
@@ -503,7 +540,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa2_kv4_plan_kernel(const PlanPa
             report(kSitePool);
             left = p.num_pages;
         }
-        p.free_state_out[0] = static_cast<int>((first + taken) % p.num_pages);
+        p.free_state_out[0] = static_cast<int>(first + taken >= p.num_pages ? first + taken - p.num_pages : first + taken);
         p.free_state_out[1] = static_cast<int>(left);
     }
 }
@@ -1300,19 +1337,24 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
                 if (sm.last) {
                     float* wt = sm.o[0];   // weights of the parts, by row
                     for (int row = warp; row < rows; row += W) {
+                        constexpr int kMost = (kMaxCtas + 31) / 32;   // parts a lane looks at
+                        float2 ml[kMost];
                         float m = -INFINITY, l = 0.0f;
-                        for (int i = lane; i < parts; i += 32) {
+#pragma unroll
+                        for (int k = 0; k < kMost; ++k) {
+                            const int i = lane + 32 * k;
                             const long long at = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
-                            m = fmaxf(m, __ldcg(p.part_ml + at * 2));
+                            ml[k] = i < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2))
+                                              : make_float2(-INFINITY, 0.0f);
+                            m = fmaxf(m, ml[k].x);
                         }
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-                        for (int i = lane; i < parts; i += 32) {
-                            const long long at = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
-                            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2));
-                            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml.x - m);
-                            wt[i * kRows + row] = f;
-                            l = fmaf(f, ml.y, l);
+#pragma unroll
+                        for (int k = 0; k < kMost; ++k) {
+                            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml[k].x - m);
+                            if (lane + 32 * k < parts) wt[(lane + 32 * k) * kRows + row] = f;
+                            l = fmaf(f, ml[k].y, l);
                         }
 #pragma unroll
                         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
@@ -1327,7 +1369,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
                         float4 o = make_float4(0, 0, 0, 0);
                         const float* src = p.part_o + (2LL * c0 * kRows + row) * D + d0;
                         axpy4(o, wt[row], __ldcg(reinterpret_cast<const float4*>(src + kRows * D)));
-#pragma unroll 8
+#pragma unroll 16
                         for (int j = 1; j < parts; ++j)
                             axpy4(o, wt[j * kRows + row], __ldcg(reinterpret_cast<const float4*>(src + 2LL * j * kRows * D)));
                         store_row4<D, kBf16>(p, row0 + row, d0, o, sm.row_ml[row][0], sm.row_ml[row][1], v_descale);

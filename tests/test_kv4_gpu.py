@@ -412,7 +412,7 @@ def test_append_of_values_that_are_not_finite(gpu_lib):
 @pytest.mark.parametrize("B,N,page,W,seed,tight", [
     (1, 1, 16, 4, 0, False), (7, 1, 16, 5, 1, False), (40, 1, 64, 30, 2, True), (300, 1, 16, 8, 3, True),
     (5, 100, 16, 9, 4, False), (33, 257, 32, 20, 5, True), (2100, 3, 16, 3, 6, False), (2100, 3, 16, 3, 7, True),
-    (64, 64, 128, 2, 8, True),
+    (64, 64, 128, 2, 8, True), (20, 1000, 16, 80, 9, False), (70, 515, 64, 12, 10, True), (1100, 300, 128, 5, 11, True),
 ])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_plan(gpu_lib, B, N, page, W, seed, tight, in_place):
