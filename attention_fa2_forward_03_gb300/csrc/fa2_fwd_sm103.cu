@@ -26,6 +26,7 @@
 #include "fa2_fwd_sm103.cuh"
 #include "fa2_fwd_d64_sm103.cuh"
 #include "fa2_kv4_sm103.cuh"
+#include "fa2_kv4_tc_sm103.cuh"
 
 // ==================================================================== host
 
@@ -61,8 +62,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
-// 4-bit cache 20-35.
-constexpr int kKernelSlots = 36;
+// 4-bit cache 20-39.
+constexpr int kKernelSlots = 40;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -677,20 +678,19 @@ fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
     return FA2_OK;
 }
 
-// A pass over the keys serves a row block of 8 NR query rows, NR <= 4 (what
-// the registers hold); more rows are cut into blocks of about equal size.
-int kv4_nr(long long rows) {
-    const long long blocks = (rows + 31) / 32;
-    return static_cast<int>((rows + 8 * blocks - 1) / (8 * blocks));
+// Query rows that a pass over the keys serves: 8 (a kernel on mma.sync), or a
+// multiple of 16 up to 64 (on tcgen05); more rows are cut into blocks of about
+// equal size.
+int kv4_block(long long rows) {
+    if (rows <= 8) return 8;
+    const long long blocks = (rows + 63) / 64;
+    return static_cast<int>((rows + 16 * blocks - 1) / (16 * blocks)) * 16;
 }
-
-constexpr int kv4_ctas_per_sm(int nr) { return nr == 1 ? 2 : 1; }
 
 // The CTAs that can have work: runs have kMinRun tiles or more, and a padded
 // line has at most one run for each segment beyond those.
-long long kv4_ctas(long long B, long long hkv, long long rows, int nr, long long max_tokens, long long most) {
-    const long long segments = B * hkv * ((rows + 8 * nr - 1) / (8 * nr));
-    const long long tiles = (max_tokens + fa2::kv4::kTile - 1) / fa2::kv4::kTile;
+long long kv4_ctas(long long segments, long long max_tokens, long long most) {
+    const long long tiles = (max_tokens + 31) / 32;
     if (segments >= most) return most;
     return std::min(most, segments * (tiles / fa2::kv4::kMinRun + 1));
 }
@@ -698,15 +698,11 @@ long long kv4_ctas(long long B, long long hkv, long long rows, int nr, long long
 // Workspace: two partial results a CTA, then a counter a CTA; nothing where
 // no segment can be split: each gets a CTA of its own (`locate`).
 int64_t kv4_workspace(long long B, long long hkv, long long rows, int d, long long max_tokens) {
-    const int nr = kv4_nr(rows);
-    const long long most = 128 * kv4_ctas_per_sm(nr);   // CTAs that a whole device runs at once
-    const long long segments = B * hkv * ((rows + 8 * nr - 1) / (8 * nr));
-    if (segments <= most &&
-        (max_tokens + fa2::kv4::kTile - 1) / fa2::kv4::kTile <= fa2::kv4::kMinRun + fa2::kv4::kSpare)
-        return 0;
-    return kv4_ctas(B, hkv, rows, nr, max_tokens, fa2::kv4::kMaxCtas) *
-           (2LL * 8 * nr * (d + 2) * static_cast<int64_t>(sizeof(float)) +
-            static_cast<int64_t>(sizeof(unsigned long long)));
+    const int block = kv4_block(rows);
+    const long long segments = B * hkv * ((rows + block - 1) / block);
+    if (segments <= 256 && max_tokens <= 32LL * (fa2::kv4::kMinRun + fa2::kv4::kSpare)) return 0;
+    return kv4_ctas(segments, max_tokens, fa2::kv4::kMaxCtas) *
+           (2LL * block * (d + 2) * static_cast<int64_t>(sizeof(float)) + static_cast<int64_t>(sizeof(unsigned long long)));
 }
 
 // A number that no other launch of this process has, and that memory left
@@ -721,40 +717,44 @@ unsigned long long kv4_nonce() {
     return n;
 }
 
-template <int D, int NR, bool kBf16>
+template <int D, int kRows, bool kBf16>
 fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
-    constexpr int kSmem = static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, NR>));
-    using Shape = fa2::kv4::Shape<NR>;
-    static_assert(Shape::kCtas == kv4_ctas_per_sm(NR), "CTAs an SM");
-    static_assert(Shape::kCtas * (kSmem + 1024) <= 228 * 1024 && kSmem <= 227 * 1024, "shared memory budget");
-    auto kern = fa2::kv4::fa2_kv4_fwd_kernel<D, NR, kBf16>;
-    const int slot = 20 + (D == 128 ? 0 : 8) + 2 * (NR - 1) + (kBf16 ? 0 : 1);
-    const fa2_status st = set_smem(dev, slot, kern, kSmem);
+    constexpr bool kTc = kRows > 8;
+    constexpr int kThreads = kTc ? fa2::kv4::tc::kThreads : fa2::kv4::Shape<1>::kThreads;
+    constexpr int kSmem = [] {
+        if constexpr (kTc) return static_cast<int>(sizeof(fa2::kv4::tc::Smem<D, kRows>)) + 1024;
+        else return static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, 1>));
+    }();
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+    auto kern = [] {
+        if constexpr (kTc) return fa2::kv4::tc::fa2_kv4_fwd_tc_kernel<D, kRows, kBf16>;
+        else return fa2::kv4::fa2_kv4_fwd_kernel<D, 1, kBf16>;
+    }();
+    const fa2_status st = set_smem(dev, 20 + (D == 128 ? 0 : 10) + 2 * (kTc ? kRows / 16 : 0) + (kBf16 ? 0 : 1), kern, kSmem);
     if (st != FA2_OK) return st;
-    p.rblocks = (p.rows + 8 * NR - 1) / (8 * NR);
+    p.rblocks = (p.rows + kRows - 1) / kRows;
     // units of the line are 32-bit, and padding can double them
-    if (static_cast<long long>(p.B) * p.hkv * p.rblocks * ((p.max_tokens + fa2::kv4::kTile - 1LL) / fa2::kv4::kTile) >
-        (1LL << 30))
-        return FA2_ERR_UNSUPPORTED;
-    p.ctas = static_cast<int>(kv4_ctas(p.B, p.hkv, p.rows, NR, p.max_tokens,
-                                       std::min(sm_count(dev) * Shape::kCtas, fa2::kv4::kMaxCtas)));
+    const long long segments = static_cast<long long>(p.B) * p.hkv * p.rblocks;
+    if (segments * ((p.max_tokens + 31LL) / 32) > (1LL << 30)) return FA2_ERR_UNSUPPORTED;
+    p.ctas = static_cast<int>(kv4_ctas(segments, p.max_tokens, std::min(sm_count(dev) * 2, fa2::kv4::kMaxCtas)));
     // Without a workspace every segment needs a CTA, also where they run in waves.
-    if (!p.part_o) p.ctas = std::max(p.ctas, p.B * p.hkv * p.rblocks);
+    if (!p.part_o) p.ctas = std::max(p.ctas, static_cast<int>(segments));
     if (p.part_o) {
-        p.part_ml = p.part_o + 2LL * p.ctas * 8 * NR * D;
-        p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * 8 * NR * 2);
+        p.part_ml = p.part_o + 2LL * p.ctas * kRows * D;
+        p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * kRows * 2);
     }
     p.nonce = kv4_nonce();
-    return kv4_launch_kernel(kern, p.ctas, Shape::kThreads, kSmem, stream, p);
+    return kv4_launch_kernel(kern, p.ctas, kThreads, kSmem, stream, p);
 }
 
 template <int D, bool kBf16>
 fa2_status kv4_launch_rows(int dev, const fa2::kv4::FwdParams& p, cudaStream_t stream) {
-    switch (kv4_nr(p.rows)) {
-        case 1: return kv4_launch<D, 1, kBf16>(dev, p, stream);
-        case 2: return kv4_launch<D, 2, kBf16>(dev, p, stream);
-        case 3: return kv4_launch<D, 3, kBf16>(dev, p, stream);
-        default: return kv4_launch<D, 4, kBf16>(dev, p, stream);
+    switch (kv4_block(p.rows)) {
+        case 8: return kv4_launch<D, 8, kBf16>(dev, p, stream);
+        case 16: return kv4_launch<D, 16, kBf16>(dev, p, stream);
+        case 32: return kv4_launch<D, 32, kBf16>(dev, p, stream);
+        case 48: return kv4_launch<D, 48, kBf16>(dev, p, stream);
+        default: return kv4_launch<D, 64, kBf16>(dev, p, stream);
     }
 }
 
@@ -963,6 +963,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
+    p.wait_limit_ns = g_wait_limit_ns.load();
     p.part = page_size * (d / 2 + d / 16);
     p.page_bytes = H_kv * 2 * p.part;
     p.causal = causal;

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
 
 constexpr int kTile = 32;      // tokens a warp takes at a time
 constexpr int kMaxCtas = 320;  // workspace is sized for this many
-constexpr int kMinRun = 32;    // tiles a CTA's run has at least
+constexpr int kMinRun = 32;    // tiles of 32 a CTA's run has at least
 constexpr int kSpare = 40;     // tiles by which a run may grow so that no segment is split
 
 // Warps a CTA and CTAs an SM by the rows a pass over the keys serves: what
@@ -580,6 +580,7 @@ struct FwdParams {
     int causal;
     int ctas;                  // CTAs that take work
     float scale_log2;
+    long long wait_limit_ns;   // of a wait for the tensor cores
 };
 
 // fp32 accumulators += A (16 x 16, fp16) B (16 x 8, fp16)
@@ -658,7 +659,11 @@ struct Cursor {
 };
 
 __device__ __forceinline__ int length_of(const FwdParams& p, int b) { return min(max(p.seq_lens[b], 0), p.max_tokens); }
-__device__ __forceinline__ int tiles_in(int len) { return (len >> 5) + ((len & 31) != 0); }
+// Tiles of 2^L tokens.
+template <int L>
+__device__ __forceinline__ int tiles_in(int len) {
+    return (len >> L) + ((len & ((1 << L) - 1)) != 0);
+}
 // `tiles` rounded up to whole runs of `pad`, of which there are fewer than
 // 2^20; inv = 1 / pad.
 __device__ __forceinline__ int padded(int tiles, int pad, float inv) {
@@ -681,7 +686,7 @@ __device__ __forceinline__ int warp_scan(int x) {
 
 // The start of this CTA's run; false if it has none. Every warp finds it for
 // itself, a lane looking at its share of the requests: no barrier.
-template <int W>
+template <int W, int L>
 __device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per, int& pad) {
     const int lane = threadIdx.x & 31;
     const int chunk = (p.B + 31) >> 5;
@@ -690,7 +695,7 @@ __device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per
     int mine = 0, longest = 0;
 #pragma unroll 4
     for (int b = b0; b < b1; ++b) {
-        const int t = tiles_in(length_of(p, b));
+        const int t = tiles_in<L>(length_of(p, b));
         mine += t;
         longest = max(longest, t);
     }
@@ -698,17 +703,17 @@ __device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per
     int total = __shfl_sync(~0u, to, 31) * hrs;
     if (total == 0) return false;
     longest = __reduce_max_sync(~0u, longest);
-    per = max((total + p.ctas - 1) / p.ctas, kMinRun);
+    per = max((total + p.ctas - 1) / p.ctas, kMinRun >> (L - 5));
     per = (per + W - 1) / W * W;
     pad = 1;
     float inv = 1.0f;
     if (p.B * hrs <= p.ctas) {
         // Every segment could have a CTA of its own, which is worth a
         // somewhat longer run: nothing to join, no second segment.
-        if (longest <= per + kSpare) per = max(per, (longest + W - 1) / W * W);
+        if (longest <= per + (kSpare >> (L - 5))) per = max(per, (longest + W - 1) / W * W);
         inv = 1.0f / static_cast<float>(per);
         int mine_p = 0;
-        for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in(length_of(p, b)), per, inv);
+        for (int b = b0; b < b1; ++b) mine_p += padded(tiles_in<L>(length_of(p, b)), per, inv);
         const int to_p = warp_scan(mine_p), total_p = __shfl_sync(~0u, to_p, 31) * hrs;
         if (total_p <= p.ctas * per) {
             pad = per;
@@ -726,7 +731,7 @@ __device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per
     if (here) {
         while (true) {
             len = length_of(p, b);
-            const int t = padded(tiles_in(len), pad, inv) * hrs;
+            const int t = padded(tiles_in<L>(len), pad, inv) * hrs;
             if (u < at + t) break;
             at += t;
             ++b;
@@ -737,7 +742,7 @@ __device__ __forceinline__ bool locate(const FwdParams& p, Cursor& cur, int& per
     cur.end = min(total, u + per);
     cur.b = __shfl_sync(~0u, b, from);
     cur.len = __shfl_sync(~0u, len, from);
-    cur.tiles = tiles_in(cur.len);
+    cur.tiles = tiles_in<L>(cur.len);
     const int rem = u - __shfl_sync(~0u, at, from), seg = padded(cur.tiles, pad, inv);
     cur.hr = rem / seg;
     cur.tile = rem - cur.hr * seg;
@@ -751,6 +756,7 @@ __device__ __forceinline__ int part_units(const Cursor& c, int pad) {
 __device__ __forceinline__ int part_tiles(const Cursor& c) { return min(c.end - c.u, c.tiles - c.tile); }
 
 // To the next segment of the run; at its end, to a place without tiles.
+template <int L>
 __device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c, int pad) {
     c.u += part_units(c, pad);
     c.tile = 0;
@@ -760,7 +766,7 @@ __device__ __forceinline__ void next_segment(const FwdParams& p, Cursor& c, int 
         do {
             c.len = length_of(p, ++c.b);
         } while (c.len == 0);
-        c.tiles = tiles_in(c.len);
+        c.tiles = tiles_in<L>(c.len);
     }
 }
 
@@ -1189,6 +1195,78 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
     return static_cast<int>(old & 0xFFFF) + 1;
 }
 
+// Joins the `parts` partial results that CTAs c0, c0 + 1, ... left of a row
+// block, by all T threads of the last CTA. wt: room for `room` weights, of as
+// many parts at a time as there is room for.
+template <int D, int kRows, int T, bool kBf16>
+__device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int room, float (*row_ml)[2], int c0, int parts,
+                                           int rows, long long row0, float v_descale) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int most = room / kRows;
+    // slot of part i: the segment begins in CTA c0, in its second place
+    auto slot = [&](int i) { return 2LL * (c0 + i) + (i == 0 ? 1 : 0); };
+    for (int row = warp; row < rows; row += T / 32) {
+        constexpr int kMost = (kMaxCtas + 31) / 32;   // parts a lane looks at
+        float2 ml[kMost];
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int i = lane + 32 * k;
+            ml[k] = i < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot(i) * kRows + row) * 2))
+                              : make_float2(-INFINITY, 0.0f);
+            m = fmaxf(m, ml[k].x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+#pragma unroll
+        for (int k = 0; k < kMost; ++k) {
+            const int i = lane + 32 * k;
+            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml[k].x - m);
+            if (i < parts && i < most) wt[i * kRows + row] = f;
+            l = fmaf(f, ml[k].y, l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+        if (lane == 0) {
+            row_ml[row][0] = m;
+            row_ml[row][1] = l;
+        }
+    }
+    __syncthreads();
+    constexpr int kItems = (kRows * (D / 4) + T - 1) / T;
+    float4 o[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) o[k] = make_float4(0, 0, 0, 0);
+    for (int j0 = 0; j0 < parts; j0 += most) {
+        const int n = min(most, parts - j0);
+        if (j0 > 0) {
+            __syncthreads();
+            for (int i = tid; i < n * rows; i += T) {
+                const int row = i % rows, part = i / rows;
+                const float m = row_ml[row][0], x = __ldcg(p.part_ml + (slot(j0 + part) * kRows + row) * 2);
+                wt[part * kRows + row] = m == -INFINITY ? 0.0f : ptx::ex2_approx(x - m);
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int i = tid + k * T, row = i / (D / 4), d0 = i % (D / 4) * 4;
+            if (row < rows) {
+                const float* src = p.part_o + (2LL * (c0 + j0) * kRows + row) * D + d0;
+                if (j0 == 0) axpy4(o[k], wt[row], __ldcg(reinterpret_cast<const float4*>(src + kRows * D)));
+#pragma unroll 8
+                for (int j = j0 == 0 ? 1 : 0; j < n; ++j)
+                    axpy4(o[k], wt[j * kRows + row], __ldcg(reinterpret_cast<const float4*>(src + 2LL * j * kRows * D)));
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = tid + k * T, row = i / (D / 4), d0 = i % (D / 4) * 4;
+        if (row < rows) store_row4<D, kBf16>(p, row0 + row, d0, o[k], row_ml[row][0], row_ml[row][1], v_descale);
+    }
+}
+
 template <int D, int NR, bool kBf16>
 __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4_fwd_kernel(const FwdParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -1201,7 +1279,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
     enter_stream_order();
     Cursor cur;
     int per = 0, pad = 1;
-    if (locate<W>(p, cur, per, pad)) {
+    if (locate<W, 5>(p, cur, per, pad)) {
         load_q<D, NR>(p, sm, cur.b, cur.hr);
         float k_descale = p.k_descale[cur.hr / p.rblocks];
         Loader<D, W> ld;
@@ -1231,7 +1309,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
                              : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;
-            next_segment(p, nxt, pad);
+            next_segment<5>(p, nxt, pad);
             const bool more = nxt.u < nxt.end;
             if (more) {
                 load_q<D, NR>(p, sm, nxt.b, nxt.hr);
@@ -1335,45 +1413,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
                 }
                 __syncthreads();
                 if (sm.last) {
-                    float* wt = sm.o[0];   // weights of the parts, by row
-                    for (int row = warp; row < rows; row += W) {
-                        constexpr int kMost = (kMaxCtas + 31) / 32;   // parts a lane looks at
-                        float2 ml[kMost];
-                        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < kMost; ++k) {
-                            const int i = lane + 32 * k;
-                            const long long at = (2LL * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + row;
-                            ml[k] = i < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + at * 2))
-                                              : make_float2(-INFINITY, 0.0f);
-                            m = fmaxf(m, ml[k].x);
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-#pragma unroll
-                        for (int k = 0; k < kMost; ++k) {
-                            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml[k].x - m);
-                            if (lane + 32 * k < parts) wt[(lane + 32 * k) * kRows + row] = f;
-                            l = fmaf(f, ml[k].y, l);
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-                        if (lane == 0) {
-                            sm.row_ml[row][0] = m;
-                            sm.row_ml[row][1] = l;
-                        }
-                    }
-                    __syncthreads();
-                    for (int i = tid; i < rows * (D / 4); i += T) {
-                        const int row = i / (D / 4), d0 = i % (D / 4) * 4;
-                        float4 o = make_float4(0, 0, 0, 0);
-                        const float* src = p.part_o + (2LL * c0 * kRows + row) * D + d0;
-                        axpy4(o, wt[row], __ldcg(reinterpret_cast<const float4*>(src + kRows * D)));
-#pragma unroll 16
-                        for (int j = 1; j < parts; ++j)
-                            axpy4(o, wt[j * kRows + row], __ldcg(reinterpret_cast<const float4*>(src + 2LL * j * kRows * D)));
-                        store_row4<D, kBf16>(p, row0 + row, d0, o, sm.row_ml[row][0], sm.row_ml[row][1], v_descale);
-                    }
+                    join_parts<D, kRows, T, kBf16>(p, sm.o[0], sizeof(sm.o) / 4, sm.row_ml, c0, parts, rows, row0, v_descale);
                     __syncthreads();
                 }
             }

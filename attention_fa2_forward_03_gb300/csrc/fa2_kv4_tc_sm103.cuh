@@ -1,0 +1,608 @@
+// Attention over the 4-bit cache for many query rows a KV head (drafted tokens,
+// large groups, chunks of prompts): both products on tcgen05.
+//
+// Transposed, as in fa2_kv4_sm103.cuh: S^T = K Q^T and O^T += V^T P^T, so that
+// the long axis (128 tokens, 128 elements of d) is the M of the instruction and
+// the few query rows its N (16 to 64). What bounds it is turning codes into
+// fp16, about one instruction an element whatever N is; mma.sync needs the same
+// and, at a quarter of the rate, as much time again for the products of 24 rows.
+//   K   codes -> fp16 in registers -> tensor memory, a thread a token: the A
+//       operand of S^T from there, so that shared memory does not carry it
+//   V   codes -> fp16 -> shared memory [token][d], read as an MN-major A
+//   Q   [row][d] in shared memory, a K-major B
+//   P^T [token][row] in shared memory, an MN-major B
+// A thread holds one token's scores of half the rows, so the maximum of a row
+// runs over threads; it is looked for only when some score passes the row's
+// reference by 2^8 (kTop), as in the other kernel.
+//
+// Two CTAs an SM; in each, the product of one kind runs while the operand of
+// the other is made: V's codes while S^T is computed, the next K's while O^T is.
+#pragma once
+
+#include "fa2_kv4_sm103.cuh"
+
+namespace fa2 {
+namespace kv4 {
+namespace tc {
+
+constexpr int kLog = 7, kTok = 1 << kLog;   // tokens of a tile
+constexpr int kThreads = 256;
+constexpr int kSiteTc = 52;                 // a wait for the tensor cores
+
+// Tensor memory: K (fp16 pairs), S^T, O^T. Two CTAs an SM.
+constexpr uint32_t kColK = 0, kColS = 64, kColO = 128, kCols = 256;
+
+template <int D, int N>
+struct Smem {
+    static constexpr int kCodes = kTok * D / 2, kScales = kTok * D / 16;
+    static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = 2 * kCodes + kScales, kStage = 2 * kCodes + 2 * kScales;
+    alignas(1024) uint8_t v[2][kTok * 128];      // two blocks of 64 elements of d; zeros in the second for D = 64
+    alignas(1024) uint8_t p[kTok * 128];
+    alignas(1024) uint8_t q[D / 64][N * 128];
+    alignas(16) uint8_t code[2][kStage];
+    alignas(16) float2 cref[N];                  // row factor, reference
+    float alpha[N], l[N];
+    float row_ml[N][2];
+    int off[N], mx[N];
+    int nan_first[D / 16];                       // first token with a NaN among its values, by scale group
+    unsigned char ok[2][8];                      // usable 16-token blocks of a stage's tile
+    unsigned long long bar[2], counter;          // products done: S^T, O^T
+    uint32_t tmem;
+    int abort, last;
+};
+
+// Eight columns of the thread's lane of tensor memory, waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// D = A B^T with A from tensor memory (8 columns a step of K = 16) and B
+// K-major in shared memory (32 bytes a step, then the next block of 64):
+// D / 16 steps, the first of which does not accumulate.
+template <int D, uint32_t kBlock>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc) {
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred e, pf, pt;\n\t.reg .b32 blo, bhi, t0, t1;\n\t.reg .b64 b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+            "mov.b64 {blo, bhi}, %2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
+            "add.u32 t0, %1, 8;\n\tadd.u32 t1, blo, 2;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 16;\n\tadd.u32 t1, blo, 4;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 24;\n\tadd.u32 t1, blo, 6;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 32;\n\tadd.u32 t1, blo, %4;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 40;\n\tadd.u32 t1, blo, %5;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 48;\n\tadd.u32 t1, blo, %6;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 56;\n\tadd.u32 t1, blo, %7;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "n"(kBlock), "n"(kBlock + 2), "n"(kBlock + 4),
+            "n"(kBlock + 6)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred e, pf, pt;\n\t.reg .b32 blo, bhi, t0, t1;\n\t.reg .b64 b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+            "mov.b64 {blo, bhi}, %2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
+            "add.u32 t0, %1, 8;\n\tadd.u32 t1, blo, 2;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 16;\n\tadd.u32 t1, blo, 4;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "add.u32 t0, %1, 24;\n\tadd.u32 t1, blo, 6;\n\tmov.b64 b, {t1, bhi};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+            "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc)
+            : "memory");
+    }
+}
+
+// 16-byte piece c of row r of a tile's codes: rows lie one after another, and
+// the pieces are swapped so that eight rows' pieces of one place, which a warp
+// reads at once, lie in different banks.
+template <int D>
+__device__ __forceinline__ int code_at(int r, int c) {
+    if constexpr (D == 128) return r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+    else return r * 32 + ((c ^ ((r >> 2) & 1)) * 16);
+}
+
+// Loads tiles ahead, warp w the tokens 16 w .. 16 w + 15 of each: of one page.
+template <int D, int N>
+struct Loader {
+    using Sm = Smem<D, N>;
+    const uint8_t* codes;      // cache + the head's offset inside a page + the lane's piece of its codes
+    const uint8_t* scales;     // the same for the piece of scales that the lane copies
+    const int* table;          // the request's row
+    uint32_t k_dst, s_dst;     // places of the lane's pieces in a stage
+    int tile, end, len;        // next tile, end of the part, the request's tokens
+    int pg;                    // page of the warp's tokens of it, -1: none
+
+    static constexpr int kPieces = D / 32, kRowsIt = 32 / kPieces;   // pieces of a token's codes, tokens a copy covers
+    static constexpr int kEach = D / 16;                             // pieces of the warp's key scales
+
+    __device__ __forceinline__ void start() {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        k_dst = code_at<D>(16 * warp + lane / kPieces, lane % kPieces);
+        s_dst = (lane >= kEach ? Sm::kVs : Sm::kKs) + warp * D + lane % kEach * 16;
+    }
+    __device__ __forceinline__ void enter(const FwdParams& p, const Cursor& c) {
+        const int lane = threadIdx.x & 31;
+        codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
+        scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;
+        codes += lane * 16;
+        table = p.block_table + static_cast<long long>(c.b) * p.max_pages;
+        len = c.len;
+        tile = c.tile;
+        end = c.tile + part_tiles(c);
+        look(p);
+    }
+    __device__ __forceinline__ void look(const FwdParams& p) {
+        const int at = tile * kTok + (threadIdx.x >> 5) * 16;
+        pg = tile < end && at < len ? table[at >> p.log2_page] : -1;
+    }
+    // Queues the next tile's copies into stage `st`.
+    __device__ __forceinline__ void issue(const FwdParams& p, Sm& sm, int st) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int tok = tile * kTok + warp * 16;
+        const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
+        if (ok) {
+            const uint32_t dst = ptx::smem_addr(sm.code[st]);
+            const int at = tok & (p.page - 1);
+            const long long page = static_cast<long long>(pg) * p.page_bytes;
+            const uint8_t* from = codes + page + at * (D / 2);
+#pragma unroll
+            for (int it = 0; it < 16 / kRowsIt; ++it) {
+                copy16(dst + k_dst + it * 512, from + it * 512);
+                copy16(dst + Sm::kV + k_dst + it * 512, from + p.part + it * 512);
+            }
+            if (lane < 2 * kEach) copy16(dst + s_dst, scales + page + at * (D / 16));
+        } else if (tok < len) {
+            report(kSitePage);
+        }
+        if (lane == 0) sm.ok[st][warp] = ok;
+        ++tile;
+        look(p);
+    }
+};
+
+// A thread's token and half of d: its codes as fp16 pairs in order, D / 4 of
+// them, each multiplied by its scale. nan: groups of 16 whose scale is a NaN,
+// which are read as zeros.
+template <int D, int N>
+__device__ __forceinline__ void decode(uint32_t (&r)[D / 4], uint32_t stage, int part, int tk, int half, bool live, uint32_t& nan) {
+    using Sm = Smem<D, N>;
+    uint32_t w[D / 16], sb;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const uint4 v = lds128(stage + (part ? Sm::kV : 0) + code_at<D>(tk, half * (D / 64) + c));
+        w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+    }
+    const uint32_t sat = stage + (part ? Sm::kVs : Sm::kKs) + tk * (D / 16) + half * (D / 32);
+    sb = D == 128 ? lds32(sat) : lds16(sat);
+    if (!live) sb = 0;
+    nan = 0;
+    if (part) {
+        nan = ((sb & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bytes 0x7F and 0xFF
+        if (nan) sb &= ~((nan >> 7) * 0xFFu);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {   // groups of 16
+        const uint32_t sc = e4m3_to_f16(__byte_perm(sb, 0, i * 0x11));
+        uint32_t a[4], b[4];
+        e2m1_to_f16(w[2 * i], a);
+        e2m1_to_f16(w[2 * i + 1], b);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[8 * i + e] = mul_f16x2(a[e], sc);
+            r[8 * i + 4 + e] = mul_f16x2(b[e], sc);
+        }
+    }
+}
+
+// Keys of a tile into tensor memory: column c of a token's lane holds
+// elements 2c and 2c + 1.
+template <int D, int N>
+__device__ __forceinline__ void put_keys(uint32_t tmem_lane, uint32_t stage, int tk, int half) {
+    uint32_t r[D / 4], nan;
+    decode<D, N>(r, stage, 0, tk, half, true, nan);
+    if constexpr (D == 128) ptx::tmem_st32_at<0>(tmem_lane + kColK + half * 32, r);
+    else ptx::tmem_st16(tmem_lane + kColK + half * 16, r);
+    ptx::tmem_wait_st();
+}
+
+// Values of a tile into shared memory: rows of 64 elements, 128-byte swizzle.
+template <int D, int N>
+__device__ __forceinline__ void put_values(Smem<D, N>& sm, uint32_t stage, int tk, int half, bool live, int pos) {
+    uint32_t r[D / 4], nan;
+    decode<D, N>(r, stage, 1, tk, half, live, nan);
+    if (nan)
+        for (int i = 0; i < D / 32; ++i)
+            if (nan >> (8 * i + 7) & 1) atomicMin(&sm.nan_first[half * (D / 32) + i], pos);
+    const uint32_t row = ptx::smem_addr(sm.v[D == 128 ? half : 0]) + tk * 128;
+    const int c0 = D == 128 ? 0 : half * 4;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+        ptx::st_shared_v4(row + (((c0 + c) ^ (tk & 7)) * 16), r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+}
+
+__device__ __forceinline__ int ordered(float x) {   // order-preserving, for integer maxima
+    const int i = __float_as_int(x);
+    return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+
+// Rows of q as fp16 (scaled as in the other kernel's stage_q), K-major with
+// the 128-byte swizzle, and the rows' factors.
+template <int D, int N, bool kBf16>
+__device__ __forceinline__ void stage_q(const FwdParams& p, Smem<D, N>& sm, const Cursor& c) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3;
+    const int h = c.hr / p.rblocks, r0 = (c.hr - h * p.rblocks) * N;
+    const float c0 = p.scale_log2 * p.k_descale[h];
+    for (int r = warp * 8 + (lane >> 2); r < N; r += kThreads / 4) {
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) w[j] = 0;
+        if (r0 + r < p.rows) {
+            const uint16_t* src = static_cast<const uint16_t*>(p.q) +
+                                  ((static_cast<long long>(c.b) * p.hkv + h) * p.rows + r0 + r) * D + t * (D / 4);
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                const uint4 v = reinterpret_cast<const uint4*>(src)[j];
+                w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+            }
+        }
+        float f = c0;
+        if constexpr (kBf16) {
+            const uint32_t quad = 0xFu << (lane & 28);   // the lanes of this row
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+            top = max(top, __shfl_xor_sync(quad, top, 1));
+            top = max(top, __shfl_xor_sync(quad, top, 2));
+            const int e = static_cast<int>(top >> 7);   // biased exponent of the largest magnitude
+            const int k = e == 255 ? 0 : min(14 + 127 - e, 126);
+            const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+            f *= __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                float lo, hi;
+                ptx::unpack2<true>(w[j], lo, hi);
+                w[j] = ptx::pack2<false>(lo * up, hi * up);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const int piece = t * (D / 32) + j;   // 8 elements
+            ptx::st_shared_v4(ptx::smem_addr(sm.q[piece >> 3]) + r * 128 + (((piece & 7) ^ (r & 7)) * 16), w[4 * j], w[4 * j + 1],
+                              w[4 * j + 2], w[4 * j + 3]);
+        }
+        if (t == 0) {
+            sm.cref[r] = make_float2(f, -INFINITY);
+            sm.off[r] = p.causal && r0 + r < p.rows ? p.nq - 1 - (r0 + r) % p.nq : 0;
+            sm.mx[r] = ordered(-INFINITY);
+        }
+    }
+    if (threadIdx.x < D / 16) sm.nan_first[threadIdx.x] = 0x7FFFFFFF;
+}
+
+template <int D, int N, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using Sm = Smem<D, N>;
+    Sm& sm = *reinterpret_cast<Sm*>(smem + ((1024 - (ptx::smem_addr(smem) & 1023)) & 1023));
+    constexpr int H = N / 2;   // rows a thread works on
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int half = warp >> 2, tk = (warp & 3) * 32 + lane;   // half of d (or of the rows); token, or element of d
+
+    enter_stream_order();
+    Cursor cur;
+    int per = 0, pad = 1;
+    if (locate<1, kLog>(p, cur, per, pad)) {
+        if (tid == 0) {
+            ptx::mbar_init(ptx::smem_addr(&sm.bar[0]), 1);
+            ptx::mbar_init(ptx::smem_addr(&sm.bar[1]), 1);
+            sm.abort = 0;
+            ptx::fence_mbar_init();
+        }
+        if (warp == 0) {
+            ptx::tmem_alloc(ptx::smem_addr(&sm.tmem), kCols);
+            ptx::tmem_relinquish();
+        }
+        if (D == 64)
+            for (int i = tid; i < kTok * 8; i += kThreads) reinterpret_cast<uint4*>(sm.v[1])[i] = make_uint4(0, 0, 0, 0);
+
+        Loader<D, N> ld;
+        ld.start();
+        ld.enter(p, cur);
+        ld.issue(p, sm, 0);
+        copy_commit();
+        ptx::tc_fence_before();
+        __syncthreads();
+        ptx::tc_fence_after();
+        const uint32_t tmem = sm.tmem;
+        const uint32_t lane_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t bar_s = ptx::smem_addr(&sm.bar[0]), bar_o = ptx::smem_addr(&sm.bar[1]);
+        const Waiter wait{&sm.abort, p.wait_limit_ns};
+        const uint64_t qdesc = ptx::desc_sw128(ptx::smem_addr(sm.q[0]), 16, 1024);
+        const uint64_t vdesc = ptx::desc_sw128(ptx::smem_addr(sm.v[0]), kTok * 128, 1024);
+        const uint64_t pdesc = ptx::desc_sw128(ptx::smem_addr(sm.p), kTok * 128, 1024);
+        constexpr uint32_t kIdS = ptx::idesc_f16(0, 0, 0, 128, N), kIdO = ptx::idesc_f16(0, 1, 1, 128, N);
+        uint32_t n_s = 0, n_o = 0, issued_s = 0, issued_o = 0;   // products waited for and issued so far
+        int st = 0;                  // stage of the next tile to work on
+        bool ok = true;
+
+        while (true) {
+            const int n = part_tiles(cur), units = part_units(cur, pad);
+            const int h = cur.hr / p.rblocks, rb = cur.hr - h * p.rblocks;
+            const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
+            const bool split = seg0 < static_cast<int>(blockIdx.x) * per || seg1 > cur.end;
+            const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
+            if (split && tid == 0)   // read ahead; in place when the tiles are done
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.counter)),
+                             "l"(p.arrived + c0)
+                             : "memory");
+            const float v_descale = p.v_descale[h];
+            Cursor nxt = cur;
+            next_segment<kLog>(p, nxt, pad);
+            const bool more = nxt.u < nxt.end;
+            const int low = p.causal ? cur.len - p.nq + 1 : cur.len;   // keys before it are seen by every row
+
+            stage_q<D, N, kBf16>(p, sm, cur);
+            ptx::fence_proxy_async_smem();
+            copy_wait_all();
+            __syncthreads();   // q and the first tile's codes are there
+            put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[st]), tk, half);
+            ptx::tc_fence_before();
+            __syncthreads();
+            if (warp == 0) {
+                ptx::tc_fence_after();
+                mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
+                ptx::tc_commit_elect(bar_s);
+            }
+            ++issued_s;
+            if (n > 1) {
+                ld.issue(p, sm, st ^ 1);
+                copy_commit();
+            }
+            float l[H];
+#pragma unroll
+            for (int j = 0; j < H; ++j) l[j] = 0.0f;
+
+            for (int i = 0; i < n; ++i, st ^= 1) {
+                const int tok0 = (cur.tile + i) * kTok, pos = tok0 + tk;
+                const bool live = pos < cur.len && sm.ok[st][tk >> 4];
+                if (i > 0) {   // the values' place is free when the last product with them is done
+                    ok = wait.wait(bar_o, n_o & 1, kSiteTc) && ok;
+                    ++n_o;
+                }
+                put_values<D, N>(sm, ptx::smem_addr(sm.code[st]), tk, half, live, pos);
+                ok = wait.wait(bar_s, n_s & 1, kSiteTc) && ok;
+                ++n_s;
+                ptx::tc_fence_after();
+
+                // weights of the thread's token for its half of the rows
+                float l2[H];
+                bool up = false;
+                const bool all = __all_sync(~0u, live) && tok0 + kTok <= low;
+                auto weigh = [&](bool check) {
+#pragma unroll
+                    for (int j0 = 0; j0 < H; j0 += 8) {
+                        uint32_t s[8];
+                        tmem_ld8(lane_at + kColS + half * H + j0, s);
+                        float pr[8];
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            const uint4 two = lds128(ptx::smem_addr(&sm.cref[half * H + j0 + j]));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float c = __uint_as_float(e ? two.z : two.x), ref = __uint_as_float(e ? two.w : two.y);
+                                const float x = fmaf(__uint_as_float(s[j + e]), c, -ref);
+                                const bool hide = !all && (!live || pos >= cur.len - sm.off[half * H + j0 + j + e]);
+                                if (check) up = up || (x > kTop && !hide);
+                                pr[j + e] = hide ? 0.0f : ptx::ex2_approx(x);
+                                l2[j0 + j + e] = l[j0 + j + e] + pr[j + e];
+                            }
+                        }
+                        ptx::st_shared_v4(ptx::smem_addr(sm.p) + tk * 128 + ((((half * H + j0) >> 3) ^ (tk & 7)) * 16),
+                                          ptx::pack2<false>(pr[0], pr[1]), ptx::pack2<false>(pr[2], pr[3]),
+                                          ptx::pack2<false>(pr[4], pr[5]), ptx::pack2<false>(pr[6], pr[7]));
+                    }
+                };
+                weigh(true);
+                ptx::fence_proxy_async_smem();
+                ptx::tc_fence_before();
+                copy_wait_all();   // the next tile's codes
+                if (__syncthreads_or(up || !ok)) {
+                    if (*static_cast<volatile int*>(&sm.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    // Rarely: the rows' maxima over the tile, new references, results rescaled.
+#pragma unroll
+                    for (int j0 = 0; j0 < H; j0 += 8) {
+                        uint32_t s[8];
+                        tmem_ld8(lane_at + kColS + half * H + j0, s);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int row = half * H + j0 + j;
+                            const bool hide = !live || pos >= cur.len - sm.off[row];
+                            const float x = __uint_as_float(s[j]);
+                            const int mx = __reduce_max_sync(~0u, ordered(hide || isnan(x) ? -INFINITY : x));
+                            if (lane == 0) atomicMax(&sm.mx[row], mx);
+                        }
+                    }
+                    __syncthreads();
+                    if (tid < N) {
+                        const float2 was = sm.cref[tid];
+                        const float mx = unordered(sm.mx[tid]);
+                        const float ref = mx == -INFINITY ? was.y : fmaxf(was.y, fmaf(mx, was.x, -kLift));
+                        // before a row's first score its sums are 0 and have no reference
+                        sm.alpha[tid] = was.y == -INFINITY ? 1.0f : ptx::ex2_approx(was.y - ref);
+                        sm.cref[tid].y = ref;
+                        sm.mx[tid] = ordered(-INFINITY);
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int j0 = 0; j0 < H; j0 += 8) {
+                        if (i > 0) {
+                            uint32_t o[8];
+                            tmem_ld8(lane_at + kColO + half * H + j0, o);
+    #pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sm.alpha[half * H + j0 + j]);
+                            tmem_st8(lane_at + kColO + half * H + j0, o);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) l[j0 + j] *= sm.alpha[half * H + j0 + j];
+                    }
+                    ptx::tmem_wait_st();
+                    weigh(false);
+                    ptx::fence_proxy_async_smem();
+                    ptx::tc_fence_before();
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int j = 0; j < H; ++j) l[j] = l2[j];
+                if (warp == 0) {
+                    ptx::tc_fence_after();
+                    ptx::mma_ss_kloop<128, 256, 384, 512, 640, 768, 896, 128, 256, 384, 512, 640, 768, 896, 8>(
+                        tmem + kColO, vdesc, pdesc, kIdO, i > 0);
+                    ptx::tc_commit_elect(bar_o);
+                }
+                ++issued_o;
+                if (ld.tile < ld.end) {   // this tile's stage is free
+                    ld.issue(p, sm, st);
+                    copy_commit();
+                }
+                if (i + 1 < n) {
+                    put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[st ^ 1]), tk, half);
+                    ptx::tc_fence_before();
+                    __syncthreads();
+                    if (warp == 0) {
+                        ptx::tc_fence_after();
+                        mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
+                        ptx::tc_commit_elect(bar_s);
+                    }
+                    ++issued_s;
+                }
+            }
+            if (ok) {
+                ok = wait.wait(bar_o, n_o & 1, kSiteTc);
+                ++n_o;
+            }
+            copy_wait_all();
+            if (!__syncthreads_and(ok)) {
+                // a wait ran out: let what is in flight finish, as far as it does
+                if (n_s < issued_s) wait.drain(bar_s, n_s & 1);
+                if (n_o < issued_o) wait.drain(bar_o, n_o & 1);
+                break;
+            }
+            if (more) {   // on their way while this segment's results are written
+                ld.enter(p, nxt);
+                ld.issue(p, sm, st);
+                copy_commit();
+            }
+            ptx::tc_fence_after();
+
+            // Row sums over the tokens: every warp adds up its 32.
+            float* sums = reinterpret_cast<float*>(sm.p);   // [4][N]
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                float x = l[j];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+                if (lane == 0) sums[(warp & 3) * N + half * H + j] = x;
+            }
+            __syncthreads();
+            const long long row0 = (static_cast<long long>(cur.b) * p.hkv + h) * p.rows + rb * N;
+            const int rows = min(N, p.rows - rb * N);
+            const int slot = 2 * blockIdx.x + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+            if (tid < N) {
+                const float sum = (sums[tid] + sums[N + tid]) + (sums[2 * N + tid] + sums[3 * N + tid]);
+                const float ref = sm.cref[tid].y, m = sum == 0.0f ? -INFINITY : ref == -INFINITY ? 0.0f : ref;
+                sm.l[tid] = sum;
+                if (tid < rows) {
+                    if (split)
+                        *reinterpret_cast<float2*>(p.part_ml + (static_cast<long long>(slot) * N + tid) * 2) = make_float2(m, sum);
+                    else
+                        p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+                }
+            }
+            __syncthreads();
+            // O^T: the thread's element of d for its half of the rows
+            const int nan_at = tk < D ? sm.nan_first[min(tk, D - 1) / 16] : 0x7FFFFFFF;
+#pragma unroll
+            for (int j0 = 0; j0 < H; j0 += 8) {
+                uint32_t o[8];
+                tmem_ld8(lane_at + kColO + half * H + j0, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = half * H + j0 + j;
+                    if (row < rows && tk < D) {
+                        float x = __uint_as_float(o[j]);
+                        if (nan_at < cur.len - sm.off[row]) x = NAN;
+                        const float sum = sm.l[row];
+                        if (split) {
+                            p.part_o[(static_cast<long long>(slot) * N + row) * D + tk] = x;
+                        } else {
+                            const uint32_t w = ptx::pack2<kBf16>(sum == 0.0f ? 0.0f : x * (v_descale / sum), 0.0f);
+                            static_cast<uint16_t*>(p.o)[(row0 + row) * D + tk] = static_cast<uint16_t>(w);
+                        }
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncthreads();
+
+            if (split) {
+                const int parts = c1 - c0 + 1;
+                if (tid == 0) {
+                    sm.last = count_in(p.arrived + c0, sm.counter, p.nonce) == parts;
+                    if (sm.last) p.arrived[c0] = 0;
+                }
+                __syncthreads();
+                if (sm.last) {
+                    join_parts<D, N, kThreads, kBf16>(p, reinterpret_cast<float*>(sm.v[0]), sizeof(sm.v[0]) / 4, sm.row_ml, c0,
+                                                      parts, rows, row0, v_descale);
+                    __syncthreads();
+                }
+            }
+            if (!more) break;
+            cur = nxt;
+        }
+        copy_wait_all();
+        ptx::tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            ptx::tc_fence_after();
+            ptx::tmem_dealloc(tmem, kCols);
+        }
+    }
+
+    // Requests without a key: O = 0, LSE = -inf.
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int len = p.seq_lens[b];
+        if (len <= 0) {
+            const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
+            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += kThreads)
+                store_row4<D, kBf16>(p, r0 + i / (D / 4), i % (D / 4) * 4, make_float4(0, 0, 0, 0), 0.0f, 0.0f, 0.0f);
+        } else if (len > p.max_tokens && tid == 0) {
+            report(kSiteLength);
+        }
+    }
+}
+
+}  // namespace tc
+}  // namespace kv4
+}  // namespace fa2
