@@ -62,8 +62,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
-// 4-bit cache 20-39.
-constexpr int kKernelSlots = 40;
+// 4-bit cache 20-43.
+constexpr int kKernelSlots = 44;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -678,14 +678,18 @@ fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
     return FA2_OK;
 }
 
-// Query rows that a pass over the keys serves: 8 (a kernel on mma.sync), or a
-// multiple of 16 up to 64 (on tcgen05); more rows are cut into blocks of about
-// equal size.
+// Query rows that a pass over the keys serves. Up to 24 (8, 16 or 24) by the
+// kernel on mma.sync, beyond by the one on tcgen05 (32, 48 or 64): 38 sequences
+// of 8192 tokens take 64, 92 and 109 us by the first for 8, 16 and 24 rows, 111
+// and 122 us by the second for 16 and 32, where the first takes 138. More than 64
+// rows are cut into blocks of about equal size.
 int kv4_block(long long rows) {
-    if (rows <= 8) return 8;
+    if (rows <= 24) return static_cast<int>((rows + 7) / 8) * 8;
     const long long blocks = (rows + 63) / 64;
-    return static_cast<int>((rows + 16 * blocks - 1) / (16 * blocks)) * 16;
+    return std::max(32, static_cast<int>((rows + 16 * blocks - 1) / (16 * blocks)) * 16);
 }
+constexpr bool kv4_on_tc(int block) { return block > 24; }
+constexpr int kv4_ctas_per_sm(int block) { return block == 8 || kv4_on_tc(block) ? 2 : 1; }
 
 // The CTAs that can have work: runs have kMinRun tiles or more, and a padded
 // line has at most one run for each segment beyond those.
@@ -700,7 +704,8 @@ long long kv4_ctas(long long segments, long long max_tokens, long long most) {
 int64_t kv4_workspace(long long B, long long hkv, long long rows, int d, long long max_tokens) {
     const int block = kv4_block(rows);
     const long long segments = B * hkv * ((rows + block - 1) / block);
-    if (segments <= 256 && max_tokens <= 32LL * (fa2::kv4::kMinRun + fa2::kv4::kSpare)) return 0;
+    // as many CTAs as a whole device runs at once have a segment each
+    if (segments <= 128 * kv4_ctas_per_sm(block) && max_tokens <= 32LL * (fa2::kv4::kMinRun + fa2::kv4::kSpare)) return 0;
     return kv4_ctas(segments, max_tokens, fa2::kv4::kMaxCtas) *
            (2LL * block * (d + 2) * static_cast<int64_t>(sizeof(float)) + static_cast<int64_t>(sizeof(unsigned long long)));
 }
@@ -719,24 +724,29 @@ unsigned long long kv4_nonce() {
 
 template <int D, int kRows, bool kBf16>
 fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
-    constexpr bool kTc = kRows > 8;
-    constexpr int kThreads = kTc ? fa2::kv4::tc::kThreads : fa2::kv4::Shape<1>::kThreads;
+    using namespace fa2::kv4;
+    constexpr bool kTc = kv4_on_tc(kRows);
+    constexpr int NR = kTc ? 1 : kRows / 8;
+    constexpr int kThreads = kTc ? tc::kAll : Shape<NR>::kThreads;
     constexpr int kSmem = [] {
-        if constexpr (kTc) return static_cast<int>(sizeof(fa2::kv4::tc::Smem<D, kRows>)) + 1024;
-        else return static_cast<int>(sizeof(fa2::kv4::FwdSmem<D, 1>));
+        if constexpr (kTc) return static_cast<int>(sizeof(tc::Smem<D, kRows>)) + 1024;
+        else return static_cast<int>(sizeof(FwdSmem<D, NR>));
     }();
-    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs an SM");
+    constexpr int kPerSm = kv4_ctas_per_sm(kRows);
+    static_assert(kTc || kPerSm == Shape<NR>::kCtas, "CTAs an SM");
+    static_assert(kPerSm * (kSmem + 1024) <= 228 * 1024, "shared memory budget");
     auto kern = [] {
-        if constexpr (kTc) return fa2::kv4::tc::fa2_kv4_fwd_tc_kernel<D, kRows, kBf16>;
-        else return fa2::kv4::fa2_kv4_fwd_kernel<D, 1, kBf16>;
+        if constexpr (kTc) return tc::fa2_kv4_fwd_tc_kernel<D, kRows, kBf16>;
+        else return fa2_kv4_fwd_kernel<D, NR, kBf16>;
     }();
-    const fa2_status st = set_smem(dev, 20 + (D == 128 ? 0 : 10) + 2 * (kTc ? kRows / 16 : 0) + (kBf16 ? 0 : 1), kern, kSmem);
+    const int slot = 20 + (D == 128 ? 0 : 12) + 2 * (kTc ? 1 + kRows / 16 : NR - 1) + (kBf16 ? 0 : 1);
+    const fa2_status st = set_smem(dev, slot, kern, kSmem);
     if (st != FA2_OK) return st;
     p.rblocks = (p.rows + kRows - 1) / kRows;
     // units of the line are 32-bit, and padding can double them
     const long long segments = static_cast<long long>(p.B) * p.hkv * p.rblocks;
     if (segments * ((p.max_tokens + 31LL) / 32) > (1LL << 30)) return FA2_ERR_UNSUPPORTED;
-    p.ctas = static_cast<int>(kv4_ctas(segments, p.max_tokens, std::min(sm_count(dev) * 2, fa2::kv4::kMaxCtas)));
+    p.ctas = static_cast<int>(kv4_ctas(segments, p.max_tokens, std::min(sm_count(dev) * kPerSm, fa2::kv4::kMaxCtas)));
     // Without a workspace every segment needs a CTA, also where they run in waves.
     if (!p.part_o) p.ctas = std::max(p.ctas, static_cast<int>(segments));
     if (p.part_o) {
@@ -752,6 +762,7 @@ fa2_status kv4_launch_rows(int dev, const fa2::kv4::FwdParams& p, cudaStream_t s
     switch (kv4_block(p.rows)) {
         case 8: return kv4_launch<D, 8, kBf16>(dev, p, stream);
         case 16: return kv4_launch<D, 16, kBf16>(dev, p, stream);
+        case 24: return kv4_launch<D, 24, kBf16>(dev, p, stream);
         case 32: return kv4_launch<D, 32, kBf16>(dev, p, stream);
         case 48: return kv4_launch<D, 48, kBf16>(dev, p, stream);
         default: return kv4_launch<D, 64, kBf16>(dev, p, stream);

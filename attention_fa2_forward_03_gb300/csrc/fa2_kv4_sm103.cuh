@@ -1196,11 +1196,11 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
 }
 
 // Joins the `parts` partial results that CTAs c0, c0 + 1, ... left of a row
-// block, by all T threads of the last CTA. wt: room for `room` weights, of as
-// many parts at a time as there is room for.
-template <int D, int kRows, int T, bool kBf16>
+// block, by the first T threads of the last CTA, with `sync` as their barrier.
+// wt: room for `room` weights, of as many parts at a time as there is room for.
+template <int D, int kRows, int T, bool kBf16, typename Sync>
 __device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int room, float (*row_ml)[2], int c0, int parts,
-                                           int rows, long long row0, float v_descale) {
+                                           int rows, long long row0, float v_descale, Sync sync) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int most = room / kRows;
     // slot of part i: the segment begins in CTA c0, in its second place
@@ -1232,7 +1232,7 @@ __device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int ro
             row_ml[row][1] = l;
         }
     }
-    __syncthreads();
+    sync();
     constexpr int kItems = (kRows * (D / 4) + T - 1) / T;
     float4 o[kItems];
 #pragma unroll
@@ -1240,13 +1240,13 @@ __device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int ro
     for (int j0 = 0; j0 < parts; j0 += most) {
         const int n = min(most, parts - j0);
         if (j0 > 0) {
-            __syncthreads();
+            sync();
             for (int i = tid; i < n * rows; i += T) {
                 const int row = i % rows, part = i / rows;
                 const float m = row_ml[row][0], x = __ldcg(p.part_ml + (slot(j0 + part) * kRows + row) * 2);
                 wt[part * kRows + row] = m == -INFINITY ? 0.0f : ptx::ex2_approx(x - m);
             }
-            __syncthreads();
+            sync();
         }
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
@@ -1413,7 +1413,8 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
                 }
                 __syncthreads();
                 if (sm.last) {
-                    join_parts<D, kRows, T, kBf16>(p, sm.o[0], sizeof(sm.o) / 4, sm.row_ml, c0, parts, rows, row0, v_descale);
+                    join_parts<D, kRows, T, kBf16>(p, sm.o[0], sizeof(sm.o) / 4, sm.row_ml, c0, parts, rows, row0, v_descale,
+                                                     [] { __syncthreads(); });
                     __syncthreads();
                 }
             }

@@ -15,9 +15,12 @@
 // runs over threads; it is looked for only when some score passes the row's
 // reference by 2^8 (kTop), as in the other kernel.
 //
-// Two CTAs an SM; in each, the product of one kind runs while the operand of
-// the other is made: V's codes while S^T is computed, the next K's while O^T is.
+// Two CTAs an SM; in each eight warps do this work, one issues the products and
+// one the copies. The product of one kind runs while the operand of the other is
+// made: V's codes while S^T is computed, the next K's while O^T is.
 #pragma once
+
+#include <type_traits>
 
 #include "fa2_kv4_sm103.cuh"
 
@@ -26,7 +29,8 @@ namespace kv4 {
 namespace tc {
 
 constexpr int kLog = 7, kTok = 1 << kLog;   // tokens of a tile
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;               // of the eight working warps
+constexpr int kAll = kThreads + 64;         // with the one that issues products and the one that loads
 constexpr int kSiteTc = 52;                 // a wait for the tensor cores
 
 // Tensor memory: K (fp16 pairs), S^T, O^T. Two CTAs an SM.
@@ -40,16 +44,32 @@ struct Smem {
     alignas(1024) uint8_t p[kTok * 128];
     alignas(1024) uint8_t q[D / 64][N * 128];
     alignas(16) uint8_t code[2][kStage];
-    alignas(16) float2 cref[N];                  // row factor, reference
+    alignas(16) float cref[N / 2][4];            // of two rows: factors, negative references
     float alpha[N], l[N];
     float row_ml[N][2];
     int off[N], mx[N];
     int nan_first[D / 16];                       // first token with a NaN among its values, by scale group
-    unsigned char ok[2][8];                      // usable 16-token blocks of a stage's tile
-    unsigned long long bar[2], counter;          // products done: S^T, O^T
+    uint32_t ok[2];                              // usable 16-token blocks of a stage's tile, a bit each
+    unsigned long long bar[8], counter;
     uint32_t tmem;
     int abort, last;
 };
+
+// Barriers: products done, their operands ready, stages of codes full and free.
+enum Bar { kBarS = 0, kBarO = 1, kBarK = 2, kBarP = 3, kBarFull = 4, kBarFree = 6 };
+
+// Barrier of the working warps, and one that also joins a condition.
+__device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool work_sync_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x))
+        : "memory");
+    return r != 0;
+}
 
 // Eight columns of the thread's lane of tensor memory, waited for.
 __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
@@ -118,64 +138,98 @@ __device__ __forceinline__ int code_at(int r, int c) {
     else return r * 32 + ((c ^ ((r >> 2) & 1)) * 16);
 }
 
-// Loads tiles ahead, warp w the tokens 16 w .. 16 w + 15 of each: of one page.
+// The loading warp: the run's tiles one after another into the two stages,
+// 16 tokens (of one page) at a time. Page ids are read while a stage is waited for.
 template <int D, int N>
-struct Loader {
+__device__ __forceinline__ void load_tiles(const FwdParams& p, Smem<D, N>& sm, Cursor c, int pad, const Waiter& wait) {
     using Sm = Smem<D, N>;
-    const uint8_t* codes;      // cache + the head's offset inside a page + the lane's piece of its codes
-    const uint8_t* scales;     // the same for the piece of scales that the lane copies
-    const int* table;          // the request's row
-    uint32_t k_dst, s_dst;     // places of the lane's pieces in a stage
-    int tile, end, len;        // next tile, end of the part, the request's tokens
-    int pg;                    // page of the warp's tokens of it, -1: none
-
-    static constexpr int kPieces = D / 32, kRowsIt = 32 / kPieces;   // pieces of a token's codes, tokens a copy covers
-    static constexpr int kEach = D / 16;                             // pieces of the warp's key scales
-
-    __device__ __forceinline__ void start() {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        k_dst = code_at<D>(16 * warp + lane / kPieces, lane % kPieces);
-        s_dst = (lane >= kEach ? Sm::kVs : Sm::kKs) + warp * D + lane % kEach * 16;
-    }
-    __device__ __forceinline__ void enter(const FwdParams& p, const Cursor& c) {
-        const int lane = threadIdx.x & 31;
-        codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
-        scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;
+    constexpr int kPieces = D / 32, kIts = 16 * kPieces / 32, kEach = D / 16;   // 16-byte pieces of a token's codes, copies of a block's, pieces of its key scales
+    const int lane = threadIdx.x & 31;
+    const uint32_t bars = ptx::smem_addr(sm.bar);
+    const uint32_t k_dst = code_at<D>(lane / kPieces, lane % kPieces);
+    const uint32_t s_dst = (lane >= kEach ? Sm::kVs : Sm::kKs) + lane % kEach * 16;
+    uint32_t k = 0;
+    bool ok = true;
+    while (c.u < c.end && ok) {
+        const uint8_t* codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
+        const uint8_t* scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;
         codes += lane * 16;
-        table = p.block_table + static_cast<long long>(c.b) * p.max_pages;
-        len = c.len;
-        tile = c.tile;
-        end = c.tile + part_tiles(c);
-        look(p);
-    }
-    __device__ __forceinline__ void look(const FwdParams& p) {
-        const int at = tile * kTok + (threadIdx.x >> 5) * 16;
-        pg = tile < end && at < len ? table[at >> p.log2_page] : -1;
-    }
-    // Queues the next tile's copies into stage `st`.
-    __device__ __forceinline__ void issue(const FwdParams& p, Sm& sm, int st) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int tok = tile * kTok + warp * 16;
-        const bool ok = static_cast<unsigned>(pg) < static_cast<unsigned>(p.num_pages);
-        if (ok) {
+        const int* table = p.block_table + static_cast<long long>(c.b) * p.max_pages;
+        const int end = c.tile + part_tiles(c);
+        for (int tile = c.tile; tile < end; ++tile, ++k) {
+            const int st = k & 1, mine = tile * kTok + (lane & 7) * 16;
+            const int id = mine < c.len ? table[mine >> p.log2_page] : -1;
+            const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
+            if (!good && mine < c.len && lane < 8) report(kSitePage);
+            const uint32_t usable = __ballot_sync(~0u, good) & 0xFF;
+            ok = wait.wait(bars + 8 * (kBarFree + st), ((k >> 1) & 1) ^ 1, kSiteTc);
+            if (!__all_sync(~0u, ok)) break;
             const uint32_t dst = ptx::smem_addr(sm.code[st]);
-            const int at = tok & (p.page - 1);
-            const long long page = static_cast<long long>(pg) * p.page_bytes;
-            const uint8_t* from = codes + page + at * (D / 2);
 #pragma unroll
-            for (int it = 0; it < 16 / kRowsIt; ++it) {
-                copy16(dst + k_dst + it * 512, from + it * 512);
-                copy16(dst + Sm::kV + k_dst + it * 512, from + p.part + it * 512);
+            for (int b = 0; b < 8; ++b) {
+                const int pg = __shfl_sync(~0u, id, b);
+                if (!(usable >> b & 1)) continue;
+                const int at = (tile * kTok + b * 16) & (p.page - 1);
+                const long long page = static_cast<long long>(pg) * p.page_bytes;
+                const uint8_t* from = codes + page + at * (D / 2);
+#pragma unroll
+                for (int it = 0; it < kIts; ++it) {
+                    copy16(dst + k_dst + b * (8 * D) + it * 512, from + it * 512);
+                    copy16(dst + Sm::kV + k_dst + b * (8 * D) + it * 512, from + p.part + it * 512);
+                }
+                if (lane < 2 * kEach) copy16(dst + s_dst + b * D, scales + page + at * (D / 16));
             }
-            if (lane < 2 * kEach) copy16(dst + s_dst, scales + page + at * (D / 16));
-        } else if (tok < len) {
-            report(kSitePage);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bars + 8 * (kBarFull + st)) : "memory");
+            if (lane == 0) {
+                sm.ok[st] = usable;
+                ptx::mbar_arrive(bars + 8 * (kBarFull + st));
+            }
         }
-        if (lane == 0) sm.ok[st][warp] = ok;
-        ++tile;
-        look(p);
+        next_segment<kLog>(p, c, pad);
     }
-};
+    copy_wait_all();
+}
+
+// The issuing warp: S^T of a segment's first tile, then O^T of each tile and
+// S^T of the next, as their operands get ready.
+template <int D, int N>
+__device__ __forceinline__ void issue_products(const FwdParams& p, Smem<D, N>& sm, Cursor c, int pad, uint32_t tmem,
+                                               const Waiter& wait) {
+    const uint32_t bars = ptx::smem_addr(sm.bar);
+    const uint64_t qdesc = ptx::desc_sw128(ptx::smem_addr(sm.q[0]), 16, 1024);
+    const uint64_t vdesc = ptx::desc_sw128(ptx::smem_addr(sm.v[0]), kTok * 128, 1024);
+    const uint64_t pdesc = ptx::desc_sw128(ptx::smem_addr(sm.p), kTok * 128, 1024);
+    constexpr uint32_t kIdS = ptx::idesc_f16(0, 0, 0, 128, N), kIdO = ptx::idesc_f16(0, 1, 1, 128, N);
+    uint32_t n_k = 0, n_p = 0;
+    bool ok = true;
+    auto scores = [&] {
+        ok = __all_sync(~0u, wait.wait(bars + 8 * kBarK, n_k & 1, kSiteTc));
+        if (!ok) return;
+        ++n_k;
+        ptx::tc_fence_after();
+        mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
+        ptx::tc_commit_elect(bars + 8 * kBarS);
+    };
+    while (c.u < c.end && ok) {
+        const int n = part_tiles(c);
+        scores();
+        for (int i = 0; i < n && ok; ++i) {
+            ok = __all_sync(~0u, wait.wait(bars + 8 * kBarP, n_p & 1, kSiteTc));
+            if (!ok) break;
+            ++n_p;
+            ptx::tc_fence_after();
+            ptx::mma_ss_kloop<128, 256, 384, 512, 640, 768, 896, 128, 256, 384, 512, 640, 768, 896, 8>(
+                tmem + kColO, vdesc, pdesc, kIdO, i > 0);
+            ptx::tc_commit_elect(bars + 8 * kBarO);
+            if (i + 1 < n) scores();
+        }
+        next_segment<kLog>(p, c, pad);
+    }
+    if (!ok) {   // a wait ran out: let what is in flight finish, as far as it does
+        if (n_k) wait.drain(bars + 8 * kBarS, (n_k - 1) & 1);
+        if (n_p) wait.drain(bars + 8 * kBarO, (n_p - 1) & 1);
+    }
+}
 
 // A thread's token and half of d: its codes as fp16 pairs in order, D / 4 of
 // them, each multiplied by its scale. nan: groups of 16 whose scale is a NaN,
@@ -289,7 +343,8 @@ __device__ __forceinline__ void stage_q(const FwdParams& p, Smem<D, N>& sm, cons
                               w[4 * j + 2], w[4 * j + 3]);
         }
         if (t == 0) {
-            sm.cref[r] = make_float2(f, -INFINITY);
+            sm.cref[r / 2][r & 1] = f;
+            sm.cref[r / 2][2 + (r & 1)] = INFINITY;
             sm.off[r] = p.causal && r0 + r < p.rows ? p.nq - 1 - (r0 + r) % p.nq : 0;
             sm.mx[r] = ordered(-INFINITY);
         }
@@ -298,7 +353,7 @@ __device__ __forceinline__ void stage_q(const FwdParams& p, Smem<D, N>& sm, cons
 }
 
 template <int D, int N, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdParams p) {
+__global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     using Sm = Smem<D, N>;
     Sm& sm = *reinterpret_cast<Sm*>(smem + ((1024 - (ptx::smem_addr(smem) & 1023)) & 1023));
@@ -310,9 +365,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
     Cursor cur;
     int per = 0, pad = 1;
     if (locate<1, kLog>(p, cur, per, pad)) {
+        const uint32_t bars = ptx::smem_addr(sm.bar);
         if (tid == 0) {
-            ptx::mbar_init(ptx::smem_addr(&sm.bar[0]), 1);
-            ptx::mbar_init(ptx::smem_addr(&sm.bar[1]), 1);
+            ptx::mbar_init(bars + 8 * kBarS, 1);
+            ptx::mbar_init(bars + 8 * kBarO, 1);
+            ptx::mbar_init(bars + 8 * kBarK, kThreads / 32);
+            ptx::mbar_init(bars + 8 * kBarP, kThreads / 32);
+            for (int s = 0; s < 2; ++s) {
+                ptx::mbar_init(bars + 8 * (kBarFull + s), 33);   // the lanes' copies, and what they left out
+                ptx::mbar_init(bars + 8 * (kBarFree + s), kThreads / 32);
+            }
             sm.abort = 0;
             ptx::fence_mbar_init();
         }
@@ -321,29 +383,27 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
             ptx::tmem_relinquish();
         }
         if (D == 64)
-            for (int i = tid; i < kTok * 8; i += kThreads) reinterpret_cast<uint4*>(sm.v[1])[i] = make_uint4(0, 0, 0, 0);
-
-        Loader<D, N> ld;
-        ld.start();
-        ld.enter(p, cur);
-        ld.issue(p, sm, 0);
-        copy_commit();
+            for (int i = tid; i < kTok * 8; i += kAll) reinterpret_cast<uint4*>(sm.v[1])[i] = make_uint4(0, 0, 0, 0);
+        ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();
         ptx::tc_fence_after();
         const uint32_t tmem = sm.tmem;
         const uint32_t lane_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint32_t bar_s = ptx::smem_addr(&sm.bar[0]), bar_o = ptx::smem_addr(&sm.bar[1]);
         const Waiter wait{&sm.abort, p.wait_limit_ns};
-        const uint64_t qdesc = ptx::desc_sw128(ptx::smem_addr(sm.q[0]), 16, 1024);
-        const uint64_t vdesc = ptx::desc_sw128(ptx::smem_addr(sm.v[0]), kTok * 128, 1024);
-        const uint64_t pdesc = ptx::desc_sw128(ptx::smem_addr(sm.p), kTok * 128, 1024);
-        constexpr uint32_t kIdS = ptx::idesc_f16(0, 0, 0, 128, N), kIdO = ptx::idesc_f16(0, 1, 1, 128, N);
-        uint32_t n_s = 0, n_o = 0, issued_s = 0, issued_o = 0;   // products waited for and issued so far
-        int st = 0;                  // stage of the next tile to work on
+        uint32_t n_s = 0, n_o = 0;   // products waited for so far
+        uint32_t k = 0;              // tiles so far: the stage of the next, and how often it was used
+        // the token's row of weights; a row's place in it is chosen by exclusive or
+        const uint32_t p_row = ptx::smem_addr(sm.p) + tk * 128 + (tk & 7) * 16;
         bool ok = true;
+        auto arrive = [&](int bar) {   // one arrival a warp, behind all its lanes' writes
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(bars + 8 * bar);
+        };
 
-        while (true) {
+        if (warp == kThreads / 32) issue_products<D, N>(p, sm, cur, pad, tmem, wait);
+        else if (warp > kThreads / 32) load_tiles<D, N>(p, sm, cur, pad, wait);
+        else while (true) {
             const int n = part_tiles(cur), units = part_units(cur, pad);
             const int h = cur.hr / p.rblocks, rb = cur.hr - h * p.rblocks;
             const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
@@ -359,73 +419,87 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
             const bool more = nxt.u < nxt.end;
             const int low = p.causal ? cur.len - p.nq + 1 : cur.len;   // keys before it are seen by every row
 
+            // Keys of the run's k-th tile, as soon as its codes are there
+            auto keys = [&](uint32_t k) {
+                ok = wait.wait(bars + 8 * (kBarFull + (k & 1)), (k >> 1) & 1, kSiteTc) && ok;
+                put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[k & 1]), tk, half);
+                ptx::tc_fence_before();
+                arrive(kBarK);
+            };
             stage_q<D, N, kBf16>(p, sm, cur);
             ptx::fence_proxy_async_smem();
-            copy_wait_all();
-            __syncthreads();   // q and the first tile's codes are there
-            put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[st]), tk, half);
-            ptx::tc_fence_before();
-            __syncthreads();
-            if (warp == 0) {
-                ptx::tc_fence_after();
-                mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
-                ptx::tc_commit_elect(bar_s);
-            }
-            ++issued_s;
-            if (n > 1) {
-                ld.issue(p, sm, st ^ 1);
-                copy_commit();
-            }
-            float l[H];
+            work_sync();   // row factors
+            keys(k);
+            uint64_t l[H / 2];   // the thread's tokens' part of the row sums, two rows a register pair
 #pragma unroll
-            for (int j = 0; j < H; ++j) l[j] = 0.0f;
+            for (int j = 0; j < H / 2; ++j) l[j] = 0;
 
-            for (int i = 0; i < n; ++i, st ^= 1) {
+            for (int i = 0; i < n; ++i, ++k) {
                 const int tok0 = (cur.tile + i) * kTok, pos = tok0 + tk;
-                const bool live = pos < cur.len && sm.ok[st][tk >> 4];
+                const bool live = pos < cur.len && (sm.ok[k & 1] >> (tk >> 4) & 1);
                 if (i > 0) {   // the values' place is free when the last product with them is done
-                    ok = wait.wait(bar_o, n_o & 1, kSiteTc) && ok;
+                    ok = wait.wait(bars + 8 * kBarO, n_o & 1, kSiteTc) && ok;
                     ++n_o;
                 }
-                put_values<D, N>(sm, ptx::smem_addr(sm.code[st]), tk, half, live, pos);
-                ok = wait.wait(bar_s, n_s & 1, kSiteTc) && ok;
+                put_values<D, N>(sm, ptx::smem_addr(sm.code[k & 1]), tk, half, live, pos);
+                arrive(kBarFree + (k & 1));
+                ok = wait.wait(bars + 8 * kBarS, n_s & 1, kSiteTc) && ok;
                 ++n_s;
                 ptx::tc_fence_after();
 
-                // weights of the thread's token for its half of the rows
-                float l2[H];
-                bool up = false;
-                const bool all = __all_sync(~0u, live) && tok0 + kTok <= low;
-                auto weigh = [&](bool check) {
+                // The thread's token and its half of the rows: exponents, then
+                // weights, which go to shared memory and into the row sums.
+                uint64_t x[H / 2];
+                auto exponents = [&](auto masked) {
+                    float top = -INFINITY;
 #pragma unroll
                     for (int j0 = 0; j0 < H; j0 += 8) {
                         uint32_t s[8];
                         tmem_ld8(lane_at + kColS + half * H + j0, s);
-                        float pr[8];
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) {
-                            const uint4 two = lds128(ptx::smem_addr(&sm.cref[half * H + j0 + j]));
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float c = __uint_as_float(e ? two.z : two.x), ref = __uint_as_float(e ? two.w : two.y);
-                                const float x = fmaf(__uint_as_float(s[j + e]), c, -ref);
-                                const bool hide = !all && (!live || pos >= cur.len - sm.off[half * H + j0 + j + e]);
-                                if (check) up = up || (x > kTop && !hide);
-                                pr[j + e] = hide ? 0.0f : ptx::ex2_approx(x);
-                                l2[j0 + j + e] = l[j0 + j + e] + pr[j + e];
+                            const int row = half * H + j0 + j;
+                            const uint4 cr = lds128(ptx::smem_addr(sm.cref[row / 2]));
+                            uint64_t x2 = ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+                                                      ptx::f2_pack(__uint_as_float(cr.x), __uint_as_float(cr.y)),
+                                                      ptx::f2_pack(__uint_as_float(cr.z), __uint_as_float(cr.w)));
+                            float x0, x1;
+                            ptx::f2_unpack(x2, x0, x1);
+                            if constexpr (decltype(masked)::value) {
+                                if (!live || pos >= cur.len - sm.off[row]) x0 = -INFINITY;
+                                if (!live || pos >= cur.len - sm.off[row + 1]) x1 = -INFINITY;
+                                x2 = ptx::f2_pack(x0, x1);
                             }
+                            top = ptx::max3(top, x0, x1);
+                            x[(j0 + j) / 2] = x2;
                         }
-                        ptx::st_shared_v4(ptx::smem_addr(sm.p) + tk * 128 + ((((half * H + j0) >> 3) ^ (tk & 7)) * 16),
-                                          ptx::pack2<false>(pr[0], pr[1]), ptx::pack2<false>(pr[2], pr[3]),
-                                          ptx::pack2<false>(pr[4], pr[5]), ptx::pack2<false>(pr[6], pr[7]));
+                    }
+                    return top;
+                };
+                auto weights = [&](bool add) {
+#pragma unroll
+                    for (int j0 = 0; j0 < H; j0 += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float p0, p1;
+                            ptx::f2_unpack(x[j0 / 2 + j], p0, p1);
+                            p0 = ptx::ex2_approx(p0);
+                            p1 = ptx::ex2_approx(p1);
+                            w[j] = ptx::pack2<false>(p0, p1);
+                            if (add) l[j0 / 2 + j] = ptx::f2_add(l[j0 / 2 + j], ptx::f2_pack(p0, p1));
+                        }
+                        ptx::st_shared_v4(p_row ^ ((half * H + j0) * 2), w[0], w[1], w[2], w[3]);
                     }
                 };
-                weigh(true);
+                const bool all = __all_sync(~0u, live) && tok0 + kTok <= low;
+                const float top = all ? exponents(std::false_type{}) : exponents(std::true_type{});
+                const bool up = __any_sync(~0u, top > kTop);
+                weights(!up);   // those past the reference may be infinite, and are done again
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before();
-                copy_wait_all();   // the next tile's codes
-                if (__syncthreads_or(up || !ok)) {
-                    if (*static_cast<volatile int*>(&sm.abort)) {
+                if (work_sync_or(up || !ok)) {
+                    if (work_sync_or(*static_cast<volatile int*>(&sm.abort) != 0)) {   // all or none
                         ok = false;
                         break;
                     }
@@ -438,99 +512,77 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
                         for (int j = 0; j < 8; ++j) {
                             const int row = half * H + j0 + j;
                             const bool hide = !live || pos >= cur.len - sm.off[row];
-                            const float x = __uint_as_float(s[j]);
-                            const int mx = __reduce_max_sync(~0u, ordered(hide || isnan(x) ? -INFINITY : x));
+                            const float v = __uint_as_float(s[j]);
+                            const int mx = __reduce_max_sync(~0u, ordered(hide || isnan(v) ? -INFINITY : v));
                             if (lane == 0) atomicMax(&sm.mx[row], mx);
                         }
                     }
-                    __syncthreads();
+                    work_sync();
                     if (tid < N) {
-                        const float2 was = sm.cref[tid];
-                        const float mx = unordered(sm.mx[tid]);
-                        const float ref = mx == -INFINITY ? was.y : fmaxf(was.y, fmaf(mx, was.x, -kLift));
+                        float* cr = sm.cref[tid / 2] + (tid & 1);
+                        const float was = -cr[2], mx = unordered(sm.mx[tid]);
+                        const float ref = mx == -INFINITY ? was : fmaxf(was, fmaf(mx, cr[0], -kLift));
                         // before a row's first score its sums are 0 and have no reference
-                        sm.alpha[tid] = was.y == -INFINITY ? 1.0f : ptx::ex2_approx(was.y - ref);
-                        sm.cref[tid].y = ref;
+                        sm.alpha[tid] = was == -INFINITY ? 1.0f : ptx::ex2_approx(was - ref);
+                        cr[2] = -ref;
                         sm.mx[tid] = ordered(-INFINITY);
                     }
-                    __syncthreads();
+                    work_sync();
 #pragma unroll
                     for (int j0 = 0; j0 < H; j0 += 8) {
                         if (i > 0) {
                             uint32_t o[8];
                             tmem_ld8(lane_at + kColO + half * H + j0, o);
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sm.alpha[half * H + j0 + j]);
                             tmem_st8(lane_at + kColO + half * H + j0, o);
                         }
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) l[j0 + j] *= sm.alpha[half * H + j0 + j];
+                        for (int j = 0; j < 8; j += 2)
+                            l[(j0 + j) / 2] = ptx::f2_mul(l[(j0 + j) / 2], ptx::f2_pack(sm.alpha[half * H + j0 + j], sm.alpha[half * H + j0 + j + 1]));
                     }
                     ptx::tmem_wait_st();
-                    weigh(false);
+                    // What a warp without such a score added is right after the rescaling.
+                    exponents(std::true_type{});
+                    weights(up);
                     ptx::fence_proxy_async_smem();
                     ptx::tc_fence_before();
-                    __syncthreads();
+                    work_sync();
                 }
-#pragma unroll
-                for (int j = 0; j < H; ++j) l[j] = l2[j];
-                if (warp == 0) {
-                    ptx::tc_fence_after();
-                    ptx::mma_ss_kloop<128, 256, 384, 512, 640, 768, 896, 128, 256, 384, 512, 640, 768, 896, 8>(
-                        tmem + kColO, vdesc, pdesc, kIdO, i > 0);
-                    ptx::tc_commit_elect(bar_o);
-                }
-                ++issued_o;
-                if (ld.tile < ld.end) {   // this tile's stage is free
-                    ld.issue(p, sm, st);
-                    copy_commit();
-                }
-                if (i + 1 < n) {
-                    put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[st ^ 1]), tk, half);
-                    ptx::tc_fence_before();
-                    __syncthreads();
-                    if (warp == 0) {
-                        ptx::tc_fence_after();
-                        mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
-                        ptx::tc_commit_elect(bar_s);
-                    }
-                    ++issued_s;
-                }
+                arrive(kBarP);
+                if (i + 1 < n) keys(k + 1);
             }
             if (ok) {
-                ok = wait.wait(bar_o, n_o & 1, kSiteTc);
+                ok = wait.wait(bars + 8 * kBarO, n_o & 1, kSiteTc);
                 ++n_o;
             }
-            copy_wait_all();
-            if (!__syncthreads_and(ok)) {
-                // a wait ran out: let what is in flight finish, as far as it does
-                if (n_s < issued_s) wait.drain(bar_s, n_s & 1);
-                if (n_o < issued_o) wait.drain(bar_o, n_o & 1);
-                break;
-            }
-            if (more) {   // on their way while this segment's results are written
-                ld.enter(p, nxt);
-                ld.issue(p, sm, st);
-                copy_commit();
-            }
+            copy_wait_all();   // the segment's counter
+            if (work_sync_or(!ok)) break;
             ptx::tc_fence_after();
 
             // Row sums over the tokens: every warp adds up its 32.
             float* sums = reinterpret_cast<float*>(sm.p);   // [4][N]
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                float x = l[j];
+            for (int j = 0; j < H / 2; ++j) {
+                float x0, x1;
+                ptx::f2_unpack(l[j], x0, x1);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
-                if (lane == 0) sums[(warp & 3) * N + half * H + j] = x;
+                for (int o = 16; o > 0; o >>= 1) {
+                    x0 += __shfl_xor_sync(~0u, x0, o);
+                    x1 += __shfl_xor_sync(~0u, x1, o);
+                }
+                if (lane == 0) {
+                    sums[(warp & 3) * N + half * H + 2 * j] = x0;
+                    sums[(warp & 3) * N + half * H + 2 * j + 1] = x1;
+                }
             }
-            __syncthreads();
+            work_sync();
             const long long row0 = (static_cast<long long>(cur.b) * p.hkv + h) * p.rows + rb * N;
             const int rows = min(N, p.rows - rb * N);
             const int slot = 2 * blockIdx.x + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
             if (tid < N) {
                 const float sum = (sums[tid] + sums[N + tid]) + (sums[2 * N + tid] + sums[3 * N + tid]);
-                const float ref = sm.cref[tid].y, m = sum == 0.0f ? -INFINITY : ref == -INFINITY ? 0.0f : ref;
+                const float ref = -sm.cref[tid / 2][2 + (tid & 1)], m = sum == 0.0f ? -INFINITY : ref == -INFINITY ? 0.0f : ref;
                 sm.l[tid] = sum;
                 if (tid < rows) {
                     if (split)
@@ -539,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
                         p.lse[row0 + tid] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
                 }
             }
-            __syncthreads();
+            work_sync();
             // O^T: the thread's element of d for its half of the rows
             const int nan_at = tk < D ? sm.nan_first[min(tk, D - 1) / 16] : 0x7FFFFFFF;
 #pragma unroll
@@ -563,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
                 }
             }
             ptx::tc_fence_before();
-            __syncthreads();
+            work_sync();
 
             if (split) {
                 const int parts = c1 - c0 + 1;
@@ -571,17 +623,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
                     sm.last = count_in(p.arrived + c0, sm.counter, p.nonce) == parts;
                     if (sm.last) p.arrived[c0] = 0;
                 }
-                __syncthreads();
+                work_sync();
                 if (sm.last) {
                     join_parts<D, N, kThreads, kBf16>(p, reinterpret_cast<float*>(sm.v[0]), sizeof(sm.v[0]) / 4, sm.row_ml, c0,
-                                                      parts, rows, row0, v_descale);
-                    __syncthreads();
+                                                      parts, rows, row0, v_descale, [] { work_sync(); });
+                    work_sync();
                 }
             }
             if (!more) break;
             cur = nxt;
         }
-        copy_wait_all();
         ptx::tc_fence_before();
         __syncthreads();
         if (warp == 0) {
@@ -595,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_kv4_fwd_tc_kernel(const FwdPa
         const int len = p.seq_lens[b];
         if (len <= 0) {
             const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
-            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += kThreads)
+            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += kAll)
                 store_row4<D, kBf16>(p, r0 + i / (D / 4), i % (D / 4) * 4, make_float4(0, 0, 0, 0), 0.0f, 0.0f, 0.0f);
         } else if (len > p.max_tokens && tid == 0) {
             report(kSiteLength);
