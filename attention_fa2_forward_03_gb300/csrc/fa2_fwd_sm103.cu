@@ -975,6 +975,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
     p.wait_limit_ns = g_wait_limit_ns.load();
+    p.debug_flags = g_debug_flags.load();
     p.part = page_size * (d / 2 + d / 16);
     p.page_bytes = H_kv * 2 * p.part;
     p.causal = causal;

@@ -581,6 +581,7 @@ struct FwdParams {
     int ctas;                  // CTAs that take work
     float scale_log2;
     long long wait_limit_ns;   // of a wait for the tensor cores
+    int debug_flags;
 };
 
 // fp32 accumulators += A (16 x 16, fp16) B (16 x 8, fp16)

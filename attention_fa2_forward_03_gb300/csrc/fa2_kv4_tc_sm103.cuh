@@ -149,7 +149,7 @@ __device__ __forceinline__ void load_tiles(const FwdParams& p, Smem<D, N>& sm, C
     const uint32_t k_dst = code_at<D>(lane / kPieces, lane % kPieces);
     const uint32_t s_dst = (lane >= kEach ? Sm::kVs : Sm::kKs) + lane % kEach * 16;
     uint32_t k = 0;
-    bool ok = true;
+    bool ok = !(p.debug_flags & 1);   // test hook: nothing is loaded, and the waits run out
     while (c.u < c.end && ok) {
         const uint8_t* codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
         const uint8_t* scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;

@@ -9,7 +9,6 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -83,17 +82,29 @@ c10::DeviceIndex device_of(const Tensor& t, const char* name) {
     return t.device().index();
 }
 
-// The stream of a call: the device's current one for None, else a
-// torch.cuda.Stream or a handle.
-cudaStream_t stream_of(PyObject* o, c10::DeviceIndex index) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
-    PyObject* h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Raised{};
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Raised{};
-    return static_cast<cudaStream_t>(p);
-}
+// The device and stream of a call: the device's current stream for None, else
+// a torch.cuda.Stream or a handle. Both are current while this lives, so what
+// is allocated belongs to the stream that writes it.
+struct On {
+    c10::cuda::CUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    cudaStream_t stream;
+    On(PyObject* o, c10::DeviceIndex index) : device(index) {
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream(index).stream();
+            return;
+        }
+        PyObject* h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+        if (!h) throw Raised{};
+        void* p = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!p && PyErr_Occurred()) throw Raised{};
+        stream = static_cast<cudaStream_t>(p);
+        // 0, 1 and 2 are CUDA's names for its default streams, not addresses
+        guard.reset_stream(reinterpret_cast<uintptr_t>(p) > 2 ? c10::cuda::getStreamFromExternal(stream, index)
+                                                              : c10::cuda::getDefaultCUDAStream(index));
+    }
+};
 
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, c10::DeviceIndex index) {
     return Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, index), std::nullopt));
@@ -163,6 +174,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const c10::DeviceIndex index = device_of(lens, "seq_lens");
         const int64_t B = table.size(0);
         const auto i32 = at::kInt;
+        const On on(a[11], index);
         want(lens, "seq_lens", index, i32, "[B]", is(lens, {B}));
         want(add, "new_lens", index, i32, "[B]", is(add, {B}));
         want(table, "block_table", index, i32, "[B, max_pages]", true);
@@ -177,12 +189,10 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Tensor lens_out = out(a[7], "seq_lens_out", "[B]", {B}), accepted = out(a[8], "accepted", "[B]", {B}),
                      slots = out(a[9], "slots", "[B, N]", {B, std::max(N, 0)}),
                      state_out = out(a[10], "free_state_out", "[2]", {2});
-        const c10::cuda::CUDAGuard on(index);
         const fa2_status rc = g_plan(ptr<int32_t>(lens), ptr<int32_t>(add), ptr<int32_t>(table), ptr<int32_t>(ring),
                                      ptr<int32_t>(state), ptr<int32_t>(lens_out), ptr<int32_t>(accepted),
                                      ptr<int32_t>(slots), ptr<int32_t>(state_out), int32(B, "B"), N,
-                                     int32(table.size(1), "max_pages"), page, int32(ring.size(0), "num_pages"),
-                                     stream_of(a[11], index));
+                                     int32(table.size(1), "max_pages"), page, int32(ring.size(0), "num_pages"), on.stream);
         if (rc != FA2_OK) return PyLong_FromLong(rc);
         return give({&lens_out, &accepted, &slots, &state_out});
     });
@@ -201,13 +211,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t B = k.size(0), H = k.size(1), N = k.size(2), d = k.size(3);
         const Cache c(cache, kd, vd, index, H, d);
         want(slots, "slots", index, at::kInt, "[B, N]", is(slots, {B, N}));
+        const On on(a[6], index);
         // the stride of an axis of length 1 is never used and may be anything
         auto st = [](const Tensor& t, int i) { return t.size(i) > 1 ? t.stride(i) : 0; };
-        const c10::cuda::CUDAGuard on(index);
         const fa2_status rc = g_append(k.data_ptr(), v.data_ptr(), ptr<int32_t>(slots), cache.data_ptr(), ptr<float>(kd),
                                        ptr<float>(vd), int32(B, "B"), c.heads, int32(N, "N"), int32(d, "d"), st(k, 0),
                                        st(k, 1), st(k, 2), st(v, 0), st(v, 1), st(v, 2), c.page_size, c.pages,
-                                       dtype_code(k.scalar_type()), stream_of(a[6], index));
+                                       dtype_code(k.scalar_type()), on.stream);
         if (rc != FA2_OK) return PyLong_FromLong(rc);
         return Py_NewRef(a[3]);
     });
@@ -238,6 +248,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
             type = reinterpret_cast<THPDtype*>(a[8])->scalar_type;
         }
         const fa2_dtype code = dtype_code(type);
+        const On on(a[11], index);
         auto out = [&](PyObject* o, const char* name) {
             const std::array<int64_t, 4> shape = {B, c.heads, N, d};
             if (o == Py_None) return fresh(shape, type, index);
@@ -246,11 +257,9 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return t;
         };
         const Tensor k = out(a[9], "k"), v = out(a[10], "v");
-        const c10::cuda::CUDAGuard on(index);
         const fa2_status rc = g_gather(cache.data_ptr(), ptr<int32_t>(table), ptr<int32_t>(lens), starts, ptr<float>(kd),
                                        ptr<float>(vd), k.data_ptr(), v.data_ptr(), int32(B, "B"), c.heads, N, d,
-                                       int32(table.size(1), "max_pages"), c.page_size, c.pages, code,
-                                       stream_of(a[11], index));
+                                       int32(table.size(1), "max_pages"), c.page_size, c.pages, code, on.stream);
         if (rc != FA2_OK) return PyLong_FromLong(rc);
         return give({&k, &v});
     });
@@ -270,6 +279,7 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Cache c(cache, kd, vd, index, -1, d);
         want(table, "block_table", index, at::kInt, "[B, max_pages]", table.size(0) == B);
         want(lens, "seq_lens", index, at::kInt, "[B]", is(lens, {B}));
+        const On on(a[11], index);
         Tensor o, lse, ws;
         if (a[6] == Py_None) {
             o = fresh(q.sizes(), q.scalar_type(), index);
@@ -290,7 +300,6 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const int causal = PyObject_IsTrue(a[10]);
         if (causal < 0) throw Raised{};
-        const cudaStream_t stream = stream_of(a[11], index);
         const int b = int32(B, "B"), hq = int32(H, "H_q"), nq = int32(N, "N_q"), dd = int32(d, "d"),
                   pages = int32(table.size(1), "max_pages");
         int64_t bytes = 0;
@@ -300,16 +309,12 @@ PyObject* fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 refuse("workspace must be a contiguous tensor on q's device");
             bytes = static_cast<int64_t>(ws.nbytes());
         } else if ((bytes = g_workspace(b, hq, c.heads, nq, dd, pages, c.page_size)) > 0) {
-            ws = fresh({bytes}, at::kByte, index);
-            if (a[11] != Py_None)   // freed below while `stream` may still use it
-                c10::cuda::CUDACachingAllocator::recordStream(ws.storage().data_ptr(),
-                                                              c10::cuda::getStreamFromExternal(stream, index));
+            ws = fresh({bytes}, at::kByte, index);   // given back to `on`'s stream behind the call
         }
-        const c10::cuda::CUDAGuard on(index);
         const fa2_status rc = g_fwd(q.data_ptr(), cache.data_ptr(), ptr<int32_t>(table), ptr<int32_t>(lens), ptr<float>(kd),
                                     ptr<float>(vd), o.data_ptr(), ptr<float>(lse), ws.defined() ? ws.data_ptr() : nullptr,
                                     bytes, b, hq, c.heads, nq, dd, pages, c.page_size, c.pages,
-                                    static_cast<float>(scale), causal, code, stream);
+                                    static_cast<float>(scale), causal, code, on.stream);
         if (rc != FA2_OK) return PyLong_FromLong(rc);
         return give({&o, &lse});
     });

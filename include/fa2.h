@@ -328,9 +328,9 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
  *   workspace : device, fa2_fwd_kv4_workspace(...) bytes (may be NULL for 0),
  *              contents irrelevant before and after; calls that may overlap
  *              need their own
- * Any N_q >= 1 is right; the kernel is made for few rows a KV head
- * (H_q / H_kv * N_q up to 32 read the cache once, every 32 more once again).
- * Prompts and their chunks are faster by fa2_kv4_gather and fa2_fwd_ex.
+ * Any N_q >= 1 is right. Up to 64 query rows a KV head (H_q / H_kv * N_q) read
+ * the cache once, every 64 more once again; prompts and long chunks of them are
+ * faster by fa2_kv4_gather and fa2_fwd_ex.
  * Query rows hold no precision less than q's own; the softmax weights are
  * rounded to fp16 (2^-11), sums are fp32. A row of q that is not finite
  * affects no other row. A NaN in the cache affects the rows that see it.
@@ -376,8 +376,9 @@ int64_t fa2_set_wait_limit_ns(int64_t limit_ns);
 
 /*
  * Test hook for the watchdog. With flags = 1 the next 16-bit forward kernels
- * and the backward's dK/dV kernel skip the load of their query tiles, so
- * their waits run out and the status word reports
+ * and the backward's dK/dV kernel skip the load of their query tiles, and the
+ * KV cache's kernel for more than 24 query rows that of its keys, so their
+ * waits run out and the status word reports
  * FA2_ERR_TIMEOUT; the kernel still frees its tensor memory, waits for its
  * own copies and returns normally. 0 (the default) restores normal
  * operation. Returns the previous flags.

@@ -23,6 +23,10 @@ from oracle import kv4
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 U = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+# fp16 results below 2^-14 are multiples of 2^-24, half a step of which is
+# 2^-25: more than U of them. Two keys one of which has almost all the weight
+# give such elements where that one's value is 0.
+SUB = {"bf16": 0.0, "fp16": 2.0 ** -25}
 
 
 def ok(fa2):
@@ -74,7 +78,7 @@ def check_attention(o, lse, q, keys, values, scale, causal, lens, dtype):
     full = ~empty
     e = (d + 8) * 2.0 ** -23 * big + 4 * 2.0 ** -23 * np.abs(np.where(full, lref, 0)) + 2.0 ** -21
     r = np.broadcast_to((n / 8 + 64) * 2.0 ** -23, big.shape)
-    bound = (2.0 ** -11 + 2 * e + r)[..., None] * A + 2.0 ** -32 * n[..., None] * vmax + U[dtype] * np.abs(ref)
+    bound = (2.0 ** -11 + 2 * e + r)[..., None] * A + 2.0 ** -32 * n[..., None] * vmax + U[dtype] * np.abs(ref) + SUB[dtype]
     err = np.abs(o - ref)
     assert np.all(err[full] <= bound[full]), f"O off by {(err[full] / np.maximum(bound[full], 1e-300)).max():.3g} bounds"
     lb = e + r + 2.0 ** -22 * np.abs(np.where(full, lref, 0))
@@ -679,4 +683,243 @@ def test_refusals_on_the_device(gpu_lib):
               (torch.zeros(1, 2, 3, 72, dtype=torch.bfloat16, device=dev)[..., 4:68],) * 2 + (slots,)):
         with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
             fa2.fa2_kv4_append(*a, cache, ds, ds)
+    ok(fa2)
+
+
+# ------------------------------------------------------------------ many query rows a KV head
+
+ROWS = [  # Hq, Hkv, Nq: 12 to 24 rows a head in one pass of mma.sync, above on tcgen05, above 64 in blocks
+    (12, 1, 1), (4, 1, 4), (6, 2, 8), (25, 1, 1), (8, 1, 4), (12, 1, 3), (6, 2, 16), (4, 2, 32), (13, 1, 5), (8, 1, 16),
+]
+
+
+@pytest.mark.parametrize("d,page,dtype,causal", [(128, 64, "bf16", True), (64, 16, "fp16", False), (64, 128, "bf16", True),
+                                                 (128, 32, "fp16", False)])
+@pytest.mark.parametrize("Hq,Hkv,Nq", ROWS)
+def test_many_rows_long_and_short_together(gpu_lib, Hq, Hkv, Nq, d, page, dtype, causal):
+    """A context that several CTAs share and join, beside empty and short ones."""
+    run_case(gpu_lib, 100 * Hq + Nq + d, [6001, 0, 2, 127, 129, 1500], Hq, Hkv, Nq, d, page, causal, dtype)
+
+
+@pytest.mark.parametrize("Hq,Nq", [(16, 1), (24, 1), (32, 1), (16, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_and_a_table_that_needs_no_workspace(gpu_lib, Hq, Nq, d):
+    """As many CTAs as segments, each with one of its own, or 125 short requests."""
+    for lens, Hkv in (([500, 1, 0, 130], 3), ([33, 0, 140, 7, 128] * 25, 1)):
+        W = -(-max(lens) // 16) + 2
+        assert gpu_lib.fa2_fwd_kv4_workspace(len(lens), Hq * Hkv, Hkv, Nq, d, W, 16) == 0
+        run_case(gpu_lib, Hq + d + len(lens), lens, Hq * Hkv, Hkv, Nq, d, 16, True, "bf16")
+
+
+@pytest.mark.parametrize("step", [1.0, 6.0, 40.0])
+@pytest.mark.parametrize("rows", [10, 20, 32, 48, 64])
+def test_running_maximum_of_many_rows(gpu_lib, rows, step):
+    """Rows whose scores grow from tile to tile by less, about and more than
+    the slack, beside rows whose scores fall or stay."""
+    fa2 = gpu_lib
+    d, page, n = 128, 32, 2560
+    rng = np.random.default_rng(int(step) + rows)
+    table, P = make_tables(rng, [n], page)
+    cache = make_cache(rng, P, 1, page, d)
+    codes, scales = cache[..., : page * d // 2], cache[..., page * d // 2:]
+    scales = scales.reshape(P, 1, 2, page, d // 16)
+    codes = codes.reshape(P, 1, 2, page, d // 2)
+    for j in range(n):
+        codes[table[0, j // page], 0, 0, j % page] = 0x22      # 1.0
+        level = int(np.searchsorted(kv4.E4M3[:127], (1 + j // 128) * step / 64.0))
+        scales[table[0, j // page], 0, 0, j % page] = min(level, 126)
+    ck = np.concatenate([codes.reshape(P, 1, 2, -1), scales.reshape(P, 1, 2, -1)], -1)
+    q = torch.full((1, rows, 1, d), 64.0 * math.log(2) / d)
+    q *= torch.tensor([1.0, 0.25, -1.0, 0.0, 0.5]).repeat(rows)[:rows].reshape(1, rows, 1, 1)
+    q = q.to(torch.bfloat16)
+    one = np.ones(1, np.float32)
+    o, lse = fa2.fa2_fwd_kv4(q.cuda(), torch.tensor(ck).cuda(), i32(table), i32([n]), torch.tensor(one).cuda(),
+                             torch.tensor(one).cuda(), scale=1.0)
+    ok(fa2)
+    keys, values = context(ck, table, [n], d, one, one)
+    check_attention(o, lse, q, keys, values, 1.0, False, [n], "bf16")
+
+
+@pytest.mark.parametrize("dtype,mag", [("bf16", 1e-38), ("bf16", 1e30), ("fp16", 6e-8), ("fp16", 3e4)])
+@pytest.mark.parametrize("Hq", [16, 40])
+def test_many_query_rows_of_any_magnitude(gpu_lib, Hq, dtype, mag):
+    fa2 = gpu_lib
+    rng = np.random.default_rng(8)
+    lens, d, page = [177], 64, 16
+    table, P = make_tables(rng, lens, page)
+    cache = make_cache(rng, P, 1, page, d)
+    q = torch.tensor(np.clip(rng.standard_normal((1, Hq, 1, d)), -2, 2)).to(DT[dtype])
+    q[0, 1::3] = (q[0, 1::3].float() * mag).to(DT[dtype])
+    one = np.ones(1, np.float32)
+    scale = 0.1 if mag < 1 else 1.0 / mag
+    o, lse = fa2.fa2_fwd_kv4(q.cuda(), torch.tensor(cache).cuda(), i32(table), i32(lens), torch.tensor(one).cuda(),
+                             torch.tensor(one).cuda(), scale=scale)
+    ok(fa2)
+    keys, values = context(cache, table, lens, d, one, one)
+    check_attention(o, lse, q, keys, values, scale, False, lens, dtype)
+
+
+@pytest.mark.parametrize("Hq,Nq", [(4, 4), (12, 4), (16, 8)])
+def test_what_is_not_finite_stays_with_its_rows(gpu_lib, Hq, Nq):
+    """NaN scales of the last new token reach the last query row of each head;
+    a query row with a NaN or an infinity leaves the others as they were."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(10)
+    n, d, page = 270, 128, 16
+    table, P = make_tables(rng, [n], page)
+    t, ln, one = i32(table), i32([n]), torch.ones(1, device="cuda")
+    q = torch.tensor(rng.standard_normal((1, Hq, Nq, d))).to(torch.float16).cuda()
+    cache = make_cache(rng, P, 1, page, d)
+    clean = torch.tensor(cache).cuda()
+    o, lse = fa2.fa2_fwd_kv4(q, clean, t, ln, one, one, causal=True)
+    for part in (0, 1):
+        c = cache.copy()
+        c[table[0, (n - 1) // page], 0, part, page * d // 2 + (n - 1) % page * (d // 16) + 3] = 0xFF
+        o2, lse2 = fa2.fa2_fwd_kv4(q, torch.tensor(c).cuda(), t, ln, one, one, causal=True)
+        ok(fa2)
+        assert torch.equal(o2[:, :, :-1], o[:, :, :-1]) and torch.equal(lse2[:, :, :-1], lse[:, :, :-1])
+        if part:
+            assert o2[:, :, -1, 48:64].isnan().all()
+            assert torch.equal(o2[:, :, -1, :48], o[:, :, -1, :48]) and torch.equal(o2[:, :, -1, 64:], o[:, :, -1, 64:])
+        else:
+            assert o2[:, :, -1].isnan().all() and lse2[:, :, -1].isnan().all()
+    q2 = q.clone()
+    q2[0, 1, 2, 5], q2[0, Hq - 1, 0, 100] = float("nan"), float("inf")
+    o2, lse2 = fa2.fa2_fwd_kv4(q2, clean, t, ln, one, one, causal=True)
+    ok(fa2)
+    keep = torch.ones(1, Hq, Nq, dtype=torch.bool)
+    keep[0, 1, 2] = keep[0, Hq - 1, 0] = False
+    assert o2[~keep].isnan().all()
+    assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[keep], lse[keep])
+
+
+@pytest.mark.parametrize("Hq", [4, 16, 40])
+def test_bad_pages_of_many_rows(gpu_lib, Hq):
+    """In a first, a middle and a last tile, a whole tile among them."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(13)
+    n, d, page = 5000, 128, 16
+    table, P = make_tables(rng, [n], page)
+    cache = make_cache(rng, P, 1, page, d)
+    one = np.ones(1, np.float32)
+    q = torch.tensor(rng.standard_normal((1, Hq, 1, d))).to(torch.bfloat16)
+    bad = table.copy()
+    out = [0, 3, *range(24, 32), 100, 101, 312]
+    bad[0, out] = rng.choice([-1, P, 2 ** 31 - 1, -2 ** 31], len(out))
+    c, ones = torch.tensor(cache).cuda(), torch.ones(1, device="cuda")
+    o, lse = fa2.fa2_fwd_kv4(q.cuda(), c, i32(bad), i32([n]), ones, ones)
+    assert fa2.fa2_check_status(torch.cuda.current_stream().cuda_stream) == fa2.FA2_ERR_BOUNDS
+    keys, values = context(cache, table, [n], d, one, one)
+    seen = np.concatenate([np.arange(j * page, min((j + 1) * page, n)) for j in range(-(-n // page)) if j not in out])
+    check_attention(o, lse, q, [keys[0][:, seen]], [values[0][:, seen]], d ** -0.5, False, [len(seen)], "bf16")
+    bad[0] = -1   # no token at all is left
+    o, lse = fa2.fa2_fwd_kv4(q.cuda(), c, i32(bad), i32([n]), ones, ones)
+    assert fa2.fa2_check_status(torch.cuda.current_stream().cuda_stream) == fa2.FA2_ERR_BOUNDS
+    assert not o.any() and lse.isneginf().all()
+
+
+@pytest.mark.parametrize("Hq,Nq", [(8, 1), (16, 1), (8, 3), (12, 4), (16, 8)])
+def test_graphs_that_share_a_workspace(gpu_lib, Hq, Nq):
+    """Two captured calls of different shapes, replayed in turn on one stream
+    with one workspace that held anything before, while eager calls use it too."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(71)
+    d, page = 128, 64
+    one = torch.ones(2, device="cuda")
+    calls, need = [], 0
+    for lens in ([7000, 300, 0], [90, 12000]):
+        table, P = make_tables(rng, lens, page)
+        cache = torch.tensor(make_cache(rng, P, 2, page, d)).cuda()
+        q = torch.tensor(rng.standard_normal((len(lens), 2 * Hq, Nq, d))).to(torch.bfloat16).cuda()
+        args = (q, cache, i32(table), i32(lens), one, one)
+        want = fa2.fa2_fwd_kv4(*args, causal=True)
+        need = max(need, fa2.fa2_fwd_kv4_workspace(len(lens), 2 * Hq, 2, Nq, d, table.shape[1], page))
+        calls.append((args, want, torch.empty_like(want[0]), torch.empty_like(want[1])))
+    assert need > 0
+    ws = torch.tensor(rng.integers(0, 256, need, dtype=np.uint8)).cuda()
+    torch.cuda.synchronize()
+    graphs = []
+    for args, _, o, lse in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa2.fa2_fwd_kv4(*args, o, lse, ws, causal=True)
+        graphs.append(g)
+    for _ in range(3):
+        for i in (0, 0, 1, 0, 1, 1):
+            args, want, o, lse = calls[i]
+            o.fill_(7), lse.fill_(7)
+            graphs[i].replay()
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+            args, want, _, _ = calls[1 - i]
+            got = fa2.fa2_fwd_kv4(*args, None, None, ws, causal=True)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    ok(fa2)
+
+
+@pytest.mark.parametrize("Hq,Nq,d", [(16, 1, 128), (24, 1, 64), (32, 1, 128), (16, 4, 64), (16, 8, 128)])
+def test_many_rows_repeat_bit_for_bit(gpu_lib, Hq, Nq, d):
+    fa2 = gpu_lib
+    rng = np.random.default_rng(62)
+    lens, page = [9000, 0, 333, 4097], 32
+    table, P = make_tables(rng, lens, page)
+    cache = torch.tensor(make_cache(rng, P, 2, page, d)).cuda()
+    one = torch.ones(2, device="cuda")
+    q = torch.tensor(rng.standard_normal((4, 2 * Hq, Nq, d))).to(torch.bfloat16).cuda()
+    a = [fa2.fa2_fwd_kv4(q, cache, i32(table), i32(lens), one, one, causal=True) for _ in range(8)]
+    ok(fa2)
+    assert all(torch.equal(x[0], a[0][0]) and torch.equal(x[1], a[0][1]) for x in a)
+
+
+def test_calls_on_a_given_stream_allocate_from_it(gpu_lib):
+    """What a call with `stream` allocates belongs to that stream: memory given
+    back there is reused behind the work queued on it, without a wait."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(63)
+    lens, d, page = [12000, 3], 128, 64
+    table, P = make_tables(rng, lens, page)
+    cache = torch.tensor(make_cache(rng, P, 2, page, d)).cuda()
+    one, t, ln = torch.ones(2, device="cuda"), i32(table), i32(lens)
+    q = torch.tensor(rng.standard_normal((2, 16, 1, d))).to(torch.bfloat16).cuda()
+    want = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(30):
+        got = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, stream=side)
+        kv = fa2.fa2_kv4_gather(cache, t, ln, one, one, 500, d, stream=side.cuda_stream)
+        with torch.cuda.stream(side):
+            same = torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert same and not kv[0][1, :, 3:].any()
+        del kv
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    again = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, stream=0)   # the default stream's handle
+    assert torch.equal(again[0], want[0])
+    ok(fa2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_watchdog_of_many_rows(gpu_lib, d):
+    """A wait that runs out ends the call with a status; the context and the
+    workspace stay usable."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(64)
+    lens, page = [6000, 20], 64
+    table, P = make_tables(rng, lens, page)
+    cache = torch.tensor(make_cache(rng, P, 1, page, d)).cuda()
+    one, t, ln = torch.ones(1, device="cuda"), i32(table), i32(lens)
+    q = torch.tensor(rng.standard_normal((2, 32, 1, d))).to(torch.bfloat16).cuda()
+    ws = torch.zeros(fa2.fa2_fwd_kv4_workspace(2, 32, 1, 1, d, table.shape[1], page), dtype=torch.uint8, device="cuda")
+    want = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, workspace=ws)
+    ok(fa2)
+    old_limit = fa2.fa2_set_wait_limit_ns(20_000_000)
+    old_flags = fa2.fa2_set_debug_flags(1)
+    try:
+        fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, workspace=ws)
+        rc = fa2.fa2_check_status(torch.cuda.current_stream().cuda_stream)
+    finally:
+        fa2.fa2_set_debug_flags(old_flags)
+        fa2.fa2_set_wait_limit_ns(old_limit)
+    assert rc == fa2.FA2_ERR_TIMEOUT
+    ok(fa2)
+    got = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     ok(fa2)
