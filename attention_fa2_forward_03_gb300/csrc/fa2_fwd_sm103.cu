@@ -753,6 +753,8 @@ fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
         p.part_ml = p.part_o + 2LL * p.ctas * kRows * D;
         p.arrived = reinterpret_cast<unsigned long long*>(p.part_ml + 2LL * p.ctas * kRows * 2);
     }
+    // 32 KB or more of zeros a CTA
+    p.idle = static_cast<int>(std::min<long long>(std::max(1, p.ctas / p.B), static_cast<long long>(p.hkv) * p.rows * D / 16384 + 1));
     p.nonce = kv4_nonce();
     return kv4_launch_kernel(kern, p.ctas, kThreads, kSmem, stream, p);
 }

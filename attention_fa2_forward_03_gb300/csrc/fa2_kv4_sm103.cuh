@@ -570,15 +570,16 @@ struct FwdParams {
     const int* block_table;    // [B, max_pages]
     void* o;
     float* lse;
-    float* part_o;             // [2 * ctas, 8 NR, D]
-    float* part_ml;            // [2 * ctas, 8 NR, 2]
+    float* part_o;             // [2 * ctas, rows of a block, D]
+    float* part_ml;            // [2 * ctas, rows of a block, 2]: reference, sum
     unsigned long long* arrived;  // [ctas]
     unsigned long long nonce;  // of this launch, low 16 bits 0
-    int B, hkv, nq, rows, rblocks;   // rows = group * N_q; rblocks = ceil(rows / (8 NR))
+    int B, hkv, nq, rows, rblocks;   // rows = group * N_q; rblocks: blocks of them
     int max_pages, max_tokens, page, log2_page, num_pages;
     int part, page_bytes;      // bytes of keys (or values) of a head's page, of a page of all heads
     int causal;
     int ctas;                  // CTAs that take work
+    int idle;                  // CTAs that write the zeros of a request without a key
     float scale_log2;
     long long wait_limit_ns;   // of a wait for the tensor cores
     int debug_flags;
@@ -1089,6 +1090,24 @@ __device__ __forceinline__ void store_row4(const FwdParams& p, long long row, in
     if (d0 == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
+// Requests without a key: O = 0, LSE = -inf, by the T threads of `idle` CTAs a
+// request. Lengths behind the table's end are reported here too.
+template <int D, bool kBf16, int T>
+__device__ __forceinline__ void idle_requests(const FwdParams& p) {
+    for (int w = blockIdx.x; w < p.B * p.idle; w += gridDim.x) {
+        const int b = p.idle == 1 ? w : w / p.idle, share = w - b * p.idle;
+        const int len = p.seq_lens[b];
+        if (len <= 0) {
+            const long long rows = static_cast<long long>(p.hkv) * p.rows;
+            for (long long i = share * T + threadIdx.x; i < rows * (D / 4); i += p.idle * T)
+                store_row4<D, kBf16>(p, b * rows + i / (D / 4), static_cast<int>(i % (D / 4)) * 4, make_float4(0, 0, 0, 0),
+                                     0.0f, 0.0f, 0.0f);
+        } else if (len > p.max_tokens && threadIdx.x == 0) {
+            report(kSiteLength);
+        }
+    }
+}
+
 __device__ __forceinline__ void axpy4(float4& y, float a, const float4& x) {
     y.x = fmaf(a, x.x, y.x);
     y.y = fmaf(a, x.y, y.y);
@@ -1424,17 +1443,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
         }
     }
 
-    // Requests without a key: O = 0, LSE = -inf.
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int len = p.seq_lens[b];
-        if (len <= 0) {
-            const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
-            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += T)
-                store_row4<D, kBf16>(p, r0 + i / (D / 4), i % (D / 4) * 4, make_float4(0, 0, 0, 0), 0.0f, 0.0f, 0.0f);
-        } else if (len > p.max_tokens && tid == 0) {
-            report(kSiteLength);
-        }
-    }
+    idle_requests<D, kBf16, T>(p);
 }
 
 }  // namespace kv4

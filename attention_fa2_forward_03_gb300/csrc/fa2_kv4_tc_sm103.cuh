@@ -641,17 +641,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
         }
     }
 
-    // Requests without a key: O = 0, LSE = -inf.
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int len = p.seq_lens[b];
-        if (len <= 0) {
-            const long long r0 = static_cast<long long>(b) * p.hkv * p.rows;
-            for (int i = tid; i < p.hkv * p.rows * (D / 4); i += kAll)
-                store_row4<D, kBf16>(p, r0 + i / (D / 4), i % (D / 4) * 4, make_float4(0, 0, 0, 0), 0.0f, 0.0f, 0.0f);
-        } else if (len > p.max_tokens && tid == 0) {
-            report(kSiteLength);
-        }
-    }
+    idle_requests<D, kBf16, kAll>(p);
 }
 
 }  // namespace tc

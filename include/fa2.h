@@ -327,14 +327,17 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
  *              allowed key gets O = 0 and LSE = -inf
  *   workspace : device, fa2_fwd_kv4_workspace(...) bytes (may be NULL for 0),
  *              contents irrelevant before and after; calls that may overlap
- *              need their own
+ *              need their own. After FA2_ERR_TIMEOUT it is zeroed before a
+ *              captured call that uses it is replayed
  * Any N_q >= 1 is right. Up to 64 query rows a KV head (H_q / H_kv * N_q) read
  * the cache once, every 64 more once again; prompts and long chunks of them are
  * faster by fa2_kv4_gather and fa2_fwd_ex.
  * Query rows hold no precision less than q's own; the softmax weights are
  * rounded to fp16 (2^-11), sums are fp32. A row of q that is not finite
  * affects no other row. A NaN in the cache affects the rows that see it.
- * B * H_q * N_q < 2^31 - 64. One launch.
+ * B * H_q * N_q < 2^31 - 64, H_kv < 32768, and the blocks of at most 64 rows
+ * of all requests and heads times max_pages * page_size / 32 up to 2^30. One
+ * launch.
  */
 fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
                        const float* k_descale, const float* v_descale, void* o, float* lse, void* workspace,

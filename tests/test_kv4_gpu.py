@@ -923,3 +923,40 @@ def test_watchdog_of_many_rows(gpu_lib, d):
     got = fa2.fa2_fwd_kv4(q, cache, t, ln, one, one, workspace=ws)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     ok(fa2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,d", [(8, 2, 1, 128), (8, 2, 700, 64), (16, 1, 16, 128), (32, 8, 300, 128)])
+def test_padded_batch_with_idle_requests(gpu_lib, Hq, Hkv, Nq, d):
+    """Requests of length 0 and below it: O = 0, LSE = -inf on every row."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(65)
+    lens, page = [0, 40, -3, 0, 0], 16
+    table, P = make_tables(rng, lens, page)
+    cache = torch.tensor(make_cache(rng, P, Hkv, page, d)).cuda()
+    one = torch.ones(Hkv, device="cuda")
+    q = torch.tensor(rng.standard_normal((5, Hq, Nq, d))).to(torch.bfloat16).cuda()
+    for sel in ([0, 1, 2, 3, 4], [2], [0, 3]):
+        o, lse = torch.full_like(q[sel], 7), torch.full((len(sel), Hq, Nq), 7.0, device="cuda")
+        fa2.fa2_fwd_kv4(q[sel], cache, i32(table[sel]), i32(np.array(lens)[sel]), one, one, o, lse)
+        ok(fa2)
+        for j, b in enumerate(sel):
+            if lens[b] <= 0:
+                assert not o[j].any() and lse[j].isneginf().all()
+            else:
+                alone = fa2.fa2_fwd_kv4(q[b: b + 1], cache, i32(table[b: b + 1]), i32(lens[b: b + 1]), one, one)
+                assert torch.equal(o[j], alone[0][0]) and torch.equal(lse[j], alone[1][0])
+
+
+def test_idle_request_of_more_elements_than_32_bits_count(gpu_lib):
+    """2^27 + 64 rows of 64: their pieces of four pass 2^31."""
+    fa2 = gpu_lib
+    Hq, Nq, d, page = 64, 2 ** 21 + 1, 64, 16
+    q = torch.zeros((1, Hq, Nq, d), dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.full_like(q, 7), torch.full((1, Hq, Nq), 7.0, device="cuda")
+    cache = torch.zeros(fa2.fa2_kv4_cache_shape(1, 1, page, d), dtype=torch.uint8, device="cuda")
+    one = torch.ones(1, device="cuda")
+    fa2.fa2_fwd_kv4(q, cache, i32([[0]]), i32([0]), one, one, o, lse)
+    ok(fa2)
+    del q
+    assert lse.isneginf().all()
+    assert all(not part.any() for part in o[0])
