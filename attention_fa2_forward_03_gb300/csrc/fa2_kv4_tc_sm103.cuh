@@ -33,8 +33,8 @@ constexpr int kThreads = 256;               // of the eight working warps
 constexpr int kAll = kThreads + 64;         // with the one that issues products and the one that loads
 constexpr int kSiteTc = 52;                 // a wait for the tensor cores
 
-// Tensor memory: K (fp16 pairs), S^T, O^T. Two CTAs an SM.
-constexpr uint32_t kColK = 0, kColS = 64, kColO = 128, kCols = 256;
+// Tensor memory: K (fp16 pairs), S^T of two tiles, O^T. Two CTAs an SM.
+constexpr uint32_t kColK = 0, kColS = 64, kColO = 192, kCols = 256;
 
 template <int D, int N>
 struct Smem {
@@ -49,14 +49,15 @@ struct Smem {
     float row_ml[N][2];
     int off[N], mx[N];
     int nan_first[D / 16];                       // first token with a NaN among its values, by scale group
-    uint32_t ok[2];                              // usable 16-token blocks of a stage's tile, a bit each
-    unsigned long long bar[8], counter;
+    alignas(8) uint32_t ok[4][2];                // usable 16-token blocks of the last tiles loaded: the first bit of each byte
+    unsigned long long bar[12], counter;
     uint32_t tmem;
     int abort, last;
 };
 
-// Barriers: products done, their operands ready, stages of codes full and free.
-enum Bar { kBarS = 0, kBarO = 1, kBarK = 2, kBarP = 3, kBarFull = 4, kBarFree = 6 };
+// Barriers: products done, their operands ready, places of codes (of keys, of
+// values; two each) full and free.
+enum Bar { kBarS = 0, kBarO = 1, kBarK = 2, kBarP = 3, kBarFull = 4, kBarFree = 8 };
 
 // Barrier of the working warps, and one that also joins a condition.
 __device__ __forceinline__ void work_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -138,60 +139,81 @@ __device__ __forceinline__ int code_at(int r, int c) {
     else return r * 32 + ((c ^ ((r >> 2) & 1)) * 16);
 }
 
-// The loading warp: the run's tiles one after another into the two stages,
-// 16 tokens (of one page) at a time. Page ids are read while a stage is waited for.
+// The loading warp: the run's tiles one after another; keys a tile ahead of
+// values, as they are used. Eight lanes take a block of 16 tokens (of one page),
+// 128 bytes of codes at a time, and every lane has two blocks, so that all
+// addresses of a tile are two and constants from them. Page ids are read a tile
+// ahead.
 template <int D, int N>
 __device__ __forceinline__ void load_tiles(const FwdParams& p, Smem<D, N>& sm, Cursor c, int pad, const Waiter& wait) {
     using Sm = Smem<D, N>;
-    constexpr int kPieces = D / 32, kIts = 16 * kPieces / 32, kEach = D / 16;   // 16-byte pieces of a token's codes, copies of a block's, pieces of its key scales
-    const int lane = threadIdx.x & 31;
-    const uint32_t bars = ptx::smem_addr(sm.bar);
-    const uint32_t k_dst = code_at<D>(lane / kPieces, lane % kPieces);
-    const uint32_t s_dst = (lane >= kEach ? Sm::kVs : Sm::kKs) + lane % kEach * 16;
-    uint32_t k = 0;
+    constexpr int kLines = D / 16, kPieces = D / 32;   // 128-byte lines of a block's codes, 16-byte pieces of a token's
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const uint32_t bars = ptx::smem_addr(sm.bar), block = (lane >> 3) * 8 * D, sblock = (lane >> 3) * D + piece * 16;
     bool ok = !(p.debug_flags & 1);   // test hook: nothing is loaded, and the waits run out
+    struct Place {
+        const uint8_t* codes[2];   // of the lane's piece in its blocks, keys
+        const uint8_t* scales[2];
+        bool good[2];
+    };
+
+    // One part (0 keys, 1 values) of the run's k-th tile, once there is room.
+    auto load = [&](int part, uint32_t k, const Place& x) {
+        const int st = 2 * part + (k & 1);
+        ok = __all_sync(~0u, wait.wait(bars + 8 * (kBarFree + st), ((k >> 1) & 1) ^ 1, kSiteTc));
+        if (!ok) return;
+        const uint32_t stage = ptx::smem_addr(sm.code[k & 1]);
+        const uint32_t dst = stage + (part ? Sm::kV : 0) + block, dst_s = stage + (part ? Sm::kVs : Sm::kKs) + sblock;
+        const int off = part ? p.part : 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (x.good[u]) {
+#pragma unroll
+                for (int j = 0; j < kLines; ++j)   // placed as code_at says
+                    copy16(dst + u * (32 * D) + j * 128 + ((piece ^ (j & (kPieces - 1))) * 16), x.codes[u] + off + j * 128);
+                if (piece < D / 16) copy16(dst_s + u * (4 * D), x.scales[u] + off);
+            }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bars + 8 * (kBarFull + st)) : "memory");
+        if (lane == 0) ptx::mbar_arrive(bars + 8 * (kBarFull + st));
+    };
+    uint32_t k = 0;
+    Place now, was;   // was: of the tile whose values are still to be loaded
     while (c.u < c.end && ok) {
-        const uint8_t* codes = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part;
-        const uint8_t* scales = codes + (lane >= kEach ? p.part : 0) + p.page * (D / 2) + lane % kEach * 16;
-        codes += lane * 16;
+        const uint8_t* head = p.cache + static_cast<long long>(c.hr / p.rblocks) * 2 * p.part + piece * 16;
         const int* table = p.block_table + static_cast<long long>(c.b) * p.max_pages;
         const int end = c.tile + part_tiles(c);
-        for (int tile = c.tile; tile < end; ++tile, ++k) {
-            const int st = k & 1, mine = tile * kTok + (lane & 7) * 16;
-            const int id = mine < c.len ? table[mine >> p.log2_page] : -1;
-            const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
-            if (!good && mine < c.len && lane < 8) report(kSitePage);
-            const uint32_t usable = __ballot_sync(~0u, good) & 0xFF;
-            ok = wait.wait(bars + 8 * (kBarFree + st), ((k >> 1) & 1) ^ 1, kSiteTc);
-            if (!__all_sync(~0u, ok)) break;
-            const uint32_t dst = ptx::smem_addr(sm.code[st]);
+        int id[2], mine = c.tile * kTok + (lane >> 3) * 16;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const int pg = __shfl_sync(~0u, id, b);
-                if (!(usable >> b & 1)) continue;
-                const int at = (tile * kTok + b * 16) & (p.page - 1);
-                const long long page = static_cast<long long>(pg) * p.page_bytes;
-                const uint8_t* from = codes + page + at * (D / 2);
+        for (int u = 0; u < 2; ++u) id[u] = mine + 64 * u < c.len ? table[(mine + 64 * u) >> p.log2_page] : -1;
+        for (int tile = c.tile; tile < end && ok; ++tile, ++k, mine += kTok) {
+            uint32_t usable[2];
 #pragma unroll
-                for (int it = 0; it < kIts; ++it) {
-                    copy16(dst + k_dst + b * (8 * D) + it * 512, from + it * 512);
-                    copy16(dst + Sm::kV + k_dst + b * (8 * D) + it * 512, from + p.part + it * 512);
-                }
-                if (lane < 2 * kEach) copy16(dst + s_dst + b * D, scales + page + at * (D / 16));
+            for (int u = 0; u < 2; ++u) {
+                now.good[u] = static_cast<unsigned>(id[u]) < static_cast<unsigned>(p.num_pages);
+                if (!now.good[u] && mine + 64 * u < c.len && piece == 0) report(kSitePage);
+                usable[u] = __ballot_sync(~0u, now.good[u]);
+                const int at = (mine + 64 * u) & (p.page - 1);
+                const uint8_t* from = head + static_cast<long long>(id[u]) * p.page_bytes;
+                now.codes[u] = from + at * (D / 2);
+                now.scales[u] = from + p.page * (D / 2) + at * (D / 16);
             }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bars + 8 * (kBarFull + st)) : "memory");
-            if (lane == 0) {
-                sm.ok[st] = usable;
-                ptx::mbar_arrive(bars + 8 * (kBarFull + st));
-            }
+            if (tile + 1 < end)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    id[u] = mine + kTok + 64 * u < c.len ? table[(mine + kTok + 64 * u) >> p.log2_page] : -1;
+            if (lane == 0) *reinterpret_cast<uint2*>(sm.ok[k & 3]) = make_uint2(usable[0], usable[1]);
+            load(0, k, now);
+            if (k > 0 && ok) load(1, k - 1, was);
+            was = now;
         }
         next_segment<kLog>(p, c, pad);
     }
+    if (k > 0 && ok) load(1, k - 1, was);
     copy_wait_all();
 }
 
-// The issuing warp: S^T of a segment's first tile, then O^T of each tile and
-// S^T of the next, as their operands get ready.
+// The issuing warp: S^T of a segment's first tile, then S^T of each next tile
+// and O^T of the one before it, as their operands get ready.
 template <int D, int N>
 __device__ __forceinline__ void issue_products(const FwdParams& p, Smem<D, N>& sm, Cursor c, int pad, uint32_t tmem,
                                                const Waiter& wait) {
@@ -205,15 +227,17 @@ __device__ __forceinline__ void issue_products(const FwdParams& p, Smem<D, N>& s
     auto scores = [&] {
         ok = __all_sync(~0u, wait.wait(bars + 8 * kBarK, n_k & 1, kSiteTc));
         if (!ok) return;
-        ++n_k;
         ptx::tc_fence_after();
-        mma_scores<D, N * 8>(tmem + kColS, tmem + kColK, qdesc, kIdS);
+        mma_scores<D, N * 8>(tmem + kColS + (n_k & 1) * 64, tmem + kColK, qdesc, kIdS);
         ptx::tc_commit_elect(bars + 8 * kBarS);
+        ++n_k;
     };
     while (c.u < c.end && ok) {
         const int n = part_tiles(c);
         scores();
         for (int i = 0; i < n && ok; ++i) {
+            if (i + 1 < n) scores();
+            if (!ok) break;
             ok = __all_sync(~0u, wait.wait(bars + 8 * kBarP, n_p & 1, kSiteTc));
             if (!ok) break;
             ++n_p;
@@ -221,7 +245,6 @@ __device__ __forceinline__ void issue_products(const FwdParams& p, Smem<D, N>& s
             ptx::mma_ss_kloop<128, 256, 384, 512, 640, 768, 896, 128, 256, 384, 512, 640, 768, 896, 8>(
                 tmem + kColO, vdesc, pdesc, kIdO, i > 0);
             ptx::tc_commit_elect(bars + 8 * kBarO);
-            if (i + 1 < n) scores();
         }
         next_segment<kLog>(p, c, pad);
     }
@@ -371,7 +394,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
             ptx::mbar_init(bars + 8 * kBarO, 1);
             ptx::mbar_init(bars + 8 * kBarK, kThreads / 32);
             ptx::mbar_init(bars + 8 * kBarP, kThreads / 32);
-            for (int s = 0; s < 2; ++s) {
+            for (int s = 0; s < 4; ++s) {
                 ptx::mbar_init(bars + 8 * (kBarFull + s), 33);   // the lanes' copies, and what they left out
                 ptx::mbar_init(bars + 8 * (kBarFree + s), kThreads / 32);
             }
@@ -392,7 +415,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
         const uint32_t lane_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const Waiter wait{&sm.abort, p.wait_limit_ns};
         uint32_t n_s = 0, n_o = 0;   // products waited for so far
-        uint32_t k = 0;              // tiles so far: the stage of the next, and how often it was used
+        uint32_t k = 0;              // tiles so far: the places of the next, and how often they were used
         // the token's row of weights; a row's place in it is chosen by exclusive or
         const uint32_t p_row = ptx::smem_addr(sm.p) + tk * 128 + (tk & 7) * 16;
         bool ok = true;
@@ -425,6 +448,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
                 put_keys<D, N>(lane_at, ptx::smem_addr(sm.code[k & 1]), tk, half);
                 ptx::tc_fence_before();
                 arrive(kBarK);
+                arrive(kBarFree + (k & 1));
             };
             stage_q<D, N, kBf16>(p, sm, cur);
             ptx::fence_proxy_async_smem();
@@ -436,16 +460,20 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
 
             for (int i = 0; i < n; ++i, ++k) {
                 const int tok0 = (cur.tile + i) * kTok, pos = tok0 + tk;
-                const bool live = pos < cur.len && (sm.ok[k & 1] >> (tk >> 4) & 1);
-                if (i > 0) {   // the values' place is free when the last product with them is done
-                    ok = wait.wait(bars + 8 * kBarO, n_o & 1, kSiteTc) && ok;
-                    ++n_o;
-                }
-                put_values<D, N>(sm, ptx::smem_addr(sm.code[k & 1]), tk, half, live, pos);
-                arrive(kBarFree + (k & 1));
+                const bool live = pos < cur.len && (sm.ok[k & 3][tk >> 6] >> (tk >> 4 & 3) * 8 & 1);
+                const uint32_t s_at = lane_at + kColS + (k & 1) * 64 + half * H;
                 ok = wait.wait(bars + 8 * kBarS, n_s & 1, kSiteTc) && ok;
                 ++n_s;
                 ptx::tc_fence_after();
+                if (i + 1 < n) keys(k + 1);   // their product runs while this tile's weights are made
+                if (i > 0) {   // the values' place is free when the last product with them is done
+                    ok = wait.wait(bars + 8 * kBarO, n_o & 1, kSiteTc) && ok;
+                    ++n_o;
+                    ptx::tc_fence_after();
+                }
+                ok = wait.wait(bars + 8 * (kBarFull + 2 + (k & 1)), (k >> 1) & 1, kSiteTc) && ok;
+                put_values<D, N>(sm, ptx::smem_addr(sm.code[k & 1]), tk, half, live, pos);
+                arrive(kBarFree + 2 + (k & 1));
 
                 // The thread's token and its half of the rows: exponents, then
                 // weights, which go to shared memory and into the row sums.
@@ -455,7 +483,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
 #pragma unroll
                     for (int j0 = 0; j0 < H; j0 += 8) {
                         uint32_t s[8];
-                        tmem_ld8(lane_at + kColS + half * H + j0, s);
+                        tmem_ld8(s_at + j0, s);
 #pragma unroll
                         for (int j = 0; j < 8; j += 2) {
                             const int row = half * H + j0 + j;
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
 #pragma unroll
                     for (int j0 = 0; j0 < H; j0 += 8) {
                         uint32_t s[8];
-                        tmem_ld8(lane_at + kColS + half * H + j0, s);
+                        tmem_ld8(s_at + j0, s);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int row = half * H + j0 + j;
@@ -550,7 +578,6 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
                     work_sync();
                 }
                 arrive(kBarP);
-                if (i + 1 < n) keys(k + 1);
             }
             if (ok) {
                 ok = wait.wait(bars + 8 * kBarO, n_o & 1, kSiteTc);
