@@ -680,9 +680,10 @@ fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
 
 // Query rows that a pass over the keys serves. Up to 24 (8, 16 or 24) by the
 // kernel on mma.sync, beyond by the one on tcgen05 (32, 48 or 64): 38 sequences
-// of 8192 tokens take 64, 92 and 109 us by the first for 8, 16 and 24 rows, 111
-// and 122 us by the second for 16 and 32, where the first takes 138. More than 64
-// rows are cut into blocks of about equal size.
+// of 8192 tokens, heads of 128, take 91 and 111 us by the first for 16 and 24
+// rows, 111 and 122 us by the second (its 32-row form for 24); for 32 rows 138 us
+// by the first and 122 us by the second. More than 64 rows are cut into blocks
+// of about equal size.
 int kv4_block(long long rows) {
     if (rows <= 24) return static_cast<int>((rows + 7) / 8) * 8;
     const long long blocks = (rows + 63) / 64;
@@ -807,7 +808,7 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
     p.num_pages = num_pages;
     // 256 threads for a decoding step, whose scan is the shorter one. Where
     // there are thousands of slots, a warp for every 256 (48 prompts of 16384:
-    // 10 us; 20 by a cluster of eight CTAs, which writing in place asks for).
+    // 7.6 us; 18 by a cluster of eight CTAs, which writing in place asks for).
     const long long all = static_cast<long long>(B) * N;
     auto in = [](const void* a, const void* out, long long n) {
         const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(out);
@@ -1038,9 +1039,9 @@ int fa2_set_tile_config(int config) {
 }
 
 #ifdef FA2_DEBUG
-const char* fa2_version(void) { return "fa2-sm103a 0.3.0 debug"; }
+const char* fa2_version(void) { return "fa2-sm103a 0.4.0 debug"; }
 #else
-const char* fa2_version(void) { return "fa2-sm103a 0.3.0"; }
+const char* fa2_version(void) { return "fa2-sm103a 0.4.0"; }
 #endif
 
 }  // extern "C"
