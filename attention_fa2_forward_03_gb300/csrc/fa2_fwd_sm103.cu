@@ -680,9 +680,9 @@ fa2_status kv4_check_pages(int page_size, int num_pages, int max_pages) {
 
 // Query rows that a pass over the keys serves. Up to 24 (8, 16 or 24) by the
 // kernel on mma.sync, beyond by the one on tcgen05 (32, 48 or 64): 38 sequences
-// of 8192 tokens, heads of 128, take 91 and 111 us by the first for 16 and 24
-// rows, 111 and 122 us by the second (its 32-row form for 24); for 32 rows 138 us
-// by the first and 122 us by the second. More than 64 rows are cut into blocks
+// of 8192 tokens, heads of 128, take 89 and 110 us by the first for 16 and 24
+// rows, 111 and 121 us by the second (its 32-row form for 24); for 32 rows 138 us
+// by the first and 121 us by the second. More than 64 rows are cut into blocks
 // of about equal size.
 int kv4_block(long long rows) {
     if (rows <= 24) return static_cast<int>((rows + 7) / 8) * 8;
@@ -700,7 +700,7 @@ long long kv4_ctas(long long segments, long long max_tokens, long long most) {
     return std::min(most, segments * (tiles / fa2::kv4::kMinRun + 1));
 }
 
-// Workspace: two partial results a CTA, then a counter a CTA; nothing where
+// Workspace: two partial results a CTA, then two counters a CTA; nothing where
 // no segment can be split: each gets a CTA of its own (`locate`).
 int64_t kv4_workspace(long long B, long long hkv, long long rows, int d, long long max_tokens) {
     const int block = kv4_block(rows);
@@ -708,7 +708,7 @@ int64_t kv4_workspace(long long B, long long hkv, long long rows, int d, long lo
     // as many CTAs as a whole device runs at once have a segment each
     if (segments <= 128 * kv4_ctas_per_sm(block) && max_tokens <= 32LL * (fa2::kv4::kMinRun + fa2::kv4::kSpare)) return 0;
     return kv4_ctas(segments, max_tokens, fa2::kv4::kMaxCtas) *
-           (2LL * block * (d + 2) * static_cast<int64_t>(sizeof(float)) + static_cast<int64_t>(sizeof(unsigned long long)));
+           (2LL * block * (d + 2) * static_cast<int64_t>(sizeof(float)) + 2 * static_cast<int64_t>(sizeof(unsigned long long)));
 }
 
 // A number that no other launch of this process has, and that memory left

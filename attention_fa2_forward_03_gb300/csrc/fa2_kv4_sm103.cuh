@@ -559,6 +559,7 @@ constexpr int kTile = 32;      // tokens a warp takes at a time
 constexpr int kMaxCtas = 320;  // workspace is sized for this many
 constexpr int kMinRun = 32;    // tiles of 32 a CTA's run has at least
 constexpr int kSpare = 40;     // tiles by which a run may grow so that no segment is split
+constexpr int kJoinAtOnce = 12;   // partial results that are joined at once
 
 // Attention for up to 24 query rows a KV head, NR blocks of eight: both
 // products on mma.sync, transposed (S^T = K Q^T, O^T += V^T P^T), so that tokens
@@ -569,9 +570,9 @@ constexpr int kSpare = 40;     // tiles by which a run may grow so that no segme
 // and CTAs are joined at the end of a segment.
 //
 // What bounds it: at 8 rows memory. 64 sequences of 32768 tokens, 8 heads of 128 (as
-// drawn, 1.56 GB) take 257 us, 6.0 TB/s, 89% of a plain copy's rate; issue slots
+// drawn, 1.56 GB) take 253 us, 6.15 TB/s, 91% of a plain copy's rate; issue slots
 // are 64% busy. Above, the issue of instructions that wait for one another:
-// 38 sequences of 8192 tokens (358 MB) take 66, 91 and 111 us for 8, 16 and 24 rows,
+// 38 sequences of 8192 tokens (358 MB) take 63, 89 and 110 us for 8, 16 and 24 rows,
 // where the tensor pipe is busy for 27, 37 and 44% of the time with 16, 8 and 8
 // warps an SM, which is what the accumulators leave registers for. Twelve warps
 // spill and are slower; two warps on one tile, half of d each, take 111 us
@@ -597,7 +598,7 @@ struct FwdParams {
     float* lse;
     float* part_o;             // [2 * ctas, rows of a block, D]
     float* part_ml;            // [2 * ctas, rows of a block, 2]: reference, sum
-    unsigned long long* arrived;  // [ctas]
+    unsigned long long* arrived;  // [2 ctas]: of a segment by its first CTA, of a group of CTAs by its first
     unsigned long long nonce;  // of this launch, low 16 bits 0
     int B, hkv, nq, rows, rblocks;   // rows = group * N_q; rblocks: blocks of them
     int max_pages, max_tokens, page, log2_page, num_pages;
@@ -832,7 +833,7 @@ struct FwdSmem {
     int off[kRows];                          // keys at the sequence's end that the row may not see
     float ml[kWarps][kRows][2];
     float row_ml[kRows][2];
-    unsigned long long counter;              // the segment's, as it was when the segment began
+    unsigned long long seen[2];              // the segment's and the group's counter, as they were when the segment began
     int last;
 };
 
@@ -1242,36 +1243,53 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
     return static_cast<int>(old & 0xFFFF) + 1;
 }
 
-// Joins the `parts` partial results that CTAs c0, c0 + 1, ... left of a row
-// block, by the first T threads of the last CTA, with `sync` as their barrier.
-// wt: room for `room` weights, of as many parts at a time as there is room for.
-template <int D, int kRows, int T, bool kBf16, typename Sync>
-__device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int room, float (*row_ml)[2], int c0, int parts,
-                                           int rows, long long row0, float v_descale, Sync sync) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int most = room / kRows;
-    // slot of part i: the segment begins in CTA c0, in its second place
-    auto slot = [&](int i) { return 2LL * (c0 + i) + (i == 0 ? 1 : 0); };
-    for (int row = warp; row < rows; row += T / 32) {
-        constexpr int kMost = (kMaxCtas + 31) / 32;   // parts a lane looks at
-        float2 ml[kMost];
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int i = lane + 32 * k;
-            ml[k] = i < parts ? __ldcg(reinterpret_cast<const float2*>(p.part_ml + (slot(i) * kRows + row) * 2))
-                              : make_float2(-INFINITY, 0.0f);
-            m = fmaxf(m, ml[k].x);
+// A segment's CTAs c0 .. c1, and how their partial results are joined: at once
+// by the last of them to be done, or, where there are many, those of `group`
+// neighbours by the last of these, and the groups' results by the last of all:
+// one request of 262139 tokens, 4 heads, takes 38 us (41 us with 74 parts joined
+// at once), with 40 rows a head 86 us (125 us).
+struct Split {
+    int c0, parts, group, first, in_group;   // first CTA of this CTA's group, CTAs in it
+    __device__ __forceinline__ Split(int begin, int end) : c0(begin), parts(end - begin + 1) {
+        group = parts;
+        if (parts > kJoinAtOnce) {
+            group = 4;
+            while (group * group < parts) ++group;
         }
+        first = c0 + (static_cast<int>(blockIdx.x) - c0) / group * group;
+        in_group = min(group, c0 + parts - first);
+    }
+    __device__ __forceinline__ int groups() const { return (parts + group - 1) / group; }
+};
+
+// Joins `n` partial results of a row block, those of CTAs from, from + step, ..,
+// by the first T threads of a CTA, with `sync` as their barrier: into the block's
+// output, or into the first one's place. wt: room for 32 weights a row.
+template <int D, int kRows, int T, bool kBf16, typename Sync>
+__device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, float (*row_ml)[2], int c0, int from, int step, int n,
+                                           bool final, int rows, long long row0, float v_descale, Sync sync) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // CTA c0 has the segment in its second place
+    const long long at0 = 2LL * from + (from == c0 ? 1 : 0);
+    auto at = [&](int i) { return i == 0 ? at0 : 2LL * (from + i * step); };
+    constexpr int kEach = (kRows + T / 32 - 1) / (T / 32);   // rows of a warp; a lane has a part
+    float2 ml[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int row = warp + k * (T / 32);
+        ml[k] = make_float2(-INFINITY, 0.0f);
+        if (lane < n && row < rows) ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + (at(lane) * kRows + row) * 2));
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int row = warp + k * (T / 32);
+        if (row >= rows) break;
+        float m = ml[k].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int i = lane + 32 * k;
-            const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml[k].x - m);
-            if (i < parts && i < most) wt[i * kRows + row] = f;
-            l = fmaf(f, ml[k].y, l);
-        }
+        const float f = m == -INFINITY ? 0.0f : ptx::ex2_approx(ml[k].x - m);
+        if (lane < n) wt[lane * kRows + row] = f;
+        float l = f * ml[k].y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
         if (lane == 0) {
@@ -1280,37 +1298,73 @@ __device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, int ro
         }
     }
     sync();
-    constexpr int kItems = (kRows * (D / 4) + T - 1) / T;
-    float4 o[kItems];
+    // Two of the thread's items at a time, but for the kernel on tcgen05, whose
+    // loop would spill (64 rows: 197 us against 169 us).
+    constexpr int kItems = (kRows * (D / 4) + T - 1) / T, kPair = kItems > 1 && kRows <= 24 ? 2 : 1;
+#pragma unroll 1
+    for (int k = 0; k < kItems; k += kPair) {
+        const int i = tid + k * T, d0 = i % (D / 4) * 4;   // T is a multiple of D / 4
+        const float* src = p.part_o + (2LL * from * kRows + i / (D / 4)) * D + d0;
+        const long long next = 2LL * step * kRows * D;
+        constexpr int kDown = T / (D / 4);   // rows from one item to the next
+        int row[kPair];
+        bool in[kPair];
+        float4 o[kPair];
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) o[k] = make_float4(0, 0, 0, 0);
-    for (int j0 = 0; j0 < parts; j0 += most) {
-        const int n = min(most, parts - j0);
-        if (j0 > 0) {
-            sync();
-            for (int i = tid; i < n * rows; i += T) {
-                const int row = i % rows, part = i / rows;
-                const float m = row_ml[row][0], x = __ldcg(p.part_ml + (slot(j0 + part) * kRows + row) * 2);
-                wt[part * kRows + row] = m == -INFINITY ? 0.0f : ptx::ex2_approx(x - m);
-            }
-            sync();
+        for (int e = 0; e < kPair; ++e) {
+            row[e] = i / (D / 4) + e * kDown;
+            in[e] = row[e] < rows;
+            o[e] = make_float4(0, 0, 0, 0);
+        }
+        auto add = [&](const float* at, int j) {
+            float4 x[kPair];
+#pragma unroll
+            for (int e = 0; e < kPair; ++e)
+                if (in[e]) x[e] = __ldcg(reinterpret_cast<const float4*>(at + e * kDown * D));
+#pragma unroll
+            for (int e = 0; e < kPair; ++e)
+                if (in[e]) axpy4(o[e], wt[j * kRows + row[e]], x[e]);
+        };
+        if (in[0]) {
+            add(src + (from == c0 ? kRows * D : 0), 0);
+#pragma unroll 4
+            for (int j = 1; j < n; ++j) add(src + j * next, j);
         }
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-            const int i = tid + k * T, row = i / (D / 4), d0 = i % (D / 4) * 4;
-            if (row < rows) {
-                const float* src = p.part_o + (2LL * (c0 + j0) * kRows + row) * D + d0;
-                if (j0 == 0) axpy4(o[k], wt[row], __ldcg(reinterpret_cast<const float4*>(src + kRows * D)));
-#pragma unroll 8
-                for (int j = j0 == 0 ? 1 : 0; j < n; ++j)
-                    axpy4(o[k], wt[j * kRows + row], __ldcg(reinterpret_cast<const float4*>(src + 2LL * j * kRows * D)));
+        for (int e = 0; e < kPair; ++e) {
+            if (!in[e]) continue;
+            if (final) {
+                store_row4<D, kBf16>(p, row0 + row[e], d0, o[e], row_ml[row[e]][0], row_ml[row[e]][1], v_descale);
+            } else {
+                *reinterpret_cast<float4*>(p.part_o + (at0 * kRows + row[e]) * D + d0) = o[e];
+                if (d0 == 0)
+                    *reinterpret_cast<float2*>(p.part_ml + (at0 * kRows + row[e]) * 2) = make_float2(row_ml[row[e]][0], row_ml[row[e]][1]);
             }
         }
     }
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int i = tid + k * T, row = i / (D / 4), d0 = i % (D / 4) * 4;
-        if (row < rows) store_row4<D, kBf16>(p, row0 + row, d0, o[k], row_ml[row][0], row_ml[row][1], v_descale);
+}
+
+// Counts this CTA's partial results of a segment in and joins what is complete.
+// seen: the words as they were when the segment began, of the segment and of
+// the group.
+template <int D, int kRows, int T, bool kBf16, typename Sync>
+__device__ __forceinline__ void finish_part(const FwdParams& p, int c0, int c1, const unsigned long long (&seen)[2], int& last,
+                                            float* wt, float (*row_ml)[2], int rows, long long row0, float v_descale, Sync sync) {
+    const Split s(c0, c1);
+    const bool tree = s.group < s.parts;
+    // level 0: of the group's CTAs; level 1: of the groups, or of all CTAs
+    for (int level = tree ? 0 : 1; level < 2; ++level) {
+        unsigned long long* word = p.arrived + (level ? s.c0 : p.ctas + s.first);
+        const int n = !level ? s.in_group : tree ? s.groups() : s.parts;
+        if (threadIdx.x == 0) {
+            last = count_in(word, seen[level ? 0 : 1], p.nonce) == n;
+            if (last) *word = 0;
+        }
+        sync();
+        if (!last) return;
+        join_parts<D, kRows, T, kBf16>(p, wt, row_ml, s.c0, level ? s.c0 : s.first, level && tree ? s.group : 1, n, level == 1, rows,
+                                       row0, v_descale, sync);
+        sync();
     }
 }
 
@@ -1350,9 +1404,9 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
             const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
             const bool split = seg0 < static_cast<int>(blockIdx.x) * per || seg1 > cur.end;
             const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
-            if (split && tid == 0)   // read ahead; in place when the tiles are done
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.counter)),
-                             "l"(p.arrived + c0)
+            if (split && tid < 2)   // read ahead; in place when the tiles are done
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.seen[tid])),
+                             "l"(p.arrived + (tid ? p.ctas + Split(c0, c1).first : c0))
                              : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;
@@ -1452,19 +1506,9 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
             if (more) stage_q<D, NR, kBf16>(p, sm, nxt.hr, k_descale);
             __syncthreads();
 
-            if (split) {
-                const int parts = c1 - c0 + 1;
-                if (tid == 0) {
-                    sm.last = count_in(p.arrived + c0, sm.counter, p.nonce) == parts;
-                    if (sm.last) p.arrived[c0] = 0;
-                }
-                __syncthreads();
-                if (sm.last) {
-                    join_parts<D, kRows, T, kBf16>(p, sm.o[0], sizeof(sm.o) / 4, sm.row_ml, c0, parts, rows, row0, v_descale,
-                                                     [] { __syncthreads(); });
-                    __syncthreads();
-                }
-            }
+            if (split)
+                finish_part<D, kRows, T, kBf16>(p, c0, c1, sm.seen, sm.last, sm.o[0], sm.row_ml, rows, row0, v_descale,
+                                                [] { __syncthreads(); });
             if (!more) break;
             cur = nxt;
         }

@@ -20,7 +20,7 @@
 // which has a place of its own, while this tile's values and weights are; O^T
 // while the next but one's keys are.
 //
-// 38 sequences of 8192 tokens, 8 KV heads of 128 (358 MB): 122, 137 and 164 us
+// 38 sequences of 8192 tokens, 8 KV heads of 128 (358 MB): 121, 137 and 169 us
 // for 32, 48 and 64 rows, where the kernel on mma.sync takes 138 us for 32. Without
 // the conversions and weights the same loop takes 68 us, without V's alone 90 us,
 // without K's 105 us: issue slots are 59% busy, 4245 instructions a tile of 128
@@ -58,7 +58,7 @@ struct Smem {
     int off[N], mx[N];
     int nan_first[D / 16];                       // first token with a NaN among its values, by scale group
     alignas(8) uint32_t ok[4][2];                // usable 16-token blocks of the last tiles loaded: the first bit of each byte
-    unsigned long long bar[12], counter;
+    unsigned long long bar[12], seen[2];         // seen: as in the other kernel
     uint32_t tmem;
     int abort, last;
 };
@@ -440,9 +440,9 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
             const int seg0 = cur.u - cur.tile, seg1 = seg0 + (pad == 1 ? cur.tiles : padded(cur.tiles, pad));
             const bool split = seg0 < static_cast<int>(blockIdx.x) * per || seg1 > cur.end;
             const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
-            if (split && tid == 0)   // read ahead; in place when the tiles are done
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.counter)),
-                             "l"(p.arrived + c0)
+            if (split && tid < 2)   // read ahead; in place when the tiles are done
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.seen[tid])),
+                             "l"(p.arrived + (tid ? p.ctas + Split(c0, c1).first : c0))
                              : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;
@@ -652,19 +652,9 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
             ptx::tc_fence_before();
             work_sync();
 
-            if (split) {
-                const int parts = c1 - c0 + 1;
-                if (tid == 0) {
-                    sm.last = count_in(p.arrived + c0, sm.counter, p.nonce) == parts;
-                    if (sm.last) p.arrived[c0] = 0;
-                }
-                work_sync();
-                if (sm.last) {
-                    join_parts<D, N, kThreads, kBf16>(p, reinterpret_cast<float*>(sm.v[0]), sizeof(sm.v[0]) / 4, sm.row_ml, c0,
-                                                      parts, rows, row0, v_descale, [] { work_sync(); });
-                    work_sync();
-                }
-            }
+            if (split)
+                finish_part<D, N, kThreads, kBf16>(p, c0, c1, sm.seen, sm.last, reinterpret_cast<float*>(sm.v[0]), sm.row_ml, rows,
+                                                   row0, v_descale, [] { work_sync(); });
             if (!more) break;
             cur = nxt;
         }

@@ -960,3 +960,41 @@ def test_idle_request_of_more_elements_than_32_bits_count(gpu_lib):
     del q
     assert lse.isneginf().all()
     assert all(not part.any() for part in o[0])
+
+
+@pytest.mark.parametrize("B,Hkv,n,page", [(1, 1, 300011, 128), (1, 2, 40000, 16), (2, 3, 33000, 64)])
+@pytest.mark.parametrize("Hq,Nq,d", [(1, 1, 64), (8, 1, 128), (16, 1, 64), (20, 1, 128), (8, 5, 128), (13, 7, 64)])
+def test_parts_joined_in_groups(gpu_lib, B, Hkv, n, page, Hq, Nq, d):
+    """Contexts so long that a row block has dozens of parts, 292 at most.
+    All tokens lie in one page that every table entry names, so that 64 bits are
+    quick: the softmax's sums run over its tokens, each counted."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(B + n + Hq + Nq + d)
+    cache = make_cache(rng, 1, Hkv, page, d)
+    lens = [n - 777 * b for b in range(B)]
+    table = np.zeros((B, -(-n // page)), np.int64)
+    q = torch.tensor(rng.standard_normal((B, Hq * Hkv, Nq, d))).to(torch.bfloat16)
+    one = np.ones(Hkv, np.float32)
+    args = (q.cuda(), torch.tensor(cache).cuda(), i32(table), i32(lens), torch.tensor(one).cuda(), torch.tensor(one).cuda())
+    o, lse = fa2.fa2_fwd_kv4(*args, causal=True)
+    again = fa2.fa2_fwd_kv4(*args, causal=True)
+    ok(fa2)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    o, lse, qd = o.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    keys, values = context(cache, np.zeros((1, 1), int), [page], d, one, one)
+    for b in range(B):
+        for h in range(Hq * Hkv):
+            k, v = keys[0][h // Hq], values[0][h // Hq]
+            for i in range(Nq):
+                m = lens[b] + i + 1 - Nq
+                count = m // page + (np.arange(page) < m % page)
+                s = d ** -0.5 * (k @ qd[b, h, i])
+                w = count * np.exp(s - s.max())
+                ref, lref = w @ v / w.sum(), s.max() + math.log(w.sum())
+                A = w @ np.abs(v) / w.sum()
+                big = d ** -0.5 * (np.abs(k) @ np.abs(qd[b, h, i])).max()
+                e = (d + 8) * 2.0 ** -23 * big + 4 * 2.0 ** -23 * abs(lref) + 2.0 ** -21
+                r = (m / 8 + 64) * 2.0 ** -23
+                bound = (2.0 ** -11 + 2 * e + r) * A + 2.0 ** -32 * m * np.abs(v).max() + U["bf16"] * np.abs(ref)
+                assert np.all(np.abs(o[b, h, i] - ref) <= bound)
+                assert abs(lse[b, h, i] - lref) <= e + r + 2.0 ** -22 * abs(lref)
