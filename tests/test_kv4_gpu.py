@@ -998,3 +998,53 @@ def test_parts_joined_in_groups(gpu_lib, B, Hkv, n, page, Hq, Nq, d):
                 bound = (2.0 ** -11 + 2 * e + r) * A + 2.0 ** -32 * m * np.abs(v).max() + U["bf16"] * np.abs(ref)
                 assert np.all(np.abs(o[b, h, i] - ref) <= bound)
                 assert abs(lse[b, h, i] - lref) <= e + r + 2.0 ** -22 * abs(lref)
+
+
+@pytest.mark.parametrize("Hq,Nq", [(2, 1), (20, 1), (13, 3)])
+def test_longest_table_and_context(gpu_lib, Hq, Nq):
+    """Positions just below 2^31, all in one page of equal tokens: O is their
+    value, LSE their score and the logarithm of their number. Every weight is 2^7
+    up to 2^-21 of it, and fewer than 2^24 of them go into a sum one by one, so
+    sums are as good."""
+    fa2 = gpu_lib
+    page, d, W = 128, 64, 2 ** 24 - 3
+    n = W * page - 41
+    cache = np.zeros((1, 1, 2, page * (d // 2 + d // 16)), np.uint8)
+    cache[..., : page * d // 2] = 0x22                   # 1.0
+    cache[..., page * d // 2:] = 0x38                    # 1.0
+    q = torch.full((1, Hq, Nq, d), 0.125)
+    q[:, ::2] *= -1
+    table = torch.zeros((1, W), dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    o, lse = fa2.fa2_fwd_kv4(q.bfloat16().cuda(), torch.tensor(cache).cuda(), table, i32([n]), one, one * 3, scale=0.25,
+                             causal=True)
+    ok(fa2)
+    assert torch.all(o == 3)
+    m = n + torch.arange(Nq, dtype=torch.float64) + 1 - Nq
+    want = m.log() + torch.where(torch.arange(Hq) % 2 == 0, -2.0, 2.0).double()[:, None]
+    assert (lse[0].double().cpu() - want).abs().max() <= 8 * 2.0 ** -23 * 24
+
+
+def test_table_rows_of_millions_of_pages(gpu_lib):
+    """The second row of a table lies 64 MB behind the first; a table that would
+    need more tiles than are counted is refused."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(66)
+    page, d, W, lens = 128, 128, 2 ** 24 - 3, [300, 170]
+    small, P = make_tables(rng, lens, page)
+    table = torch.full((2, W), -1, dtype=torch.int32, device="cuda")
+    table[:, : small.shape[1]] = i32(small)
+    for Hkv, G in ((4, 1), (2, 20)):
+        cache = torch.tensor(make_cache(rng, P, Hkv, page, d)).cuda()
+        one = torch.ones(Hkv, device="cuda")
+        q = torch.tensor(rng.standard_normal((2, Hkv * G, 1, d))).to(torch.bfloat16).cuda()
+        a = fa2.fa2_fwd_kv4(q, cache, table, i32(lens), one, one)
+        b = fa2.fa2_fwd_kv4(q, cache, i32(small), i32(lens), one, one)
+        ok(fa2)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        ka, kb = (fa2.fa2_kv4_gather(cache, t, i32(lens), one, one, 300, d)[0] for t in (table, i32(small)))
+        assert torch.equal(ka, kb)
+    many = torch.zeros(fa2.fa2_kv4_cache_shape(1, 32, page, d), dtype=torch.uint8, device="cuda")
+    with pytest.raises(fa2.FA2Error):
+        fa2.fa2_fwd_kv4(torch.zeros(2, 32, 1, d, dtype=torch.bfloat16, device="cuda"), many, table, i32(lens),
+                        torch.ones(32, device="cuda"), torch.ones(32, device="cuda"))
