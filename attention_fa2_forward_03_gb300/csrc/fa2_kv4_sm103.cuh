@@ -1245,21 +1245,31 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
 
 // A segment's CTAs c0 .. c1, and how their partial results are joined: at once
 // by the last of them to be done, or, where there are many, those of `group`
-// neighbours by the last of these, and the groups' results by the last of all:
-// one request of 262139 tokens, 4 heads, takes 38 us (41 us with 74 parts joined
-// at once), with 40 rows a head 86 us (125 us).
+// neighbours by the last of these (level 0), and the groups' results by the last
+// of all (level 1): one request of 262139 tokens, 4 heads, takes 38 us (41 us with
+// 74 parts joined at once), with 40 rows a head 86 us (125 us).
 struct Split {
-    int c0, parts, group, first, in_group;   // first CTA of this CTA's group, CTAs in it
-    __device__ __forceinline__ Split(int begin, int end) : c0(begin), parts(end - begin + 1) {
+    int c0, parts, group, first, in_group;   // first CTA of CTA `cta`'s group, CTAs in it
+    __host__ __device__ __forceinline__ Split(int begin, int end, int cta) : c0(begin), parts(end - begin + 1) {
         group = parts;
         if (parts > kJoinAtOnce) {
             group = 4;
             while (group * group < parts) ++group;
         }
-        first = c0 + (static_cast<int>(blockIdx.x) - c0) / group * group;
-        in_group = min(group, c0 + parts - first);
+        first = c0 + (cta - c0) / group * group;
+        in_group = c0 + parts - first < group ? c0 + parts - first : group;
     }
-    __device__ __forceinline__ int groups() const { return (parts + group - 1) / group; }
+    __host__ __device__ __forceinline__ bool tree() const { return group < parts; }
+    __host__ __device__ __forceinline__ int groups() const { return (parts + group - 1) / group; }
+    // The level at which the CTA begins, the counter of a level, and the
+    // count at which all are done. A group of one has its result in place and is
+    // not counted: its CTA may begin the next segment, whose first group would
+    // count on the same word. Any other group's first CTA goes on to the next
+    // CTA within the segment, and so does c0, which no two segments can: each
+    // word has one segment.
+    __host__ __device__ __forceinline__ int begins() const { return tree() && in_group > 1 ? 0 : 1; }
+    __host__ __device__ __forceinline__ int word(int level, int ctas) const { return level ? c0 : ctas + first; }
+    __host__ __device__ __forceinline__ int count(int level) const { return !level ? in_group : tree() ? groups() : parts; }
 };
 
 // Joins `n` partial results of a row block, those of CTAs from, from + step, ..,
@@ -1350,19 +1360,17 @@ __device__ __forceinline__ void join_parts(const FwdParams& p, float* wt, float 
 template <int D, int kRows, int T, bool kBf16, typename Sync>
 __device__ __forceinline__ void finish_part(const FwdParams& p, int c0, int c1, const unsigned long long (&seen)[2], int& last,
                                             float* wt, float (*row_ml)[2], int rows, long long row0, float v_descale, Sync sync) {
-    const Split s(c0, c1);
-    const bool tree = s.group < s.parts;
-    // level 0: of the group's CTAs; level 1: of the groups, or of all CTAs
-    for (int level = tree ? 0 : 1; level < 2; ++level) {
-        unsigned long long* word = p.arrived + (level ? s.c0 : p.ctas + s.first);
-        const int n = !level ? s.in_group : tree ? s.groups() : s.parts;
+    const Split s(c0, c1, static_cast<int>(blockIdx.x));
+    for (int level = s.begins(); level < 2; ++level) {
+        unsigned long long* word = p.arrived + s.word(level, p.ctas);
+        const int n = s.count(level);
         if (threadIdx.x == 0) {
             last = count_in(word, seen[level ? 0 : 1], p.nonce) == n;
             if (last) *word = 0;
         }
         sync();
         if (!last) return;
-        join_parts<D, kRows, T, kBf16>(p, wt, row_ml, s.c0, level ? s.c0 : s.first, level && tree ? s.group : 1, n, level == 1, rows,
+        join_parts<D, kRows, T, kBf16>(p, wt, row_ml, s.c0, level ? s.c0 : s.first, level && s.tree() ? s.group : 1, n, level == 1, rows,
                                        row0, v_descale, sync);
         sync();
     }
@@ -1406,7 +1414,7 @@ __global__ void __launch_bounds__(Shape<NR>::kThreads, Shape<NR>::kCtas) fa2_kv4
             const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
             if (split && tid < 2)   // read ahead; in place when the tiles are done
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.seen[tid])),
-                             "l"(p.arrived + (tid ? p.ctas + Split(c0, c1).first : c0))
+                             "l"(p.arrived + Split(c0, c1, static_cast<int>(blockIdx.x)).word(1 - tid, p.ctas))
                              : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;

@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kAll, 2) fa2_kv4_fwd_tc_kernel(const FwdParams
             const int c0 = split ? seg0 / per : 0, c1 = split ? (seg1 - 1) / per : 0;
             if (split && tid < 2)   // read ahead; in place when the tiles are done
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_addr(&sm.seen[tid])),
-                             "l"(p.arrived + (tid ? p.ctas + Split(c0, c1).first : c0))
+                             "l"(p.arrived + Split(c0, c1, static_cast<int>(blockIdx.x)).word(1 - tid, p.ctas))
                              : "memory");
             const float v_descale = p.v_descale[h];
             Cursor nxt = cur;
