@@ -386,6 +386,51 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Where in the ring the page lies that comes `at` places behind page 0's.
+__device__ __forceinline__ int ring_place(long long at, int num_pages) {
+    if (at >= num_pages) at -= num_pages;   // below 3 num_pages in a sane ring
+    if (at >= num_pages) at -= num_pages;
+    if (at >= num_pages) at %= num_pages;
+    return static_cast<int>(at);
+}
+
+// Writes the pages of the n requests at table row `rows` that end into the ring from
+// place `behind` on without the ids outside the cache among them, the pages
+// behind such an id moving up; returns how many pages there are. A call of its
+// own, for a table that holds such an id. s_page is unused by requests that end.
+template <int T>
+__device__ __noinline__ long long release_usable(const int* rows, int* free_pages, int max_pages, int log2_page, int num_pages, int n,
+                                                 const int* s_len, const int* s_add, int* s_page, int* s_back,
+                                                 long long (*sm)[T / 32], long long behind) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int pass = 0; pass < 2; ++pass) {   // counts them, then writes them
+        for (int q = warp; q < n; q += T / 32) {
+            if (s_add[q] >= 0) continue;
+            const int have = (s_len[q] + (1 << log2_page) - 1) >> log2_page;
+            const int* row = rows + static_cast<long long>(q) * max_pages;
+            int kept = 0;
+            for (int j = lane; j < (have + 31) / 32 * 32; j += 32) {
+                const int id = j < have ? row[j] : -1;
+                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(num_pages);
+                const unsigned mask = __ballot_sync(~0u, good);
+                if (pass && good)
+                    free_pages[ring_place(static_cast<long long>(s_back[q]) + kept + __popc(mask & ((1u << lane) - 1)), num_pages)] = id;
+                kept += __popc(mask);
+            }
+            if (!pass && lane == 0) s_page[q] = kept;
+        }
+        if (pass) break;
+        __syncthreads();
+        long long kept = tid < n && s_add[tid] < 0 ? s_page[tid] : 0, none = 0, all, unused;
+        block_scan2<T>(kept, none, all, unused, sm);
+        s_back[tid] = ring_place(behind + kept, num_pages);
+        __syncthreads();
+        if (tid == 0) sm[0][0] = all;   // every thread's copy need not live through the second pass
+    }
+    __syncthreads();
+    return sm[0][0];
+}
+
 // Every CTA scans the requests in order, T at a time, so that each knows where
 // every request's pages lie in the ring; then they share the writing. Where
 // outputs are the inputs the CTAs are one cluster, whose barrier lies between. A
@@ -432,11 +477,7 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
         s_len[tid] = len;
         s_add[tid] = ends ? -1 : granted ? add : 0;
         s_page[tid] = granted ? static_cast<int>(first + want + a) : 0;   // of its first new page in the ring; < 2 num_pages if it has one
-        long long behind = first + static_cast<long long>(count) + back + r;   // below 3 num_pages in a sane ring
-        if (behind >= p.num_pages) behind -= p.num_pages;
-        if (behind >= p.num_pages) behind -= p.num_pages;
-        if (behind >= p.num_pages) behind %= p.num_pages;
-        s_back[tid] = static_cast<int>(behind);
+        s_back[tid] = ring_place(first + static_cast<long long>(count) + back + r, p.num_pages);
         // those that got pages are the first of those that wanted any
         taken = want + a_all <= count ? want + a_all : taken;
         const bool cut = want <= count && want + a_all > count;
@@ -447,7 +488,6 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
             taken += want;
         }
         want += a_all;
-        back += r_all;
         __syncthreads();
         if (p.in_place) cluster_sync();
 
@@ -513,14 +553,17 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
                 }
             }
         }
-        // pages of requests that end, a warp each
-        if (r_all > 0) {
-            unsigned seen = 0, turn = rank * (T / 32) + warp;   // requests that end, so far; the next that is this warp's
+        // Pages of requests that end, a warp each, by the CTA that also writes
+        // the ring's state. An id outside the cache is reported and does not join the
+        // ring; it is seen when the others have been written, which is then done again.
+        bool odd = false;
+        if (r_all > 0 && rank == 0) {
+            unsigned seen = 0, turn = warp;   // requests that end, so far; the next that is this warp's
             for (int q0 = 0; q0 < n; q0 += 32) {
                 unsigned who = __ballot_sync(~0u, q0 + lane < n && s_add[min(q0 + lane, T - 1)] < 0);
                 for (; who; who &= who - 1, ++seen) {
                     if (seen != turn) continue;
-                    turn += ranks * (T / 32);
+                    turn += T / 32;
                     const int q = q0 + __ffs(who) - 1, have_q = (s_len[q] + p.page - 1) >> p.log2_page;
                     const int* row = p.block_table + static_cast<long long>(b0 + q) * p.max_pages;
                     for (int j0 = lane; j0 < have_q; j0 += 128) {
@@ -535,12 +578,19 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
                                 if (k >= p.num_pages) k -= p.num_pages;
                                 if (k >= p.num_pages) k %= p.num_pages;   // more pages than there are
                                 p.free_pages[k] = pg[j];
+                                odd |= static_cast<unsigned>(pg[j]) >= static_cast<unsigned>(p.num_pages);
                             }
                     }
                 }
             }
         }
-        __syncthreads();
+        if (__syncthreads_or(odd)) {
+            if (tid == 0) report(kSitePage);
+            r_all = release_usable<T>(p.block_table + static_cast<long long>(b0) * p.max_pages, p.free_pages, p.max_pages, p.log2_page,
+                                      p.num_pages, n, s_len, s_add, s_page, s_back, sm, first + static_cast<long long>(count) + back);
+            __syncthreads();
+        }
+        back += r_all;
     }
     if (tid == 0 && rank == 0) {
         long long left = count - taken + back;

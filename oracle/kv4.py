@@ -114,8 +114,9 @@ def plan(seq_lens, new_lens, table, ring, state, page, N):
         have = -(-n // page)
         if add < 0:
             for j in range(have):
-                ring[(first + count + back) % P] = table[b, j]
-                back += 1
+                if 0 <= table[b, j] < P:   # an id outside the cache does not join the ring
+                    ring[(first + count + back) % P] = table[b, j]
+                    back += 1
             seq_lens[b] = 0
             continue
         if add > N or n + add > W * page:
