@@ -692,6 +692,21 @@ int kv4_block(long long rows) {
 constexpr bool kv4_on_tc(int block) { return block > 24; }
 constexpr int kv4_ctas_per_sm(int block) { return block == 8 || kv4_on_tc(block) ? 2 : 1; }
 
+// Sizes that the attention takes.
+fa2_status kv4_check_sizes(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size) {
+    if (B <= 0 || H_q <= 0 || H_kv <= 0 || N_q <= 0 || d <= 0 || H_q % H_kv != 0) return FA2_ERR_INVALID_ARG;
+    const fa2_status st = kv4_check_pages(page_size, 1, max_pages);
+    if (st != FA2_OK) return st;
+    if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    if (static_cast<long long>(B) * H_q > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit,
+    if (H_kv > 65535 / 2) return FA2_ERR_UNSUPPORTED;                                             // and a page's bytes,
+    // and units of the line of tiles, which padding can double
+    const long long rows = static_cast<long long>(H_q / H_kv) * N_q, block = kv4_block(rows);
+    const long long segments = static_cast<long long>(B) * H_kv * ((rows + block - 1) / block);
+    if (segments * ((static_cast<long long>(max_pages) * page_size + 31) / 32) > (1LL << 30)) return FA2_ERR_UNSUPPORTED;
+    return FA2_OK;
+}
+
 // The CTAs that can have work: runs have kMinRun tiles or more, and a padded
 // line has at most one run for each segment beyond those.
 long long kv4_ctas(long long segments, long long max_tokens, long long most) {
@@ -744,9 +759,7 @@ fa2_status kv4_launch(int dev, fa2::kv4::FwdParams p, cudaStream_t stream) {
     const fa2_status st = set_smem(dev, slot, kern, kSmem);
     if (st != FA2_OK) return st;
     p.rblocks = (p.rows + kRows - 1) / kRows;
-    // units of the line are 32-bit, and padding can double them
     const long long segments = static_cast<long long>(p.B) * p.hkv * p.rblocks;
-    if (segments * ((p.max_tokens + 31LL) / 32) > (1LL << 30)) return FA2_ERR_UNSUPPORTED;
     p.ctas = static_cast<int>(kv4_ctas(segments, p.max_tokens, std::min(sm_count(dev) * kPerSm, fa2::kv4::kMaxCtas)));
     // Without a workspace every segment needs a CTA, also where they run in waves.
     if (!p.part_o) p.ctas = std::max(p.ctas, static_cast<int>(segments));
@@ -926,9 +939,7 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
 }
 
 int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size) {
-    if (B <= 0 || H_q <= 0 || H_kv <= 0 || N_q <= 0 || H_q % H_kv != 0 || (d != 64 && d != 128) ||
-        kv4_check_pages(page_size, 1, max_pages) != FA2_OK)
-        return -1;
+    if (kv4_check_sizes(B, H_q, H_kv, N_q, d, max_pages, page_size) != FA2_OK) return -1;
     return kv4_workspace(B, H_kv, static_cast<long long>(H_q / H_kv) * N_q, d,
                          static_cast<long long>(max_pages) * page_size);
 }
@@ -950,10 +961,7 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     if (causal != 0 && causal != 1) return FA2_ERR_INVALID_ARG;
     fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
     if (st != FA2_OK) return st;
-    if (d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
-    const long long heads = static_cast<long long>(B) * H_q;
-    if (heads > (0x7FFFFFFFLL - 64) / N_q) return FA2_ERR_UNSUPPORTED;   // row indices are 32-bit,
-    if (H_kv > 65535 / 2) return FA2_ERR_UNSUPPORTED;                    // and a page's bytes
+    if ((st = kv4_check_sizes(B, H_q, H_kv, N_q, d, max_pages, page_size)) != FA2_OK) return st;
     const int64_t need = fa2_fwd_kv4_workspace(B, H_q, H_kv, N_q, d, max_pages, page_size);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FA2_ERR_INVALID_ARG;
     int dev = 0;
