@@ -4,7 +4,9 @@
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -22,8 +24,9 @@ DEPENDS = SOURCES + [os.path.join(CSRC, "ptx_sm103.cuh"), os.path.join(CSRC, "fa
                      os.path.join(CSRC, "fa2_fwd_d64_sm103.cuh"), os.path.join(CSRC, "fa2_kv4_sm103.cuh"),
                      os.path.join(CSRC, "fa2_kv4_tc_sm103.cuh"),
                      os.path.join(INCLUDE, "fa2.h")]
-# The extension that passes torch tensors to the KV cache entry points (host code only).
+# The extension that passes torch tensors to the KV cache entry points (host code only), and the torch it was built for.
 TORCH_LIB = os.path.join(PKG, "_kv4_torch.so")
+TORCH_STAMP = TORCH_LIB + ".for"
 TORCH_SOURCES = [os.path.join(CSRC, "kv4_torch.cpp")]
 TORCH_DEPENDS = TORCH_SOURCES + [os.path.join(INCLUDE, "fa2.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,18 +37,45 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def installed_torch():
+    """(version, folder) of the torch that the extension is built against,
+    found without importing it; None without torch or its headers."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except ValueError:
+        spec = None
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    if not os.path.exists(os.path.join(root, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return None
+    return str(runpy.run_path(os.path.join(root, "version.py"))["__version__"]), root
+
+
+def built_for():
+    """Version of the torch that the extension was built for; None if there is none."""
+    try:
+        with open(TORCH_STAMP) as f:
+            return f.read().strip()
+    except OSError:
+        return None
+
+
 def needs_build(lib: str = LIB) -> bool:
+    if lib == TORCH_LIB:
+        torch = installed_torch()
+        if torch is None:
+            return False
+        if torch[0] != built_for():
+            return True
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
     return any(os.path.getmtime(f) > t for f in (TORCH_DEPENDS if lib == TORCH_LIB else DEPENDS))
 
 
-def torch_command(out: str) -> list:
-    """g++ command of the extension, against the installed torch."""
-    import torch
-
-    root = os.path.dirname(torch.__file__)
+def torch_command(out: str, root: str) -> list:
+    """g++ command of the extension, against the torch in `root`."""
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, "-I", os.path.join(root, "include"), "-I",
             os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"), "-I",
@@ -56,12 +86,9 @@ def torch_command(out: str) -> list:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile libfa2.so, libfa2_debug.so and the torch extension next to this
     file (in parallel) if they are missing or stale; returns the release
-    library's path."""
+    library's path. The C libraries need nvcc alone: without torch there is no
+    extension, and one that does not compile leaves them in place."""
     jobs = []
-    if force or needs_build(TORCH_LIB):
-        tmp = TORCH_LIB + f".tmp{os.getpid()}"
-        cmd = torch_command(tmp)
-        jobs.append((subprocess.Popen(cmd), tmp, TORCH_LIB, cmd))
     for lib, extra in ((LIB, []), (DEBUG_LIB, ["-DFA2_DEBUG"])):
         if not force and not needs_build(lib):
             continue
@@ -71,10 +98,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         jobs.append((subprocess.Popen(cmd), tmp, lib, cmd))
+    torch = installed_torch()
+    if torch is not None and (force or needs_build(TORCH_LIB)):
+        tmp = TORCH_LIB + f".tmp{os.getpid()}"
+        cmd = torch_command(tmp, torch[1])
+        jobs.append((subprocess.Popen(cmd), tmp, TORCH_LIB, cmd))
+    failed = None
     for proc, tmp, lib, cmd in jobs:
         if proc.wait() != 0:
-            raise subprocess.CalledProcessError(proc.returncode, cmd)
+            failed = failed or subprocess.CalledProcessError(proc.returncode, cmd)
+            continue
         os.replace(tmp, lib)
+        if lib == TORCH_LIB:
+            with open(TORCH_STAMP, "w") as f:
+                f.write(torch[0] + "\n")
+    if failed:
+        raise failed
     return LIB
 
 

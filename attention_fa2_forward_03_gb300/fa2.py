@@ -417,10 +417,13 @@ def _kv4():
 
         import torch  # before the extension, which resolves against its libraries
 
+        from . import build
+
         lib = load()
-        if not os.path.exists(KV4_TORCH_LIB):
-            raise ImportError(f"extension {KV4_TORCH_LIB} is missing: run __graft_entry__.build() "
-                              "(python -m attention_fa2_forward_03_gb300.build)")
+        made = build.built_for() if os.path.exists(KV4_TORCH_LIB) else None
+        if made != torch.__version__:
+            raise ImportError(f"extension {KV4_TORCH_LIB} is {f'built for torch {made}' if made else 'missing'}, torch is "
+                              f"{torch.__version__}: run __graft_entry__.build() (python -m attention_fa2_forward_03_gb300.build)")
         loader = importlib.machinery.ExtensionFileLoader("_kv4_torch", KV4_TORCH_LIB)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kv4_torch", loader))
         loader.exec_module(mod)
