@@ -453,7 +453,7 @@ def fa2_kv4_plan(seq_lens, new_lens, block_table, free_pages, free_state, page_s
 def fa2_kv4_append(k, v, slots, cache, k_descale, v_descale, stream=None):
     """Quantises k, v [B, Hkv, N, d] (any strides that are multiples of 8
     elements, rows of adjacent elements) into the slots [B, N] of the cache;
-    negative slots are skipped. Returns the cache."""
+    negative slots are skipped, no other may occur twice. Returns the cache."""
     out = (_kv4_mod or _kv4()).append(k, v, slots, cache, k_descale, v_descale, stream)
     if type(out) is int:
         raise FA2Error(out, "fa2_kv4_append")

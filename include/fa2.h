@@ -294,8 +294,9 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
  *            strides of request, head and token are given in elements
  *            (multiples of 8, 0 .. 2^31 - 8) so that views of a
  *            projection's output need no copy
- *   slots  : [B, N] int32; a negative slot is skipped. A slot named twice in
- *            one call holds, 16 elements by 16 elements, either token
+ *   slots  : [B, N] int32; a negative slot is skipped. A slot may be named
+ *            once in a call: two tokens written to one slot at the same time
+ *            leave codes of the one beside scales of the other
  * For each 16 elements x: scale = e4m3(max|x| / (6 descale)), t = scale *
  * descale in fp32, code = e2m1(x / t), every rounding to nearest, ties to
  * even, limited to the format's largest value; t = 0 gives codes 0. 16
