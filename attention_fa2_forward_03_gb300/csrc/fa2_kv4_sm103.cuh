@@ -7,7 +7,10 @@
 // [page, D/16]. Element = code * scale * descale[head]. A product code * scale
 // has at most six significant bits and lies in [2^-10, 2688], so it is exact in
 // fp16: both matrix products of the attention run on fp16 operands whatever
-// the type of q, and the cache costs no precision beyond its own rounding.
+// the type of q, and the cache costs no precision beyond its own rounding. The
+// softmax's weights are the other operand of the second product and become fp16
+// too, 2^-11 of each (bf16 would be 2^-8): as fp32 they would take a second
+// product for their lower bits.
 #pragma once
 
 #include <cstdint>
@@ -901,8 +904,9 @@ __device__ __forceinline__ void load_q(const FwdParams& p, FwdSmem<D, NR>& sm, i
 
 // Rows of q as B fragments of Q^T (k = d, n = row), in fp16. A bf16 row is
 // scaled by the power of two that brings its largest magnitude into
-// [2^14, 2^15): its 8 bits are kept exactly but for elements below 2^-29 of
-// that magnitude. Thread (g, t) of a warp takes row g and elements
+// [2^14, 2^15): its elements' 8 bits stay as they are down to 2^-17, 2^-31 of that
+// magnitude; below they become multiples of 2^-24, off by 2^-39 of it at most.
+// Thread (g, t) of a warp takes row g and elements
 // [t D/4, (t + 1) D/4): the order of d inside a product is free, and this one
 // lets a thread read a key's codes as one piece.
 template <int D, int NR, bool kBf16>

@@ -336,7 +336,9 @@ fa2_status fa2_kv4_gather(const void* cache, const int32_t* block_table, const i
  * Any N_q >= 1 is right. Up to 64 query rows a KV head (H_q / H_kv * N_q) read
  * the cache once, every 64 more once again; prompts and long chunks of them are
  * faster by fa2_kv4_gather and fa2_fwd_ex.
- * Query rows hold no precision less than q's own; the softmax weights are
+ * Query rows are fp16 for the products: fp16 ones as they are, bf16 ones scaled
+ * by a power of two a row, exactly but for elements below 2^-31 of the row's
+ * largest, which are off by 2^-39 of that at most. The softmax weights are
  * rounded to fp16 (2^-11), sums are fp32. A row of q that is not finite
  * affects no other row. A NaN in the cache affects the rows that see it.
  * B * H_q * N_q < 2^31 - 64, H_kv < 32768, and the blocks of at most 64 rows
