@@ -800,7 +800,8 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
     if (B <= 0 || N <= 0) return FA2_ERR_INVALID_ARG;
     fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
     if (st != FA2_OK) return st;
-    if (static_cast<long long>(B) * N > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
+    // requests are counted in steps of up to 1024, slots in steps of 256
+    if (static_cast<long long>(B) * N > 0x7FFFFFFFLL - 1024) return FA2_ERR_UNSUPPORTED;
     int dev = 0;
     if ((st = check_device(&dev)) != FA2_OK) return st;
     fa2::kv4::PlanParams p{};

@@ -280,8 +280,8 @@ fa2_status fa2_bwd_noalloc(const void* q, const void* k, const void* v, const vo
  * is a ring that is not one. An id outside the cache in the row of a request that
  * ends is reported and does not join the ring; one in the ring itself is reported
  * when it is handed out, and the slots on it are -1. A page that two requests
- * share must be given back once only. One launch; calls that share a ring must be
- * ordered.
+ * share must be given back once only. B * N < 2^31 - 1024. One launch; calls that
+ * share a ring must be ordered.
  */
 fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
                         int32_t* free_pages, const int32_t* free_state, int32_t* seq_lens_out,

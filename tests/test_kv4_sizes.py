@@ -1,5 +1,6 @@
 """Sizes that the attention over the 4-bit cache refuses: fa2_fwd_kv4 and
-fa2_fwd_kv4_workspace say the same, before any device is touched (CPU only)."""
+fa2_fwd_kv4_workspace say the same, before any device is touched; and those that
+the plan refuses (CPU only)."""
 import pytest
 
 from attention_fa2_forward_03_gb300 import build, fa2
@@ -35,3 +36,9 @@ def test_what_the_forward_refuses_needs_no_workspace(B, Hq, Hkv, Nq, d, max_page
 ])
 def test_the_largest_sizes_have_a_workspace(B, Hq, Hkv, Nq, d, max_pages, page):
     assert fa2.fa2_fwd_kv4_workspace(B, Hq, Hkv, Nq, d, max_pages, page) >= 0
+
+
+@pytest.mark.parametrize("B,N", [(2 ** 31 - 1, 1), (2 ** 31 - 1023, 1), (1, 2 ** 31 - 1), (1, 2 ** 31 - 1023), (2, 2 ** 30 - 511)])
+def test_plan_refuses_counts_that_its_steps_would_carry_past_32_bits(B, N):
+    """The kernel counts requests by up to 1024 and slots by 256 in 32 bits."""
+    assert fa2.fa2_kv4_plan_ptr(*[A] * 9, B, N, 10, 64, 100) == UNS
