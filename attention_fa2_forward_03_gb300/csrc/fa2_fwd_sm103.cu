@@ -820,9 +820,12 @@ fa2_status fa2_kv4_plan(const int32_t* seq_lens, const int32_t* new_lens, int32_
     p.page = page_size;
     p.log2_page = log2_of(page_size);
     p.num_pages = num_pages;
-    // 256 threads for a decoding step, whose scan is the shorter one. Where
-    // there are thousands of slots, a warp for every 256 (48 prompts of 16384:
-    // 7.6 us; 18 by a cluster of eight CTAs, which writing in place asks for).
+    // 256 threads for a decoding step, whose scan is the shorter one: 256 requests of
+    // one token take 2.9 us (3.8 with 1024 threads), of four 4.2 (3.9); 512 of one take
+    // 4.6 us (4.0). One CTA up to 8192 slots: by a CTA for every 1024 slots 16 requests of
+    // 512 take the same 4.4 us (512 of 16: 4.0 instead of 7.2); 32 of 512 take 5.8 by one
+    // CTA and 4.4 by more. Above, a warp for every 256 slots: 48 prompts of 16384 take
+    // 5.2 us (120 by one CTA; 20.9 by a cluster of eight, which writing in place asks for).
     const long long all = static_cast<long long>(B) * N;
     auto in = [](const void* a, const void* out, long long n) {
         const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(out);

@@ -91,8 +91,9 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float* x) {
 // For each 16 elements: scale s = e4m3(max|x| / (6 descale)), t = s descale,
 // code = e2m1(x / t). A row is 2 D bytes in and 9 D / 16 out. 262112 rows of 128
 // of keys and of values (4 prompts of 8191 tokens, 8 heads) take 42 us, 4.1 TB/s,
-// 60% of a plain copy's rate: what bounds it is instructions, a quotient rounded
-// to nearest and a conversion for every element, in 71% of the issue slots.
+// 60% of a plain copy's rate: what bounds it is instructions, about 130 for the eight
+// elements that a lane has of one part (24 of them quotients), in 71% of the issue
+// slots.
 struct AppendParams {
     const void* x[2];          // keys, values
     int sb[2], sh[2], sn[2];   // strides in elements: request, head, token
@@ -440,8 +441,8 @@ __device__ __noinline__ long long release_usable(const int* rows, int* free_page
 // request gets its pages iff the pages wanted up to and including it are free
 // (or it needs none); pages of requests that end join the ring behind its last
 // page and are not handed out by this call. Bound by latency, three dependent
-// reads, and by the launch: 7 us from call to call for a step of 256 requests,
-// 7.6 us for 48 prompts of 16384 tokens (3.4 MB).
+// reads, and by the launch: 2.9 us for a step of 256 requests, 5.1 us where 6% of
+// them end; 5.2 us for 48 prompts of 16384 tokens (3.4 MB), 20.9 us in place.
 template <int T>
 __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
     __shared__ long long sm[2][T / 32];
@@ -610,9 +611,20 @@ __global__ void __launch_bounds__(T) fa2_kv4_plan_kernel(const PlanParams p) {
 
 constexpr int kTile = 32;      // tokens a warp takes at a time
 constexpr int kMaxCtas = 320;  // workspace is sized for this many
-constexpr int kMinRun = 32;    // tiles of 32 a CTA's run has at least
-constexpr int kSpare = 40;     // tiles by which a run may grow so that no segment is split
-constexpr int kJoinAtOnce = 12;   // partial results that are joined at once
+// Tiles of 32 that a CTA's run has at least. With 64, one request of 4096 tokens and
+// 8 heads takes 15.8 us instead of 12.2. With 16, one of 2304 takes 10.0 us instead of
+// 14.6, but one of 8192 with 64 rows a head 41.7 instead of 37.6, and 16 requests of up
+// to 2304 with 64 rows 56 instead of 44.
+constexpr int kMinRun = 32;
+// Tiles by which a run may grow so that no segment is split. With none, 256 segments of
+// up to 2304 tokens, heads of 64, take 20.7 us instead of 15.7, and 128 with 20 rows
+// 34 instead of 22.7; a few segments pay for it: 8 of 2304 tokens take 14.6 us, 12.0
+// with none. With 96, 8 of 4096 take 22 us instead of 12.2.
+constexpr int kSpare = 40;
+// Partial results that are joined at once. With 6, ten parts of 20 rows (16 heads of
+// 65536 tokens) take 64.0 us instead of 62.2; with 24, 19 parts (8 heads) 40.5 instead of
+// 39.0, although of 8 rows (16 heads) 36.4 instead of 37.3.
+constexpr int kJoinAtOnce = 12;
 
 // Attention for up to 24 query rows a KV head, NR blocks of eight: both
 // products on mma.sync, transposed (S^T = K Q^T, O^T += V^T P^T), so that tokens
@@ -1172,8 +1184,9 @@ __device__ __forceinline__ void store_row4(const FwdParams& p, long long row, in
 
 // Requests without a key: O = 0, LSE = -inf, by the T threads of `idle` CTAs a
 // request. Lengths behind the table's end are reported here too. A call, so
-// that the registers of the tiles' loop are not chosen with this in sight
-// (152 sequences of 8192 tokens: 238 us, 242 us inlined).
+// that the registers of the tiles' loop are not chosen with this in sight: 152
+// sequences of 8192 tokens take 231 us either way, one of 512 tokens 7.2 us, inlined
+// 6.8 us.
 template <int D, bool kBf16, int T>
 __device__ __noinline__ void idle_requests(const FwdParams& p) {
     for (int w = blockIdx.x; w < p.B * p.idle; w += gridDim.x) {
@@ -1301,7 +1314,7 @@ __device__ __forceinline__ int count_in(unsigned long long* word, unsigned long 
 // by the last of them to be done, or, where there are many, those of `group`
 // neighbours by the last of these (level 0), and the groups' results by the last
 // of all (level 1): one request of 262139 tokens, 4 heads, takes 38 us (41 us with
-// 74 parts joined at once), with 40 rows a head 86 us (125 us).
+// 74 parts joined at once), with 40 rows a head 85 us (125 us).
 struct Split {
     int c0, parts, group, first, in_group;   // first CTA of CTA `cta`'s group, CTAs in it
     __host__ __device__ __forceinline__ Split(int begin, int end, int cta) : c0(begin), parts(end - begin + 1) {

@@ -20,7 +20,7 @@
 // which has a place of its own, while this tile's values and weights are; O^T
 // while the next but one's keys are.
 //
-// 38 sequences of 8192 tokens, 8 KV heads of 128 (358 MB): 121, 137 and 169 us
+// 38 sequences of 8192 tokens, 8 KV heads of 128 (358 MB): 121, 138 and 169 us
 // for 32, 48 and 64 rows, where the kernel on mma.sync takes 138 us for 32. Without
 // the conversions and weights the same loop takes 68 us, without V's alone 90 us,
 // without K's 105 us: issue slots are 59% busy, 4245 instructions a tile of 128
