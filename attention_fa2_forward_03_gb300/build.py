@@ -22,7 +22,8 @@ DEBUG_LIB = os.path.join(PKG, "libfa2_debug.so")
 SOURCES = [os.path.join(CSRC, "fa2_fwd_sm103.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "ptx_sm103.cuh"), os.path.join(CSRC, "fa2_fwd_sm103.cuh"), os.path.join(CSRC, "fa2_bwd_sm103.cuh"), os.path.join(CSRC, "fa2_fwd_fp8_sm103.cuh"),
                      os.path.join(CSRC, "fa2_fwd_d64_sm103.cuh"), os.path.join(CSRC, "fa2_kv4_sm103.cuh"),
-                     os.path.join(CSRC, "fa2_kv4_tc_sm103.cuh"),
+                     os.path.join(CSRC, "fa2_kv4_tc_sm103.cuh"), os.path.join(CSRC, "fa2_rope_sm103.cuh"),
+                     os.path.join(CSRC, "fa2_kv16_sm103.cuh"),
                      os.path.join(INCLUDE, "fa2.h")]
 # The extension that passes torch tensors to the KV cache entry points (host code only), and the torch it was built for.
 TORCH_LIB = os.path.join(PKG, "_kv4_torch.so")

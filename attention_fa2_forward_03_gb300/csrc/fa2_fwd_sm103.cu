@@ -27,6 +27,8 @@
 #include "fa2_fwd_d64_sm103.cuh"
 #include "fa2_kv4_sm103.cuh"
 #include "fa2_kv4_tc_sm103.cuh"
+#include "fa2_rope_sm103.cuh"
+#include "fa2_kv16_sm103.cuh"
 
 // ==================================================================== host
 
@@ -62,8 +64,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
-// 4-bit cache 20-43.
-constexpr int kKernelSlots = 44;
+// 4-bit cache 20-43, over the 16-bit cache 44-47.
+constexpr int kKernelSlots = 48;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -999,6 +1001,301 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
     if (d == 128)
         return bf ? kv4_launch_rows<128, true>(dev, p, stream) : kv4_launch_rows<128, false>(dev, p, stream);
     return bf ? kv4_launch_rows<64, true>(dev, p, stream) : kv4_launch_rows<64, false>(dev, p, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- rotary positions, the paged 16-bit KV cache
+
+namespace {
+
+// The part of the arguments that the rotation and the append share.
+fa2_status rope_check(const void* positions, const void* inv_freq, const void* axes, int d, int rot_dim, int n_axes,
+                      int interleaved, fa2_dtype dtype) {
+    if (!positions || !inv_freq || !aligned4(positions) || !aligned4(inv_freq) || !aligned4(axes)) return FA2_ERR_INVALID_ARG;
+    if (d <= 0 || rot_dim <= 0 || n_axes <= 0 || (interleaved != 0 && interleaved != 1)) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_BF16 && dtype != FA2_FP16) return FA2_ERR_INVALID_ARG;
+    return FA2_OK;
+}
+bool rope_sizes(int d, int rot_dim, int n_axes) { return (d == 64 || d == 128) && rot_dim <= d && rot_dim % 16 == 0 && n_axes <= 8; }
+
+// Eight tokens a block where that gives every SM four blocks or more: their
+// angles are made eight at a time. Else one, which spreads few tokens wider.
+template <bool kCache>
+fa2_status rope_launch(int dev, const fa2::rope::Params& p, int d, bool bf, cudaStream_t stream) {
+    using namespace fa2::rope;
+    const long long eights = (static_cast<long long>(p.tokens) + 7) / 8;
+    const bool many = eights >= 4LL * sm_count(dev);
+    const long long grid = many ? eights : p.tokens;
+    auto go = [&](auto few, auto many_k) { return kv4_launch_kernel(many ? +many_k : +few, grid, kThreads, 0, stream, p); };
+    if (d == 128)
+        return bf ? go(fa2_rope_kernel<128, true, kCache, 1>, fa2_rope_kernel<128, true, kCache, 8>)
+                  : go(fa2_rope_kernel<128, false, kCache, 1>, fa2_rope_kernel<128, false, kCache, 8>);
+    return bf ? go(fa2_rope_kernel<64, true, kCache, 1>, fa2_rope_kernel<64, true, kCache, 8>)
+              : go(fa2_rope_kernel<64, false, kCache, 1>, fa2_rope_kernel<64, false, kCache, 8>);
+}
+
+fa2_status rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,
+                const int32_t* axes, int B, int H_q, int H_kv, int N, int d, int rot_dim, int n_axes, int interleaved,
+                int inverse, const int64_t* strides, fa2_dtype dtype, cudaStream_t stream) {
+    if (!q || !q_out || !strides || !k != !k_out) return FA2_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return FA2_ERR_INVALID_ARG;
+    if (B <= 0 || H_q <= 0 || N <= 0 || (k ? H_kv <= 0 : H_kv != 0)) return FA2_ERR_INVALID_ARG;
+    const int sizes[3] = {B, 0, N};
+    for (int i = 0; i < 12; ++i) {
+        if (!k && (i / 3) % 2) continue;
+        const int64_t s = strides[i];
+        if (s < 0 || s % 8 != 0) return FA2_ERR_INVALID_ARG;
+        // what is written may not lie on itself
+        const int n = i % 3 == 1 ? (i < 9 ? H_q : H_kv) : sizes[i % 3];
+        if (i >= 6 && s == 0 && n > 1) return FA2_ERR_INVALID_ARG;
+    }
+    fa2_status st = rope_check(positions, inv_freq, axes, d, rot_dim, n_axes, interleaved, dtype);
+    if (st != FA2_OK) return st;
+    if (!rope_sizes(d, rot_dim, n_axes)) return FA2_ERR_UNSUPPORTED;
+    for (int i = 0; i < 12; ++i)
+        if ((k || !((i / 3) % 2)) && strides[i] > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
+    // tokens, and a block's rows, are counted in 32 bits
+    if (B > (0x7FFFFFFF - 1024) / N || static_cast<long long>(H_q) + H_kv > (1 << 24)) return FA2_ERR_UNSUPPORTED;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::rope::Params p{};
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    for (int i = 0; i < 2; ++i) {
+        p.in[i] = in[i];
+        p.out[i] = out[i];
+        if (!in[i]) continue;
+        p.in_b[i] = static_cast<int>(strides[3 * i]);
+        p.in_h[i] = static_cast<int>(strides[3 * i + 1]);
+        p.in_n[i] = static_cast<int>(strides[3 * i + 2]);
+        p.out_b[i] = static_cast<int>(strides[6 + 3 * i]);
+        p.out_h[i] = static_cast<int>(strides[6 + 3 * i + 1]);
+        p.out_n[i] = static_cast<int>(strides[6 + 3 * i + 2]);
+    }
+    p.heads[0] = H_q;
+    p.heads[1] = H_kv;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.axes = axes;
+    p.tokens = B * N;
+    p.n = N;
+    p.n_axes = n_axes;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.inverse = inverse;
+    return rope_launch<false>(dev, p, d, dtype == FA2_BF16, stream);
+}
+
+// Pages of the 16-bit cache as matrices [page_size, d]: boxes of a page's 64
+// columns. A coordinate past the last one reads as zeros.
+fa2_status kv16_encode_cache(CUtensorMap* m, const void* ptr, uint64_t mats, int page_size, int d) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size), mats};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(page_size) * d * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
+}
+
+// q [T, H_q, d] with boxes of the `group` heads that share a KV head and as
+// many tokens as fill 128 rows.
+fa2_status kv16_encode_q(CUtensorMap* m, const void* ptr, int T, int H_q, int d, int group, int64_t stride_t, int64_t stride_h) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H_q), static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride_h) * 2, static_cast<cuuint64_t>(stride_t) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+    cuuint32_t es[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
+}
+
+// Units (a row block against 128 keys) that T new tokens of B requests can have.
+long long kv16_units(int T, int B, int H_q, int H_kv, long long max_tokens) {
+    const long long block = 2 * (128 / (H_q / H_kv));
+    return (T / block + std::min(T, B)) * H_kv * ((max_tokens + 127) / 128);
+}
+
+fa2_status kv16_check_sizes(int T, int B, int H_q, int H_kv, int d, int max_pages, int page_size) {
+    if (T <= 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || d <= 0 || H_q % H_kv != 0) return FA2_ERR_INVALID_ARG;
+    const fa2_status st = kv4_check_pages(page_size, 1, max_pages);
+    if (st != FA2_OK) return st;
+    if ((d != 64 && d != 128) || H_q / H_kv > 128) return FA2_ERR_UNSUPPORTED;
+    if (static_cast<long long>(T) * H_q > 0x7FFFFFFFLL || B > 0x7FFFFFFF - 1024) return FA2_ERR_UNSUPPORTED;
+    const long long blocks = T / (2 * (128 / (H_q / H_kv))) + std::min(T, B);
+    if (blocks * H_kv > (1LL << 30) || kv16_units(T, B, H_q, H_kv, static_cast<long long>(max_pages) * page_size) > (1LL << 30))
+        return FA2_ERR_UNSUPPORTED;
+    return FA2_OK;
+}
+
+// Rows of a buffer of partial results: blocks are two tiles unless all tokens fit one.
+int kv16_part_rows(int T, int group) { return T <= 128 / group ? (T * group + 31) / 32 * 32 : 256; }
+
+int kv16_ctas(int T, int B, int H_q, int H_kv, long long max_tokens, int most) {
+    const long long units = kv16_units(T, B, H_q, H_kv, max_tokens);
+    return static_cast<int>(std::min<long long>(most, (units + fa2::kv16::kMinRun - 1) / fa2::kv16::kMinRun));
+}
+
+template <int D, bool kBf16>
+fa2_status kv16_launch(int dev, const CUtensorMap& mq, const CUtensorMap& mkv, const fa2::kv16::Params& p, cudaStream_t stream) {
+    using namespace fa2::kv16;
+    constexpr int kSmem = Lay<D>::kSmemBytes;
+    auto kern = fa2_kv16_fwd_kernel<D, kBf16>;
+    const fa2_status st = set_smem(dev, 44 + (D == 128 ? 0 : 2) + (kBf16 ? 0 : 1), kern, kSmem);
+    if (st != FA2_OK) return st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+    cfg.blockDim = dim3(fa2::kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, mq, mkv, p) != cudaSuccess) return cuda_fail();
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), kJoinY);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, fa2_kv16_join_kernel<D, kBf16>, p) == cudaSuccess ? FA2_OK : cuda_fail();
+}
+
+}  // namespace
+
+extern "C" {
+
+fa2_status fa2_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,
+                    const int32_t* axes, int B, int H_q, int H_kv, int N, int d, int rot_dim, int n_axes, int interleaved,
+                    const int64_t* strides, fa2_dtype dtype, cudaStream_t stream) {
+    return rope(q, k, q_out, k_out, positions, inv_freq, axes, B, H_q, H_kv, N, d, rot_dim, n_axes, interleaved, 0, strides,
+                dtype, stream);
+}
+
+fa2_status fa2_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const int32_t* positions,
+                        const float* inv_freq, const int32_t* axes, int B, int H_q, int H_kv, int N, int d, int rot_dim,
+                        int n_axes, int interleaved, const int64_t* strides, fa2_dtype dtype, cudaStream_t stream) {
+    return rope(dq_out, dk_out, dq, dk, positions, inv_freq, axes, B, H_q, H_kv, N, d, rot_dim, n_axes, interleaved, 1, strides,
+                dtype, stream);
+}
+
+fa2_status fa2_kv16_append(const void* q, const void* k, const void* v, const int32_t* slots, const int32_t* positions,
+                           const float* inv_freq, const int32_t* axes, void* cache, void* q_out, int T, int H_q, int H_kv, int d,
+                           int rot_dim, int n_axes, int interleaved, const int64_t* strides, int page_size, int num_pages,
+                           fa2_dtype dtype, cudaStream_t stream) {
+    if (!k || !v || !slots || !cache || !strides || !q != !q_out) return FA2_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned16(q_out) || !aligned4(slots))
+        return FA2_ERR_INVALID_ARG;
+    if (T <= 0 || H_kv <= 0 || d <= 0 || (q ? H_q <= 0 : H_q != 0)) return FA2_ERR_INVALID_ARG;
+    for (int i = q ? 0 : 2; i < 6; ++i)
+        if (strides[i] < 0 || strides[i] % 8 != 0) return FA2_ERR_INVALID_ARG;
+    fa2_status st = FA2_OK;
+    if (positions) {
+        if ((st = rope_check(positions, inv_freq, axes, d, rot_dim, n_axes, interleaved, dtype)) != FA2_OK) return st;
+    } else if (q || rot_dim != 0 || (dtype != FA2_BF16 && dtype != FA2_FP16)) {
+        return FA2_ERR_INVALID_ARG;   // without positions nothing is rotated, and there is nothing to do with q
+    }
+    if ((st = kv4_check_pages(page_size, num_pages, 1)) != FA2_OK) return st;
+    if (positions ? !rope_sizes(d, rot_dim, n_axes) : d != 64 && d != 128) return FA2_ERR_UNSUPPORTED;
+    for (int i = q ? 0 : 2; i < 6; ++i)
+        if (strides[i] > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
+    if (T > 0x7FFFFFFF - 1024 || H_kv > (1 << 23) || H_q > (1 << 23)) return FA2_ERR_UNSUPPORTED;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    fa2::rope::Params p{};
+    const void* in[3] = {q, k, v};
+    for (int i = 0; i < 3; ++i) {
+        p.in[i] = in[i];
+        if (!in[i]) continue;
+        p.in_n[i] = static_cast<int>(strides[2 * i]);
+        p.in_h[i] = static_cast<int>(strides[2 * i + 1]);
+    }
+    p.out[0] = q_out;
+    p.out_n[0] = H_q * d;
+    p.out_h[0] = d;
+    p.heads[0] = H_q;
+    p.heads[1] = p.heads[2] = H_kv;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.axes = axes;
+    p.tokens = p.n = T;
+    p.n_axes = n_axes;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.slots = slots;
+    p.cache = cache;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.num_slots = num_pages * page_size;
+    return rope_launch<true>(dev, p, d, dtype == FA2_BF16, stream);
+}
+
+int64_t fa2_fwd_kv16_workspace(int T, int B, int H_q, int H_kv, int d, int max_pages, int page_size) {
+    if (kv16_check_sizes(T, B, H_q, H_kv, d, max_pages, page_size) != FA2_OK) return -1;
+    const int64_t ctas = kv16_ctas(T, B, H_q, H_kv, static_cast<long long>(max_pages) * page_size, fa2::kv16::kMaxCtas);
+    return ctas * (2LL * kv16_part_rows(T, H_q / H_kv) * (d + 2) * static_cast<int64_t>(sizeof(float)) +
+                   static_cast<int64_t>(sizeof(fa2::kv16::Begun)));
+}
+
+fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                        const int32_t* q_starts, const int32_t* q_lens, void* o, float* lse, void* workspace,
+                        int64_t workspace_bytes, int T, int B, int H_q, int H_kv, int d, int64_t q_stride_t, int64_t q_stride_h,
+                        int max_pages, int page_size, int num_pages, float scale, int causal, fa2_dtype dtype,
+                        cudaStream_t stream) {
+    if (!q || !cache || !block_table || !seq_lens || !q_starts || !q_lens || !o || !lse || !workspace) return FA2_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(o) || !aligned16(lse) || !aligned16(workspace)) return FA2_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(q_starts) || !aligned4(q_lens)) return FA2_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.0f)) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_BF16 && dtype != FA2_FP16) return FA2_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return FA2_ERR_INVALID_ARG;
+    if (T <= 0 || B <= 0 || H_q <= 0 || H_kv <= 0 || d <= 0 || H_q % H_kv != 0) return FA2_ERR_INVALID_ARG;
+    if (q_stride_t <= 0 || q_stride_h <= 0 || q_stride_t % 8 != 0 || q_stride_h % 8 != 0) return FA2_ERR_INVALID_ARG;
+    fa2_status st = kv4_check_pages(page_size, num_pages, max_pages);
+    if (st != FA2_OK) return st;
+    if ((st = kv16_check_sizes(T, B, H_q, H_kv, d, max_pages, page_size)) != FA2_OK) return st;
+    if (q_stride_t > 0x7FFFFFFFLL || q_stride_h > 0x7FFFFFFFLL) return FA2_ERR_UNSUPPORTED;
+    if (static_cast<long long>(num_pages) * H_kv > (0x7FFFFFFFLL - 2) / 2) return FA2_ERR_UNSUPPORTED;
+    if (workspace_bytes < fa2_fwd_kv16_workspace(T, B, H_q, H_kv, d, max_pages, page_size)) return FA2_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((st = check_device(&dev)) != FA2_OK) return st;
+    if ((st = get_encoder()) != FA2_OK) return st;
+    const int group = H_q / H_kv;
+    CUtensorMap mq, mkv;
+    if (kv16_encode_q(&mq, q, T, H_q, d, group, q_stride_t, q_stride_h) != FA2_OK ||
+        kv16_encode_cache(&mkv, cache, static_cast<uint64_t>(num_pages) * H_kv * 2, page_size, d) != FA2_OK)
+        return cuda_fail();
+    fa2::kv16::Params p{};
+    p.q_starts = q_starts;
+    p.q_lens = q_lens;
+    p.seq_lens = seq_lens;
+    p.block_table = block_table;
+    p.o = o;
+    p.lse = lse;
+    p.B = B;
+    p.T = T;
+    p.hq = H_q;
+    p.hkv = H_kv;
+    p.group = group;
+    p.tok_tile = 128 / group;
+    p.part_rows = kv16_part_rows(T, group);
+    p.max_pages = max_pages;
+    p.max_tokens = max_pages * page_size;
+    p.page = page_size;
+    p.log2_page = log2_of(page_size);
+    p.num_pages = num_pages;
+    p.causal = causal;
+    p.ctas = kv16_ctas(T, B, H_q, H_kv, p.max_tokens, std::min(sm_count(dev), fa2::kv16::kMaxCtas));
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = p.part_o + 2LL * p.ctas * p.part_rows * d;
+    p.begun = reinterpret_cast<fa2::kv16::Begun*>(p.part_ml + 4LL * p.ctas * p.part_rows);
+    p.debug_flags = g_debug_flags.load();
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    p.wait_limit_ns = g_wait_limit_ns.load();
+    const bool bf = dtype == FA2_BF16;
+    if (d == 128) return bf ? kv16_launch<128, true>(dev, mq, mkv, p, stream) : kv16_launch<128, false>(dev, mq, mkv, p, stream);
+    return bf ? kv16_launch<64, true>(dev, mq, mkv, p, stream) : kv16_launch<64, false>(dev, mq, mkv, p, stream);
 }
 
 fa2_status fa2_check_status(cudaStream_t stream) {

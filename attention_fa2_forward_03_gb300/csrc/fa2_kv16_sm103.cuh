@@ -1,0 +1,1080 @@
+// Attention of new tokens over a paged KV cache held in 16 bits (sm_103a): one
+// token a request (decoding), a chunk of a prompt, or both in one call.
+//
+// The cache is [num_pages, H_kv, 2, page, D] 16-bit elements: of a page and KV
+// head first the keys, then the values of `page` tokens. Request b has q_lens[b]
+// new tokens, rows q_starts[b] .. of q [T, H_q, D], and seq_lens[b] cached ones,
+// its own among them.
+//
+// How. The tiles are those of the forward kernel: 128 query rows (tokens times
+// the G query heads that share a KV head, heads next to each other) against 128
+// keys, S = Q K^T and O += P V on tcgen05 with S and O in tensor memory, keys
+// and values by TMA, a box for each page of a tile. A block of query rows is up
+// to two tiles; both read the same keys (`pair`). A block of one tile, such as a
+// decoding request's few rows, uses the second S and O for every other tile of
+// keys instead (`single`): two softmax streams over the same rows, whose results
+// the epilogue adds up, so that one's exponentials overlap the other's products.
+//
+// Lengths are known on the device only. The key tiles of all (request, KV head,
+// row block) are one line of units that is cut into equal runs, one a CTA. A run
+// may begin and end inside a row block; its CTAs then leave partial results in
+// fp32, which a second, small kernel joins in a fixed order. A warp of each CTA
+// finds the run and hands its parts, row block by row block, to the others.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "fa2.h"
+#include "fa2_fwd_sm103.cuh"
+#include "fa2_kv4_sm103.cuh"
+#include "ptx_sm103.cuh"
+
+namespace fa2 {
+namespace kv16 {
+
+using kv4::report;
+
+// Sites of the status word (page ids and lengths as for the 4-bit cache).
+enum Site : int { kSiteRows = 53, kSitePart = 54 };
+
+constexpr int kMaxCtas = 160;
+constexpr int kSchedWarp = 14;
+constexpr int kMinRun = 2;        // units a CTA has at least
+constexpr int kParts = 4;         // parts on their way from the scheduling warp
+constexpr int kPartUsers = 14;    // warps that read a part
+constexpr int kJoinY = 4, kJoinThreads = 256;
+
+struct Begun {                    // the row block that begins in a CTA's run and ends behind it
+    int parts;                    // CTAs that share it; 0: none
+    int q0, ntok, h;
+};
+
+struct Params {
+    const int* q_starts;          // [B]
+    const int* q_lens;            // [B]
+    const int* seq_lens;          // [B]
+    const int* block_table;       // [B, max_pages]
+    void* o;                      // [T, hq, D]
+    float* lse;                   // [T, hq]
+    float* part_o;                // [2 ctas, part_rows, D]: a CTA's part of a block that began before its run, of one that begins in it
+    float* part_ml;               // [2 ctas, part_rows, 2]: running maximum (log2 units) and sum
+    Begun* begun;                 // [ctas]
+    int B, T, hq, hkv, group;
+    int tok_tile;                 // tokens of a tile of query rows: 128 / group
+    int part_rows;
+    int max_pages, max_tokens, page, log2_page, num_pages;
+    int causal, ctas;
+    int debug_flags;
+    float scale_log2;
+    long long wait_limit_ns;
+};
+
+// A part: the key tiles jb .. jb + n of one row block that this CTA works on.
+struct __align__(16) Part {
+    int kind;                     // 0: no more, 1: two tiles of query rows, 2: one
+    int steps0, steps1;           // key tiles of each softmax stream
+    int jb, n;
+    int len, b, h;
+    int q0, ntok;                 // first token (row of q) of the block, its tokens
+    int vis0;                     // keys that its first token sees
+    int buffer;                   // of partial results, or -1: the whole block
+    int qslot;                    // single: the place of its query tile
+    int jmask0, jmask1;           // first key tile that some row of the stream does not see whole
+    int pad;
+
+    __device__ __forceinline__ int steps(int t) const { return t ? steps1 : steps0; }
+    __device__ __forceinline__ int jmask(int t) const { return t ? jmask1 : jmask0; }
+};
+static_assert(sizeof(Part) == 64, "four 16-byte loads");
+constexpr int kPair = 1, kSingle = 2;
+
+template <int D>
+struct Lay {
+    static constexpr int kBlkBytes = Layout<D>::kBlkBytes;
+    static constexpr int kTileBytes = Layout<D>::kTileBytes;
+    static constexpr int kStages = Layout<D>::kStages;
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = 2 * kTileBytes;
+    static constexpr int kStageOff = kRingOff + kStages * kTileBytes;   // the epilogue's staging
+    static constexpr int kBarOff = kStageOff + kBM * 128;
+    // q_full[2] q_empty[2] kv_full[S] kv_empty[S] s_full[2] alpha[2] stats[2] p_full[2] o_full[2] mma_done
+    // stats_free[2] part_full[4] part_empty[4]
+    static constexpr int kNumBars = 2 * kStages + 17 + 2 * kParts;
+    static constexpr int kRowOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // alpha[2][128], m[2][128], l[2][128]
+    static constexpr int kPartOff = kRowOff + 6 * kBM * 4;
+    static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
+    static constexpr int kMiscOff = kIdOff + 4 * 32 * 4;
+    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+};
+
+template <int D>
+struct BarSet : Bars<D> {
+    static constexpr int S = Layout<D>::kStages;
+    __device__ uint32_t part_full(int s) const { return this->base + 8 * (17 + 2 * S + s); }
+    __device__ uint32_t part_empty(int s) const { return this->base + 8 * (17 + 2 * S + kParts + s); }
+};
+
+// 16 columns of the thread's lane of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+
+// ---------------------------------------------------------------- the line of units
+
+// A request as the call may use it: what points outside q or the table counts
+// as nothing and is reported.
+struct Request {
+    int start, n, len, blocks;
+};
+
+__device__ __forceinline__ Request request(const Params& p, int b) {
+    Request r{p.q_starts[b], p.q_lens[b], p.seq_lens[b], 0};
+    if (r.n < 0 || r.start < 0 || r.start > p.T - max(r.n, 0)) {
+        if (blockIdx.x == 0 && r.n != 0) report(kSiteRows);
+        r.n = 0;
+    }
+    if (r.len < 0 || r.len > p.max_tokens) {
+        if (blockIdx.x == 0 && r.n > 0) report(kv4::kSiteLength);
+        r.len = min(max(r.len, 0), p.max_tokens);
+    }
+    r.blocks = r.n <= p.tok_tile ? (r.n > 0) : (r.n + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
+    return r;
+}
+
+__device__ __forceinline__ int tiles_in(int keys) { return keys <= 0 ? 0 : (keys + kBN - 1) / kBN; }
+
+// The sum of floor((a i + b) / m) over i < n, by Euclid's algorithm on (a, m).
+__device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned a, long long b) {
+    long long sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
+        }
+        const long long y = static_cast<long long>(a) * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const unsigned t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// The first row block in which some row sees a key (len > 0).
+__device__ __forceinline__ int first_block(const Params& p, const Request& r) {
+    return p.causal && r.n > r.len ? (r.n - r.len) / (2 * p.tok_tile) : 0;
+}
+
+// Key tiles of the first x row blocks of one head.
+__device__ __forceinline__ long long tiles_before(const Params& p, const Request& r, int x) {
+    if (x <= 0 || r.len == 0) return 0;
+    if (!p.causal) return static_cast<long long>(x) * tiles_in(r.len);
+    const bool last = x >= r.blocks;
+    const int k0 = first_block(p, r), step = 2 * p.tok_tile;
+    long long sum = last ? tiles_in(r.len) : 0;   // its last row sees every key
+    const int full = last ? r.blocks - 1 : x;
+    // block k's last row sees len - n + (k + 1) step keys
+    if (full > k0)
+        sum += floor_sum(full - k0, kBN, step, static_cast<long long>(r.len) - r.n + static_cast<long long>(k0 + 1) * step + kBN - 1);
+    return sum;
+}
+
+// The scheduling warp: finds this CTA's run and hands out its parts.
+template <int D>
+__device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const BarSet<D>& bars, const Waiter& w) {
+    const int lane = threadIdx.x & 31;
+    volatile Part* ring = reinterpret_cast<Part*>(smem + Lay<D>::kPartOff);
+    int n_part = 0;
+    bool ok = true;
+    auto put = [&](const Part& x) {
+        const int s = n_part % kParts;
+        ok = __all_sync(~0u, w.wait(bars.part_empty(s), ((n_part / kParts) & 1) ^ 1, kSitePart));
+        if (!ok) return;
+        if (lane == 0) {
+            uint4* to = reinterpret_cast<uint4*>(const_cast<Part*>(&ring[s]));
+            const uint4* from = reinterpret_cast<const uint4*>(&x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = from[i];
+            ptx::mbar_arrive(bars.part_full(s));
+        }
+        __syncwarp();
+        ++n_part;
+    };
+
+    // Units in front of each lane's share of the requests.
+    const int chunk = (p.B + 31) / 32, b0 = min(lane * chunk, p.B), b1 = min(b0 + chunk, p.B);
+    long long mine = 0, rows = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Request r = request(p, b);
+        mine += tiles_before(p, r, r.blocks) * p.hkv;
+        rows += r.n;
+    }
+    long long to = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, to, o);
+        if (lane >= o) to += y;
+        rows += __shfl_xor_sync(~0u, rows, o);
+    }
+    long long sum = __shfl_sync(~0u, to, 31);
+    if (rows > p.T) {   // requests name a row twice
+        if (blockIdx.x == 0 && lane == 0) report(kSiteRows);
+        sum = 0;
+    }
+    const int total = static_cast<int>(sum);   // below 2^30: the host's bound for T rows
+    const int per = max((total + p.ctas - 1) / p.ctas, kMinRun);
+    int u = static_cast<int>(blockIdx.x) * per;
+    const int begin = u, end = min(total, u + per);
+    Begun begun{0, 0, 0, 0};
+    if (u < end) {
+        long long at = to - mine;
+        int b = b0;
+        const bool here = u >= at && u < to;
+        if (here)
+            while (true) {
+                const Request r = request(p, b);
+                const long long t = tiles_before(p, r, r.blocks) * p.hkv;
+                if (u < at + t) break;
+                at += t;
+                ++b;
+            }
+        const int from = __ffs(__ballot_sync(~0u, here)) - 1;
+        b = __shfl_sync(~0u, b, from);
+        const int rem = u - static_cast<int>(__shfl_sync(~0u, at, from));
+        Request r = request(p, b);
+        const int each = static_cast<int>(tiles_before(p, r, r.blocks));
+        int h = rem / each;
+        const int inside = rem - h * each;
+        // the row block: 32 candidates at a time
+        int lo = 0, hi = r.blocks;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+            const uint32_t below = __ballot_sync(~0u, x < hi && tiles_before(p, r, x) <= inside);
+            lo += (31 - __clz(below)) * step;
+            hi = min(hi, lo + step);
+        }
+        int rb = lo, tile = inside - static_cast<int>(tiles_before(p, r, rb));
+        int first = first_block(p, r);
+        int singles = 0;
+        while (ok) {
+            const int tok0 = rb * 2 * p.tok_tile, ntok = min(2 * p.tok_tile, r.n - tok0);
+            const int vis0 = p.causal ? r.len - r.n + tok0 + 1 : r.len;
+            const int more = p.causal ? 1 : 0;
+            const int tiles = tiles_in(vis0 + more * (ntok - 1));
+            const int n = min(end - u, tiles - tile), seg0 = u - tile, seg1 = seg0 + tiles;
+            Part x;
+            x.kind = ntok > p.tok_tile ? kPair : kSingle;
+            x.jb = tile;
+            x.n = n;
+            x.len = r.len;
+            x.b = b;
+            x.h = h;
+            x.q0 = r.start + tok0;
+            x.ntok = ntok;
+            x.vis0 = vis0;
+            x.buffer = -1;
+            x.qslot = 0;
+            x.pad = 0;
+            if (seg0 < begin || seg1 > end) {
+                const bool begins = seg0 >= begin;
+                x.buffer = 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
+                if (begins) begun = Begun{(seg1 - 1) / per - static_cast<int>(blockIdx.x) + 1, x.q0, ntok, h};
+            }
+            if (x.kind == kPair) {
+                x.steps0 = max(min(tile + n, tiles_in(vis0 + more * (p.tok_tile - 1))) - tile, 0);
+                x.steps1 = n;
+                x.jmask1 = max(vis0 + more * p.tok_tile, 0) / kBN;
+            } else {
+                x.steps0 = (n + 1) / 2;
+                x.steps1 = n / 2;
+                x.jmask1 = max(vis0, 0) / kBN;
+                x.qslot = singles++ & 1;
+            }
+            x.jmask0 = max(vis0, 0) / kBN;
+            put(x);
+            u += n;
+            tile = 0;
+            if (u >= end) break;
+            if (++rb == r.blocks) {
+                if (++h == p.hkv) {
+                    h = 0;
+                    do {
+                        r = request(p, ++b);
+                    } while (r.n == 0 || r.len == 0);
+                    first = first_block(p, r);
+                }
+                rb = first;
+            }
+        }
+    }
+    if (lane == 0) p.begun[blockIdx.x] = begun;
+    Part x{};
+    if (ok) put(x);
+}
+
+// The next part; false behind the last one or if the CTA is aborting (`ok`).
+template <int D>
+__device__ __forceinline__ bool next_part(uint8_t* smem, const BarSet<D>& bars, const Waiter& w, int& n_part, Part& x, bool& ok) {
+    const int s = n_part % kParts;
+    ok = __all_sync(~0u, w.wait(bars.part_full(s), (n_part / kParts) & 1, kSitePart));
+    if (!ok) return false;
+    const uint32_t at = ptx::smem_addr(smem + Lay<D>::kPartOff + s * static_cast<int>(sizeof(Part)));
+    uint4* to = reinterpret_cast<uint4*>(&x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to[i] = ptx::ld_shared_v4(at + 16 * i);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars.part_empty(s));
+    ++n_part;
+    return x.kind != 0;
+}
+
+// ---------------------------------------------------------------- producer
+
+// Order of a part's tiles in the ring, the order of their use. Pair: K_0 V_0
+// K_1 V_1 ..; single: K_0 K_1 V_0 K_2 V_1 .. V_{n-2} V_{n-1}.
+__device__ __forceinline__ void ring_entry(bool pair, int n, int k, int& value, int& tile) {
+    if (pair) {
+        value = k & 1;
+        tile = k >> 1;
+    } else if (k == 2 * n - 1) {
+        value = 1;
+        tile = n - 1;
+    } else if (k < 2) {
+        value = 0;
+        tile = k;
+    } else {
+        value = (k & 1) ^ 1;
+        tile = value ? (k - 2) / 2 : (k + 1) / 2;
+    }
+}
+__device__ __forceinline__ int value_entry(bool pair, int n, int tile) { return pair ? 2 * tile + 1 : min(2 + 2 * tile, 2 * n - 1); }
+
+template <int D>
+__device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p, uint8_t* smem,
+                                         uint32_t sbase, const BarSet<D>& bars, const Waiter& w) {
+    using L = Lay<D>;
+    constexpr int S = L::kStages, kBlks = D / 64;
+    const int lane = threadIdx.x & 31;
+    const int pages = kBN >> p.log2_page;          // of a tile
+    const int page_at = lane / kBlks, blk = lane % kBlks;   // a lane's box: a page's 64 columns
+    const bool loads = page_at < pages;
+    const uint32_t box = blk * L::kBlkBytes + page_at * (p.page * 128);
+    int* ids = reinterpret_cast<int*>(smem + L::kIdOff) + lane;   // of the lane's page, tile modulo 4
+    const bool load_q = (p.debug_flags & 1) == 0;  // test hook
+    const uint32_t q_bytes = p.tok_tile * p.group * (D * 2);
+    const int nothing = p.num_pages * p.hkv * 2;   // past the tensor: a box of zeros
+    int ring = 0, n_part = 0;
+    uint32_t nq = 0, ever = 0;   // a bit for each query place: loads modulo 2, any load
+    bool ok = true;
+    Part x;
+    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+        const bool pair = x.kind == kPair;
+        const int* table = p.block_table + static_cast<long long>(x.b) * p.max_pages;
+        const int used = (x.len + p.page - 1) >> p.log2_page;   // pages of the request
+        const int entry0 = x.jb * pages + page_at;
+        auto look = [&](int tile) {
+            const int e = entry0 + tile * pages;
+            return loads && tile < x.n && e < used ? __ldg(table + e) : -1;
+        };
+        int ahead[2] = {look(0), look(1)};   // page ids of the next two tiles of keys
+        auto load_kv = [&](int k) {
+            int value, tile;
+            ring_entry(pair, x.n, k, value, tile);
+            const int s = ring % S;
+            ok = __all_sync(~0u, w.wait(bars.kv_empty(s), ((ring / S) & 1) ^ 1, kSiteKvEmpty));
+            if (!ok) return;
+            int z;
+            if (value) {
+                z = ids[32 * (tile & 3)];
+                z = z < 0 ? nothing : z + 1;
+            } else {
+                const int id = ahead[0];
+                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
+                if (!good && loads && entry0 + tile * pages < used) report(kv4::kSitePage);
+                z = good ? (id * p.hkv + x.h) * 2 : -1;
+                ids[32 * (tile & 3)] = z;
+                z = good ? z : nothing;
+                ahead[0] = ahead[1];
+                ahead[1] = look(tile + 2);
+            }
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bars.kv_full(s), L::kTileBytes);
+            __syncwarp();
+            if (loads) ptx::tma_load_3d(sbase + L::kRingOff + s * L::kTileBytes + box, tmKV, blk * 64, 0, z, bars.kv_full(s));
+            ++ring;
+        };
+        // Keys first: their places free up before the query tiles' do.
+        const int pre = min(2, 2 * x.n);
+        for (int k = 0; k < pre && ok; ++k) load_kv(k);
+        for (int t = 0; t < 2 && ok; ++t) {
+            if (pair ? x.steps(t) == 0 : t != x.qslot) continue;
+            ok = __all_sync(~0u, w.wait(bars.q_empty(t), ((nq >> t) & 1) ^ 1, kSiteQEmpty));
+            if (!ok) break;
+            if (load_q && lane == 0) {
+                ptx::mbar_arrive_expect_tx(bars.q_full(t), q_bytes);
+#pragma unroll
+                for (int c = 0; c < kBlks; ++c)
+                    ptx::tma_load_3d(sbase + L::kQOff + t * L::kTileBytes + c * L::kBlkBytes, tmQ, c * 64, x.h * p.group,
+                                     x.q0 + (pair ? t * p.tok_tile : 0), bars.q_full(t));
+            }
+            nq ^= 1u << t;
+            ever |= 1u << t;
+        }
+        for (int k = pre; k < 2 * x.n && ok; ++k) load_kv(k);
+        if (!ok) break;
+    }
+    if (!ok) {   // aborting: every copy that this CTA started lands before it exits
+        const int first = ring > S ? ring - S : 0;
+        for (int r = first; r < ring; ++r) w.drain(bars.kv_full(r % S), (r / S) & 1);
+        if (load_q)
+            for (int t = 0; t < 2; ++t)
+                if ((ever >> t) & 1) w.drain(bars.q_full(t), ((nq >> t) & 1) ^ 1);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- MMA issuer
+
+template <int D, bool kBf16>
+__device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint32_t sbase, uint32_t tmem, const BarSet<D>& bars,
+                                           const Waiter& w) {
+    using L = Lay<D>;
+    constexpr int S = L::kStages;
+    constexpr uint32_t kAB = kBf16 ? 1u : 0u;
+    constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kBN);
+    constexpr uint32_t kIdO = ptx::idesc_f16(kAB, 0, 1, kBM, D);
+    auto stage_addr = [&](int r) { return sbase + L::kRingOff + (r % S) * L::kTileBytes; };
+    auto issue_qk = [&](int t, int qslot, int k_ring) {
+        const uint64_t qd = ptx::desc_sw128(sbase + L::kQOff + qslot * L::kTileBytes, 16, 1024);
+        const uint64_t kd = ptx::desc_sw128(stage_addr(k_ring), 16, 1024);
+        qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
+        ptx::tc_commit_elect(bars.s_full(t));
+    };
+    auto issue_pv = [&](int t, int v_ring, bool acc) {
+        const uint64_t vd = ptx::desc_sw128(stage_addr(v_ring), L::kBlkBytes, 1024);
+        pv_kloop(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
+    };
+    auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
+    auto wait_ring = [&](int r) { return wait_u(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull); };
+    auto release = [&](int r) { ptx::tc_commit_elect(bars.kv_empty(r % S)); };
+
+    int ring = 0, n_part = 0;
+    uint32_t nq = 0, np = 0;   // a bit for each place: query tiles used, P tiles consumed, modulo 2
+    bool ok = true;
+    Part x;
+    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+        if (x.kind == kPair) {
+            // As the forward kernel's general mode: at key tile j the streams with j < steps[t] take part.
+            for (int t = 0; t < 2 && ok; ++t)
+                if (x.steps(t) > 0) ok = wait_u(bars.q_full(t), (nq >> t) & 1, kSiteQFull);
+            if (!ok || !(ok = wait_ring(ring))) break;
+            ptx::tc_fence_after();
+            for (int t = 0; t < 2; ++t) {
+                if (x.steps(t) == 0) continue;
+                issue_qk(t, t, ring);
+                if (x.steps(t) == 1) ptx::tc_commit_elect(bars.q_empty(t));
+            }
+            release(ring);
+            int k_ring = ring++;
+            for (int j = 0; j < x.n; ++j) {
+                const bool more = j + 1 < x.n;
+                const int v_ring = ring++;
+                if (more) k_ring = ring++;
+                const int t0 = j < x.steps0 ? 0 : 1;
+                const int kr = more ? k_ring : v_ring;
+                const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(kr % S), bars.p_full(t0)};
+                const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((kr / S) & 1),
+                                        (np >> t0) & 1};
+                if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
+                for (int t = 0; t < 2; ++t) {   // stream 1 takes part in every tile
+                    if (t < t0) continue;
+                    if (t != t0 && !(ok = wait_u(bars.p_full(t), (np >> t) & 1, kSitePFull))) break;
+                    np ^= 1u << t;
+                    ptx::tc_fence_after();
+                    issue_pv(t, v_ring, j > 0);
+                    if (t == 1) release(v_ring);
+                    if (j + 1 < x.steps(t)) {
+                        issue_qk(t, t, k_ring);
+                        if (j + 2 == x.steps(t)) ptx::tc_commit_elect(bars.q_empty(t));
+                        if (t == 1) release(k_ring);
+                    } else {
+                        ptx::tc_commit_elect(bars.o_full(t));
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+            for (int t = 0; t < 2; ++t)
+                if (x.steps(t) > 0) nq ^= 1u << t;
+        } else {
+            const int n = x.n;
+            if (!(ok = wait_u(bars.q_full(x.qslot), (nq >> x.qslot) & 1, kSiteQFull))) break;
+            for (int t = 0; t < min(n, 2) && ok; ++t) {
+                if (!(ok = wait_ring(ring))) break;
+                ptx::tc_fence_after();
+                issue_qk(t, x.qslot, ring);
+                if (t + 1 == n) ptx::tc_commit_elect(bars.q_empty(x.qslot));
+                release(ring++);
+            }
+            if (!ok) break;
+            for (int j = 0; j < n; ++j) {
+                const int t = j & 1;
+                const bool more = j + 2 < n;   // the stream's next keys
+                const int v_ring = ring++, k_ring = more ? ring++ : v_ring;
+                const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(k_ring % S), bars.p_full(t)};
+                const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((k_ring / S) & 1),
+                                        (np >> t) & 1};
+                if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
+                np ^= 1u << t;
+                ptx::tc_fence_after();
+                issue_pv(t, v_ring, j > 1);
+                release(v_ring);
+                if (more) {
+                    issue_qk(t, x.qslot, k_ring);
+                    release(k_ring);
+                    if (j + 3 == n) ptx::tc_commit_elect(bars.q_empty(x.qslot));
+                } else {
+                    ptx::tc_commit_elect(bars.o_full(t));
+                }
+            }
+            if (!ok) break;
+            nq ^= 1u << x.qslot;
+        }
+    }
+    // Every MMA issued above finishes before the CTA frees its TMEM.
+    ptx::tc_commit_elect(bars.mma_done());
+    w.drain(bars.mma_done(), 0);
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- softmax
+
+// Tokens of the tile that a stream's rows belong to.
+__device__ __forceinline__ int stream_tokens(const Params& p, const Part& x, int t) {
+    return x.kind == kPair ? min(x.ntok - t * p.tok_tile, p.tok_tile) : x.ntok;
+}
+
+// r / group for r < 128: inv = ceil(2^16 / group), which is off by less than
+// group / 2^16 of a quotient, so r / group by less than 1 / group.
+__device__ __forceinline__ int by_group(int r, uint32_t inv) { return static_cast<int>((static_cast<uint32_t>(r) * inv) >> 16); }
+
+template <int D, bool kBf16>
+__device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars,
+                                             const Waiter& w, int t) {
+    using L = Lay<D>;
+    constexpr int S = L::kStages;
+    const int row = threadIdx.x & 127;          // row of the query tile = TMEM lane
+    const uint32_t row_addr = tmem + (static_cast<uint32_t>(row & ~31) << 16);
+    const uint32_t colS = Layout<D>::col_s(t);
+    float* alpha_buf = reinterpret_cast<float*>(smem + L::kRowOff) + t * kBM;
+    float* m_buf = alpha_buf + 2 * kBM;
+    float* l_buf = m_buf + 2 * kBM;
+    const float c = p.scale_log2;
+    const uint64_t c2 = ptx::f2_pack(c, c);
+    const int tok = by_group(row, (65536u + p.group - 1) / p.group);   // the row's token in the tile
+
+    int n_s = 0, n_item = 0, n_part = 0, ring = 0;
+    bool ok = true;
+    Part x;
+    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+        const bool pair = x.kind == kPair;
+        const int steps = x.steps(t), jmask = x.jmask(t);
+        const int ring0 = ring;
+        ring += 2 * x.n;
+        if (steps == 0) continue;
+        const int rows = stream_tokens(p, x, t) * p.group;
+        const bool live = (row & ~31) < rows;   // of the warp: some row is a query's
+        const int kend = min(x.len, x.vis0 + (p.causal ? tok + (pair ? t * p.tok_tile : 0) : 0));
+        float m = -INFINITY;  // running row max of the scaled scores, log2 units
+        float l = 0.0f;       // running sum of exp2(s*c - m)
+        for (int i = 0; i < steps; ++i, ++n_s) {
+            const int jj = pair ? i : 2 * i + t, j = x.jb + jj;
+            ok = w.wait(bars.s_full(t), n_s & 1, kSiteSFull);
+            if (!__all_sync(~0u, ok)) {
+                ok = false;
+                break;
+            }
+            const int valid = x.len - j * kBN;
+            if (valid < kBN) {
+                // The request ends inside this tile. What lies behind it in its last page has weight 0, but may be
+                // anything, NaN too: those rows of V become zeros. (Two streams that share the tile write the same.)
+                const int r = ring0 + value_entry(pair, x.n, jj);
+                ok = w.wait(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (row >= valid) {
+                    const uint32_t at = sbase + L::kRingOff + (r % S) * L::kTileBytes + row * 128;
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k)
+                        ptx::st_shared_v4(at + (k / 8) * L::kBlkBytes + (((k ^ row) & 7) << 4), 0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            if (!live) {   // no row of this warp is a query's: its lanes of P and O may hold anything
+                ptx::mbar_arrive(bars.alpha_ready(t));
+                if (i + 1 == steps) {
+                    ok = w.wait(bars.stats_free(t), (n_item & 1) ^ 1, kSiteStats);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive(bars.stats_ready(t));
+                }
+                ptx::mbar_arrive(bars.p_full(t));
+                continue;
+            }
+            ptx::tc_fence_after();
+            uint32_t s[kBN];
+            float m_tile;
+            if (j >= jmask) {
+                ptx::tmem_ld32_at<0>(row_addr + colS + 0, s);
+                ptx::tmem_ld32_at<32>(row_addr + colS + 32, s);
+                ptx::tmem_ld32_at<64>(row_addr + colS + 64, s);
+                ptx::tmem_ld32_at<96>(row_addr + colS + 96, s);
+                ptx::tmem_wait_ld();
+                const int lim = kend - j * kBN;
+#pragma unroll
+                for (int k = 0; k < kBN; ++k) s[k] = k < lim ? s[k] : 0xFF800000u;
+                float mx[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float a = __uint_as_float(s[k]);
+#pragma unroll
+                    for (int e = 1; e < 15; e += 2)
+                        a = ptx::max3(a, __uint_as_float(s[k + 8 * e]), __uint_as_float(s[k + 8 * (e + 1)]));
+                    mx[k] = fmaxf(a, __uint_as_float(s[k + 120]));
+                }
+                m_tile = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), ptx::max3(mx[3], mx[4], ptx::max3(mx[5], mx[6], mx[7]))) * c;
+            } else {
+                float mq[4];
+                ptx::tmem_ld32_max_at<0>(row_addr + colS + 0, s, mq[0]);
+                ptx::tmem_ld32_max_at<32>(row_addr + colS + 32, s, mq[1]);
+                ptx::tmem_ld32_max_at<64>(row_addr + colS + 64, s, mq[2]);
+                ptx::tmem_ld32_max_at<96>(row_addr + colS + 96, s, mq[3]);
+                ptx::tmem_wait_ld();
+                m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
+            }
+            const float m_new = fmaxf(m, m_tile);
+            const float alpha = (i == 0 || m_new == m) ? 1.0f : ptx::ex2_approx(m - m_new);
+            alpha_buf[row] = alpha;
+            ptx::mbar_arrive(bars.alpha_ready(t));
+            l *= alpha;
+            m = m_new;
+            // A row with no key so far keeps m = -inf; its weights are exp2(-inf - 0) = 0.
+            const float m_use = m == -INFINITY ? 0.0f : m;
+            const uint64_t nm2 = ptx::f2_pack(-m_use, -m_use);
+            uint64_t acc[4] = {0, 0, 0, 0};
+            uint32_t pk[kBN / 2];
+#pragma unroll
+            for (int k = 0; k < kBN / 2; ++k) {
+                float x0, x1;
+                ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, nm2), x0, x1);
+                x0 = ptx::ex2_approx(x0);
+                x1 = ptx::ex2_approx(x1);
+                acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(x0, x1));
+                pk[k] = ptx::pack2<kBf16>(x0, x1);
+            }
+            float a0, a1;
+            ptx::f2_unpack(ptx::f2_add(ptx::f2_add(acc[0], acc[1]), ptx::f2_add(acc[2], acc[3])), a0, a1);
+            l += a0 + a1;
+            ptx::tmem_st32_at<0>(row_addr + colS, pk);
+            ptx::tmem_st32_at<32>(row_addr + colS + 32, pk);
+            if (i + 1 == steps) {
+                // the epilogue has read the stream's last m and l
+                ok = w.wait(bars.stats_free(t), (n_item & 1) ^ 1, kSiteStats);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                m_buf[row] = m;
+                l_buf[row] = l;
+                ptx::mbar_arrive(bars.stats_ready(t));
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bars.p_full(t));
+        }
+        if (!ok) break;
+        ++n_item;
+    }
+}
+
+// ---------------------------------------------------------------- correction + epilogue
+
+// Stores 128 bytes of each of 32 rows (v: the calling lane's row) through the
+// warp's 4 KB staging slice as whole lines; see store_o_rows. to(r): where row r
+// of the 32 goes, NULL for nowhere.
+template <typename To>
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], uint32_t wslice, int lane, To to) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        ptx::st_shared_v4(wslice + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(c) ^ (lane & 7u)) << 4), v[4 * c],
+                          v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+    const int r0 = lane >> 3;
+    const uint32_t rd = wslice + static_cast<uint32_t>(r0) * 128u + (static_cast<uint32_t>((lane & 7) ^ r0) << 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint4 x = ptx::ld_shared_v4((rd ^ ((i & 1) << 6)) + static_cast<uint32_t>(i) * 512u);
+        uint4* at = to(4 * i + r0);
+        if (at) at[lane & 7] = x;
+    }
+}
+
+template <int D, bool kBf16>
+__device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars,
+                                                const Waiter& w) {
+    using L = Lay<D>;
+    const int q = (threadIdx.x / 32) & 3;
+    const int lane = threadIdx.x & 31;
+    const int row = 32 * q + lane;
+    const uint32_t row_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const float* rowbuf = reinterpret_cast<const float*>(smem + L::kRowOff);  // alpha | m | l
+    const uint32_t wslice = sbase + L::kStageOff + static_cast<uint32_t>(q) * (32u * 128u);
+    const uint32_t inv_group = (65536u + p.group - 1) / p.group;
+
+    uint32_t n_s = 0, n_items = 0;   // a bit for each stream: steps, parts, modulo 2
+    int n_part = 0;
+    bool ok = true;
+    Part x;
+    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+        const bool pair = x.kind == kPair;
+        const int most = max(x.steps0, x.steps1);
+        for (int i = 0; i < most && ok; ++i) {
+            for (int t = 0; t < 2; ++t) {
+                if (i >= x.steps(t)) continue;
+                ok = w.wait(bars.alpha_ready(t), (n_s >> t) & 1, kSiteAlpha);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                n_s ^= 1u << t;
+                const bool live = 32 * q < stream_tokens(p, x, t) * p.group;
+                const float alpha = live ? rowbuf[t * kBM + row] : 1.0f;
+                if (i > 0 && __any_sync(~0u, alpha != 1.0f)) {
+                    ptx::tc_fence_after();
+                    const uint32_t colO = Layout<D>::col_o(t);
+                    const uint64_t a2 = ptx::f2_pack(alpha, alpha);
+#pragma unroll
+                    for (int h = 0; h < D; h += 32) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32_at<0>(row_addr + colO + h, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float o0, o1;
+                            ptx::f2_unpack(
+                                ptx::f2_mul(ptx::f2_pack(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), a2), o0, o1);
+                            o[2 * k] = __float_as_uint(o0);
+                            o[2 * k + 1] = __float_as_uint(o1);
+                        }
+                        ptx::tmem_st32_at<0>(row_addr + colO + h, o);
+                    }
+                    ptx::tmem_wait_st();
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bars.p_full(t));
+            }
+        }
+        // Epilogue. The next part's first PV overwrites O only behind this
+        // warpgroup's next p_full arrival, which comes after these loads.
+        for (int tile = 0; tile < (pair ? 2 : 1) && ok; ++tile) {
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // of the streams that have this tile's rows
+            bool has[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = pair ? tile : e;
+                has[e] = (!pair || e == 0) && x.steps(t) > 0;
+                if (!has[e]) continue;
+                ok = ok && w.wait(bars.stats_ready(t), (n_items >> t) & 1, kSiteStats) &&
+                     w.wait(bars.o_full(t), (n_items >> t) & 1, kSiteOFull);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                n_items ^= 1u << t;
+                m[e] = rowbuf[(2 + t) * kBM + row];
+                l[e] = rowbuf[(4 + t) * kBM + row];
+                ptx::mbar_arrive(bars.stats_free(t));
+            }
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const int rows = stream_tokens(p, x, tile) * p.group;
+            if (32 * q >= rows) continue;
+            float mm = m[0], ll = l[0], f[2] = {1.0f, 0.0f};
+            if (has[1]) {
+                mm = fmaxf(m[0], m[1]);
+                const float ref = mm == -INFINITY ? 0.0f : mm;
+                f[0] = ptx::ex2_approx(m[0] - ref);
+                f[1] = ptx::ex2_approx(m[1] - ref);
+                ll = f[0] * l[0] + f[1] * l[1];
+            }
+            const bool whole = x.buffer < 0;
+            const uint32_t col0 = Layout<D>::col_o(pair ? tile : 0), col1 = Layout<D>::col_o(1);
+            if (whole) {
+                // l = 0 only for a row without a key: O = 0, LSE = -inf.
+                const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+                f[0] *= inv;
+                f[1] *= inv;
+            }
+            // Columns c .. c + 16 of the row, pairs at v[0 .. 16).
+            auto load16 = [&](int c, float (&v)[16]) {
+                uint32_t a[16], b[16];
+                if (has[0]) tmem_ld16(row_addr + col0 + c, a);
+                if (has[1]) tmem_ld16(row_addr + col1 + c, b);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    v[k] = has[0] ? __uint_as_float(a[k]) * f[0] : 0.0f;
+                    if (has[1]) v[k] = fmaf(__uint_as_float(b[k]), f[1], v[k]);
+                    if (ll == 0.0f) v[k] = 0.0f;   // no key, whatever the values hold
+                }
+            };
+            const long long tok0 = x.q0 + (pair ? tile * p.tok_tile : 0);
+            if (whole) {
+#pragma unroll 1
+                for (int h = 0; h < D; h += 64) {
+                    uint32_t out[32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float v[16];
+                        load16(h + 16 * k, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) out[8 * k + e] = ptx::pack2<kBf16>(v[2 * e], v[2 * e + 1]);
+                    }
+                    store_rows(out, wslice, lane, [&](int r) -> uint4* {
+                        r += 32 * q;
+                        if (r >= rows) return nullptr;
+                        const int tk = by_group(r, inv_group);
+                        const long long line = (tok0 + tk) * p.hq + x.h * p.group + (r - tk * p.group);
+                        return reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + line * D + h);
+                    });
+                }
+                if (row < rows) {
+                    const int tk = by_group(row, inv_group);
+                    p.lse[(tok0 + tk) * p.hq + x.h * p.group + (row - tk * p.group)] =
+                        ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
+                }
+            } else {
+                const long long line0 = static_cast<long long>(x.buffer) * p.part_rows + tile * kBM;
+#pragma unroll 1
+                for (int h = 0; h < D; h += 32) {
+                    uint32_t out[32];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float v[16];
+                        load16(h + 16 * k, v);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) out[16 * k + e] = __float_as_uint(v[e]);
+                    }
+                    store_rows(out, wslice, lane, [&](int r) -> uint4* {
+                        r += 32 * q;
+                        return r < rows ? reinterpret_cast<uint4*>(p.part_o + (line0 + r) * D + h) : nullptr;
+                    });
+                }
+                if (row < rows) *reinterpret_cast<float2*>(p.part_ml + 2 * (line0 + row)) = make_float2(mm, ll);
+            }
+        }
+        ptx::tc_fence_before();
+        if (!ok) break;
+    }
+}
+
+// ---------------------------------------------------------------- kernels
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa2_kv16_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV, const Params p) {
+    using L = Lay<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_addr(smem);
+    BarSet<D> bars;
+    bars.base = sbase + L::kBarOff;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(bars.q_full(t), 1);
+            ptx::mbar_init(bars.q_empty(t), 1);
+            ptx::mbar_init(bars.s_full(t), 1);
+            ptx::mbar_init(bars.alpha_ready(t), kBM);
+            ptx::mbar_init(bars.stats_ready(t), kBM);
+            ptx::mbar_init(bars.stats_free(t), kBM);
+            ptx::mbar_init(bars.p_full(t), 2 * kBM);
+            ptx::mbar_init(bars.o_full(t), 1);
+        }
+        for (int s = 0; s < L::kStages; ++s) {
+            ptx::mbar_init(bars.kv_full(s), 1);
+            ptx::mbar_init(bars.kv_empty(s), 1);
+        }
+        for (int s = 0; s < kParts; ++s) {
+            ptx::mbar_init(bars.part_full(s), 1);
+            ptx::mbar_init(bars.part_empty(s), kPartUsers);
+        }
+        ptx::mbar_init(bars.mma_done(), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kLoadWarp && lane == 0) {
+        ptx::tma_prefetch_desc(&tmQ);
+        ptx::tma_prefetch_desc(&tmKV);
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), Layout<D>::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    kv4::enter_stream_order();
+    const uint32_t tmem = *tmem_slot;
+    const Waiter w{abort_flag, p.wait_limit_ns};
+
+    if (warp < kCorrWarp0) {
+        ptx::setmaxnreg_inc<kRegSoftmax>();
+        softmax_role<D, kBf16>(p, tmem, smem, sbase, bars, w, warp / 4);
+    } else if (warp < kLoadWarp) {
+        ptx::setmaxnreg_dec<kRegCorr>();
+        correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
+    } else {
+        ptx::setmaxnreg_dec<kRegOther>();
+        if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
+        else if (warp == kMmaWarp) mma_issuer<D, kBf16>(p, smem, sbase, tmem, bars, w);
+        else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, Layout<D>::kTmemCols);
+    }
+}
+
+// Joins the partial results of the row blocks that several CTAs share, and
+// writes the rows that no key is visible to where a whole block has none
+// (O = 0, LSE = -inf). Block (c, y) has every kJoinY-th of the rows that CTA c
+// began.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) fa2_kv16_join_kernel(const Params p) {
+    constexpr int W = kJoinThreads / 32, kVecs = D / 4;   // lanes of a row, four elements each
+    __shared__ float4 acc[W][32];
+    __shared__ float2 stat[W];
+    kv4::enter_stream_order();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+    const Begun begun = p.begun[c];
+    const int rows = begun.ntok * p.group;
+    // Row k of the block: its line in a buffer and in the output.
+    auto buffer_row = [&](int k) {
+        const int tok = k / p.group, tile = tok / p.tok_tile;
+        return tile * kBM + k - tile * p.tok_tile * p.group;
+    };
+    auto finish = [&](int k, float m, float l, const float4& o) {
+        const int tok = k / p.group;
+        const long long line = static_cast<long long>(begun.q0 + tok) * p.hq + begun.h * p.group + (k - tok * p.group);
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        if (lane < kVecs)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + line * D + 4 * lane) =
+                make_uint2(ptx::pack2<kBf16>(o.x * inv, o.y * inv), ptx::pack2<kBf16>(o.z * inv, o.w * inv));
+        if (lane == 0) p.lse[line] = l != 0.0f ? (m + ptx::lg2_approx(l)) * 0.69314718055994530942f : -INFINITY;
+    };
+    // Adds parts i0, i0 + step, .. of row k to (m, l, o), a running softmax.
+    auto add = [&](int k, int i0, int step, float& m, float& l, float4& o) {
+        const int r = buffer_row(k);
+        constexpr int U = 4;
+        for (int i = i0; i < begun.parts; i += U * step) {
+            float2 ml[U];
+            float4 v[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                const int part = i + e * step;
+                ml[e] = make_float2(-INFINITY, 0.0f);
+                if (part >= begun.parts) continue;
+                const long long line = (2LL * (c + part) + (part == 0 ? 1 : 0)) * p.part_rows + r;
+                ml[e] = *reinterpret_cast<const float2*>(p.part_ml + 2 * line);
+                if (lane < kVecs) v[e] = *reinterpret_cast<const float4*>(p.part_o + line * D + 4 * lane);
+            }
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < U; ++e) top = fmaxf(top, ml[e].x);
+            const float ref = top == -INFINITY ? 0.0f : top, f0 = ptx::ex2_approx(m - ref);
+            l *= f0;
+            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+            m = top;
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                if (ml[e].x == -INFINITY && ml[e].y == 0.0f) continue;   // it saw no key
+                const float f = ptx::ex2_approx(ml[e].x - ref);
+                l = fmaf(f, ml[e].y, l);
+                if (lane < kVecs) kv4::axpy4(o, f, v[e]);
+            }
+        }
+    };
+    if (begun.parts > 2 * W) {   // many parts: the warps share those of a row
+        for (int k = blockIdx.y; k < rows; k += kJoinY) {
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0, 0, 0, 0);
+            add(k, warp, W, m, l, o);
+            acc[warp][lane] = o;
+            if (lane == 0) stat[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp == 0) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < W; ++e) top = fmaxf(top, stat[e].x);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                l = 0.0f;
+                o = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    const float f = ptx::ex2_approx(stat[e].x - ref);
+                    l = fmaf(f, stat[e].y, l);
+                    kv4::axpy4(o, f, acc[e][lane]);
+                }
+                finish(k, top, l, o);
+            }
+            __syncthreads();
+        }
+    } else if (begun.parts > 0) {
+        for (int k = blockIdx.y * W + warp; k < rows; k += kJoinY * W) {
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0, 0, 0, 0);
+            add(k, 0, 1, m, l, o);
+            finish(k, m, l, o);
+        }
+    }
+    // Blocks of rows without a key.
+    for (int b = c; b < p.B; b += gridDim.x) {
+        const Request r = request(p, b);
+        const int none = r.n == 0 ? 0 : r.len == 0 ? r.n : min(r.n, first_block(p, r) * 2 * p.tok_tile);
+        const long long lines = static_cast<long long>(none) * p.hq, line0 = static_cast<long long>(r.start) * p.hq;
+        for (long long i = blockIdx.y * kJoinThreads + threadIdx.x; i < lines * (D / 8); i += kJoinY * kJoinThreads)
+            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + line0 * D)[i] = make_uint4(0, 0, 0, 0);
+        for (long long i = blockIdx.y * kJoinThreads + threadIdx.x; i < lines; i += kJoinY * kJoinThreads) p.lse[line0 + i] = -INFINITY;
+    }
+}
+
+}  // namespace kv16
+}  // namespace fa2

@@ -25,6 +25,7 @@ FA2_ERR_BOUNDS = 5   # a device-side bounds check failed (KV cache: every build;
 # symbols declared in include/fa2.h
 EXPORTS = ("fa2_fwd", "fa2_fwd_gqa", "fa2_fwd_ex", "fa2_fwd_fp8", "fa2_fwd_fp8_ex", "fa2_bwd", "fa2_bwd_noalloc",
            "fa2_kv4_plan", "fa2_kv4_append", "fa2_kv4_gather", "fa2_fwd_kv4", "fa2_fwd_kv4_workspace",
+           "fa2_rope", "fa2_rope_bwd", "fa2_kv16_append", "fa2_fwd_kv16", "fa2_fwd_kv16_workspace",
            "fa2_check_status", "fa2_status_string",
            "fa2_set_wait_limit_ns", "fa2_set_debug_flags", "fa2_set_tile_config", "fa2_version")
 
@@ -72,6 +73,16 @@ def load(path: str = LIB_PATH):
     lib.fa2_fwd_kv4.restype = i
     lib.fa2_fwd_kv4_workspace.argtypes = [i, i, i, i, i, i, i]
     lib.fa2_fwd_kv4_workspace.restype = ll
+    lib.fa2_rope.argtypes = [p] * 7 + [i] * 8 + [p, i, p]
+    lib.fa2_rope.restype = i
+    lib.fa2_rope_bwd.argtypes = [p] * 7 + [i] * 8 + [p, i, p]
+    lib.fa2_rope_bwd.restype = i
+    lib.fa2_kv16_append.argtypes = [p] * 9 + [i] * 7 + [p, i, i, i, p]
+    lib.fa2_kv16_append.restype = i
+    lib.fa2_fwd_kv16.argtypes = [p] * 9 + [ll, i, i, i, i, i, ll, ll, i, i, i, f, i, i, p]
+    lib.fa2_fwd_kv16.restype = i
+    lib.fa2_fwd_kv16_workspace.argtypes = [i] * 7
+    lib.fa2_fwd_kv16_workspace.restype = ll
     lib.fa2_check_status.argtypes = [p]
     lib.fa2_check_status.restype = i
     lib.fa2_status_string.argtypes = [i]
@@ -175,6 +186,53 @@ def fa2_fwd_kv4_workspace(B: int, H_q: int, H_kv: int, N_q: int, d: int, max_pag
     """Bytes of workspace that fa2_fwd_kv4 needs for these sizes, whatever the
     lengths; -1 for sizes that it does not take."""
     return load().fa2_fwd_kv4_workspace(B, H_q, H_kv, N_q, d, max_pages, page_size)
+
+
+def _numbers(x, n):
+    """A host array of n int64 strides."""
+    if len(x) != n:
+        raise ValueError(f"expected {n} strides, got {len(x)}")
+    return (ctypes.c_int64 * n)(*x)
+
+
+def fa2_rope_ptr(q, k, q_out, k_out, positions, inv_freq, axes, B, H_q, H_kv, N, d, rot_dim, n_axes, interleaved, strides,
+                 dtype, stream=0) -> int:
+    """fa2_rope on raw device addresses (ints; k, k_out and axes may be 0) and
+    12 strides in elements; returns the status code."""
+    return load().fa2_rope(q, k or None, q_out, k_out or None, positions, inv_freq, axes or None, B, H_q, H_kv, N, d, rot_dim,
+                           n_axes, int(interleaved), _numbers(strides, 12), int(dtype), stream or None)
+
+
+def fa2_rope_bwd_ptr(dq_out, dk_out, dq, dk, positions, inv_freq, axes, B, H_q, H_kv, N, d, rot_dim, n_axes, interleaved,
+                     strides, dtype, stream=0) -> int:
+    """fa2_rope_bwd on raw device addresses (ints; dk_out, dk and axes may be
+    0) and 12 strides in elements; returns the status code."""
+    return load().fa2_rope_bwd(dq_out, dk_out or None, dq, dk or None, positions, inv_freq, axes or None, B, H_q, H_kv, N, d,
+                               rot_dim, n_axes, int(interleaved), _numbers(strides, 12), int(dtype), stream or None)
+
+
+def fa2_kv16_append_ptr(q, k, v, slots, positions, inv_freq, axes, cache, q_out, T, H_q, H_kv, d, rot_dim, n_axes,
+                        interleaved, strides, page_size, num_pages, dtype, stream=0) -> int:
+    """fa2_kv16_append on raw device addresses (ints; q, q_out, positions,
+    inv_freq and axes may be 0) and 6 strides in elements; returns the status
+    code."""
+    return load().fa2_kv16_append(q or None, k, v, slots, positions or None, inv_freq or None, axes or None, cache,
+                                  q_out or None, T, H_q, H_kv, d, rot_dim, n_axes, int(interleaved), _numbers(strides, 6),
+                                  page_size, num_pages, int(dtype), stream or None)
+
+
+def fa2_fwd_kv16_ptr(q, cache, block_table, seq_lens, q_starts, q_lens, o, lse, workspace, workspace_bytes, T, B, H_q, H_kv, d,
+                     q_stride_t, q_stride_h, max_pages, page_size, num_pages, scale, causal, dtype, stream=0) -> int:
+    """fa2_fwd_kv16 on raw device addresses (ints); returns the status code."""
+    return load().fa2_fwd_kv16(q, cache, block_table, seq_lens, q_starts, q_lens, o, lse, workspace, workspace_bytes, T, B, H_q,
+                               H_kv, d, q_stride_t, q_stride_h, max_pages, page_size, num_pages, float(scale), int(causal),
+                               int(dtype), stream or None)
+
+
+def fa2_fwd_kv16_workspace(T: int, B: int, H_q: int, H_kv: int, d: int, max_pages: int, page_size: int) -> int:
+    """Bytes of workspace that fa2_fwd_kv16 needs for these sizes, whatever the
+    lengths; -1 for sizes that it does not take."""
+    return load().fa2_fwd_kv16_workspace(T, B, H_q, H_kv, d, max_pages, page_size)
 
 
 def fa2_check_status(stream=0) -> int:
@@ -428,7 +486,8 @@ def _kv4():
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kv4_torch", loader))
         loader.exec_module(mod)
         mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.fa2_kv4_plan, lib.fa2_kv4_append, lib.fa2_kv4_gather, lib.fa2_fwd_kv4, lib.fa2_fwd_kv4_workspace)),
+            lib.fa2_kv4_plan, lib.fa2_kv4_append, lib.fa2_kv4_gather, lib.fa2_fwd_kv4, lib.fa2_fwd_kv4_workspace, lib.fa2_rope,
+            lib.fa2_rope_bwd, lib.fa2_kv16_append, lib.fa2_fwd_kv16, lib.fa2_fwd_kv16_workspace)),
                  torch.OutOfMemoryError)
         _kv4_mod = mod
     return _kv4_mod
@@ -483,4 +542,60 @@ def fa2_fwd_kv4(q, cache, block_table, seq_lens, k_descale, v_descale, o=None, l
                                    causal, stream)
     if type(out) is int:
         raise FA2Error(out, "fa2_fwd_kv4")
+    return out
+
+
+# ------------------------------------------------------------------ rotary positions, the paged 16-bit KV cache
+
+def fa2_rope(q, k, positions, inv_freq, axes=None, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Rotates q [B, Hq, N, d] and k [B, Hkv, N, d] (or None) by their
+    positions, int32 [n_axes, B, N] (or [B, N] for one axis): pair i, of the
+    first 2 * len(inv_freq) elements, by positions[axes[i]] * inv_freq[i]
+    (include/fa2.h). Tensors may have any strides that are multiples of 8 elements,
+    rows of adjacent elements; outputs are dense if not given, and may be the
+    inputs. Returns (q_out, k_out)."""
+    out = (_kv4_mod or _kv4()).rope(q, k, positions, inv_freq, axes, interleaved, q_out, k_out, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_rope")
+    return out
+
+
+def fa2_rope_bwd(dq_out, dk_out, positions, inv_freq, axes=None, interleaved=False, dq=None, dk=None, stream=None):
+    """The gradient of fa2_rope: from dq_out, dk_out (or None), those of its
+    outputs, to those of its inputs. Arguments as fa2_rope. Returns (dq, dk)."""
+    out = (_kv4_mod or _kv4()).rope_bwd(dq_out, dk_out, positions, inv_freq, axes, interleaved, dq, dk, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_rope_bwd")
+    return out
+
+
+def fa2_kv16_cache_shape(num_pages: int, H_kv: int, page_size: int, d: int) -> tuple:
+    """Shape of the bf16 or fp16 cache tensor (layout: include/fa2.h)."""
+    return (num_pages, H_kv, 2, page_size, d)
+
+
+def fa2_kv16_append(k, v, slots, cache, q=None, positions=None, inv_freq=None, axes=None, interleaved=False, q_out=None,
+                    stream=None):
+    """Writes k, v [T, Hkv, d] into the slots [T] of the cache (negative ones
+    are skipped, no other may occur twice), with positions int32 [n_axes, T] (or
+    [T]) the keys rotated as fa2_rope does, and q [T, Hq, d] too, into q_out
+    [T, Hq, d]. k, v and q may have any strides that are multiples of 8 elements,
+    rows of adjacent elements. Returns (cache, q_out), q_out None without q."""
+    out = (_kv4_mod or _kv4()).append16(k, v, slots, cache, q, positions, inv_freq, axes, interleaved, q_out, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_kv16_append")
+    return out
+
+
+def fa2_fwd_kv16(q, cache, block_table, seq_lens, q_starts, q_lens, o=None, lse=None, workspace=None, scale=None, causal=False,
+                 stream=None):
+    """Attention of each request's newest tokens over its seq_lens[b] cached
+    ones: rows q_starts[b] .. + q_lens[b] of q [T, Hq, d] (strides as in
+    fa2_kv16_append). Rows of o and lse that belong to no request stay as they
+    were. `workspace`: a CUDA tensor of fa2_fwd_kv16_workspace(...) bytes that no
+    other call in flight uses; allocated with torch when not given, as o and lse
+    are. Returns (o [T, Hq, d], lse fp32 [T, Hq])."""
+    out = (_kv4_mod or _kv4()).fwd16(q, cache, block_table, seq_lens, q_starts, q_lens, o, lse, workspace, scale, causal, stream)
+    if type(out) is int:
+        raise FA2Error(out, "fa2_fwd_kv16")
     return out

@@ -357,6 +357,119 @@ fa2_status fa2_fwd_kv4(const void* q, const void* cache, const int32_t* block_ta
 int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_pages, int page_size);
 
 /*
+ * Rotary positions with several axes (one for text; time, height and width
+ * for images and video). (The source pages take q and k as they are; this
+ * makes them.) Of each head's d elements the first rot_dim are rotated, as
+ * rot_dim / 2 pairs: pair i is elements i and i + rot_dim / 2, or 2i and 2i + 1
+ * with interleaved = 1. Its angle is positions[axes[i]][b, n] * inv_freq[i], and
+ *     y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * in fp32, rounded once; elements behind rot_dim are copied. Angles are exact
+ * in a turn to 2^-32 of it for every position, far ones too.
+ *   q, q_out : [B, H_q, N, d] bf16 or fp16; k, k_out : [B, H_kv, N, d], or both
+ *              NULL with H_kv = 0. Elements of a row adjacent
+ *   strides  : 12 numbers in host memory, read during the call: the strides of
+ *              batch entry, head and token of q, of k, of q_out and of k_out, in
+ *              elements (multiples of 8, 0 .. 2^31 - 8; 0 in an output only for
+ *              an axis of length 1), so that q and k may be views of a
+ *              projection's output. Those of k and k_out are not read without k
+ *   positions : [n_axes, B, N] int32, any value; inv_freq : [rot_dim / 2] fp32,
+ *              finite; axes : [rot_dim / 2] int32 or NULL (all 0). An axis outside
+ *              0 .. n_axes - 1 is reported by fa2_check_status as FA2_ERR_BOUNDS
+ *              and its pair's angle is 0
+ *   d : 64 or 128; rot_dim : a multiple of 16 up to d; n_axes : up to 8
+ * An output may be its input (with its strides); otherwise nothing that is
+ * written may overlap anything else. Pointers: tensors 16-byte aligned, others 4-byte
+ * aligned. B * N < 2^31 - 1024. Errors otherwise as fa2_fwd_gqa; nothing is
+ * allocated; one launch.
+ */
+fa2_status fa2_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                    const float* inv_freq, const int32_t* axes, int B, int H_q, int H_kv, int N, int d,
+                    int rot_dim, int n_axes, int interleaved, const int64_t* strides, fa2_dtype dtype,
+                    cudaStream_t stream);
+
+/*
+ * The gradient of fa2_rope: from those of its outputs (such as dq and dk of
+ * fa2_bwd) to those of its inputs, the rotation by the opposite angles. Arguments
+ * as fa2_rope, with dq_out, dk_out read and dq, dk written.
+ */
+fa2_status fa2_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const int32_t* positions,
+                        const float* inv_freq, const int32_t* axes, int B, int H_q, int H_kv, int N, int d,
+                        int rot_dim, int n_axes, int interleaved, const int64_t* strides, fa2_dtype dtype,
+                        cudaStream_t stream);
+
+/*
+ * A paged KV cache in the tensors' own 16 bits. (The source pages leave the KV
+ * cache out.) The cache is the caller's device memory,
+ *     cache : [num_pages, H_kv, 2, page_size, d] bf16 or fp16
+ * of a page and KV head first the keys of page_size tokens, then the values. A
+ * token's place is its slot, page * page_size + offset; slots, block tables and
+ * lengths are those of the 4-bit cache, and fa2_kv4_plan makes them for both.
+ * Tokens come packed, [T, H, d], whatever requests they belong to.
+ *   d : 64 or 128; page_size : 16, 32, 64 or 128; num_pages * page_size < 2^31 - 256
+ * Page ids, slots, rows and lengths that point outside the cache, the table or
+ * the tensors are skipped on the device and reported by fa2_check_status as
+ * FA2_ERR_BOUNDS. Pointers: tensors, cache and workspace 16-byte aligned, the
+ * others 4-byte aligned. Errors otherwise as fa2_fwd_gqa; nothing is allocated.
+ */
+
+/*
+ * Writes new keys and values into their slots, the keys rotated on the way, and
+ * rotates the queries of the same tokens.
+ *   k, v     : [T, H_kv, d]; q : [T, H_q, d] or NULL with H_q = 0
+ *   q_out    : [T, H_q, d] dense (output; NULL without q; may be q if that is dense)
+ *   strides  : 6 numbers in host memory: the strides of token and head of q, k
+ *              and v, in elements (multiples of 8, 0 .. 2^31 - 8)
+ *   slots    : [T] int32; the keys and values of a negative slot are skipped, its
+ *              queries are not. A slot may be named once in a call
+ *   positions, inv_freq, axes, rot_dim, n_axes, interleaved : as fa2_rope, with
+ *              positions [n_axes, T]; positions NULL with rot_dim = 0 and without q:
+ *              keys are written as they are
+ * T < 2^31 - 1024. One launch.
+ */
+fa2_status fa2_kv16_append(const void* q, const void* k, const void* v, const int32_t* slots,
+                           const int32_t* positions, const float* inv_freq, const int32_t* axes, void* cache,
+                           void* q_out, int T, int H_q, int H_kv, int d, int rot_dim, int n_axes,
+                           int interleaved, const int64_t* strides, int page_size, int num_pages,
+                           fa2_dtype dtype, cudaStream_t stream);
+
+/*
+ * Attention of each request's newest tokens, one or a whole chunk of a prompt,
+ * over its cached tokens (their own keys and values included, if they were
+ * appended). Requests of any lengths go in one call.
+ *   q        : [T, H_q, d] 16-bit, of the cache's type; strides of token and
+ *              head in elements (multiples of 8, 8 .. 2^31 - 8)
+ *   o        : [T, H_q, d] dense; lse : [T, H_q] fp32
+ *   q_starts, q_lens : [B] int32: request b's new tokens are rows q_starts[b] ..
+ *              q_starts[b] + q_lens[b] - 1; 0 for an idle request. No row may belong
+ *              to two. Rows of o and lse that belong to no request stay as they were
+ *   seq_lens : [B] int32, cached tokens of each request
+ *   block_table : [B, max_pages] int32, max_pages * page_size < 2^31 - 256; entries
+ *              behind a request's last page are never read
+ *   causal   : 0 or 1. With 1, new token i of request b attends position
+ *              j < seq_lens[b] + i + 1 - q_lens[b]. A row with no allowed key gets
+ *              O = 0 and LSE = -inf
+ *   workspace : device, fa2_fwd_kv16_workspace(...) bytes, contents irrelevant
+ *              before and after; calls that may overlap need their own
+ * Query heads that share a KV head: up to 128. Both products take 16-bit operands:
+ * the softmax's weights are rounded to the cache's type (bf16 2^-8, fp16 2^-11);
+ * scores, sums and partial results are fp32. What lies in a request's pages behind
+ * its last token has no effect, whatever it is. A page that is skipped reads as
+ * zeros.
+ * T * H_q < 2^31, num_pages * H_kv < 2^30 - 1, and the blocks of two tiles of 128
+ * query rows times H_kv times the tiles of 128 keys of a full table up to 2^30. Two
+ * launches.
+ */
+fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                        const int32_t* q_starts, const int32_t* q_lens, void* o, float* lse, void* workspace,
+                        int64_t workspace_bytes, int T, int B, int H_q, int H_kv, int d, int64_t q_stride_t,
+                        int64_t q_stride_h, int max_pages, int page_size, int num_pages, float scale, int causal,
+                        fa2_dtype dtype, cudaStream_t stream);
+
+/* Bytes of workspace that fa2_fwd_kv16 needs for these sizes, whatever the
+ * lengths; -1 for sizes that it does not take. */
+int64_t fa2_fwd_kv16_workspace(int T, int B, int H_q, int H_kv, int d, int max_pages, int page_size);
+
+/*
  * Synchronises `stream`, then reads and clears the status word of the device
  * that `stream` belongs to (the current device is switched to it for the
  * read and restored afterwards). Returns FA2_ERR_TIMEOUT if a kernel since
