@@ -717,25 +717,25 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
 
 // ---------------------------------------------------------------- correction + epilogue
 
-// Stores 128 bytes of each of 32 rows (v: the calling lane's row) through the
-// warp's 4 KB staging slice as whole lines; see store_o_rows. to(r): where row r
-// of the 32 goes, NULL for nowhere.
+// The warp's 4 KB staging slice holds 128 bytes of each of its 32 rows, as in
+// store_o_rows: each lane puts 16-byte pieces of its own row, then the warp
+// stores whole lines.
+__device__ __forceinline__ void put_piece(uint32_t wslice, int lane, int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    ptx::st_shared_v4(wslice + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(c) ^ (lane & 7u)) << 4), x, y, z, w);
+}
+// to(r): where row r of the 32 goes, NULL for nowhere.
 template <typename To>
-__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], uint32_t wslice, int lane, To to) {
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        ptx::st_shared_v4(wslice + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(c) ^ (lane & 7u)) << 4), v[4 * c],
-                          v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+__device__ __forceinline__ void store_lines(uint32_t wslice, int lane, To to) {
     __syncwarp();
     const int r0 = lane >> 3;
     const uint32_t rd = wslice + static_cast<uint32_t>(r0) * 128u + (static_cast<uint32_t>((lane & 7) ^ r0) << 4);
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < 8; ++i) {
         const uint4 x = ptx::ld_shared_v4((rd ^ ((i & 1) << 6)) + static_cast<uint32_t>(i) * 512u);
         uint4* at = to(4 * i + r0);
         if (at) at[lane & 7] = x;
     }
+    __syncwarp();   // before the slice is written again
 }
 
 template <int D, bool kBf16>
@@ -772,7 +772,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                     ptx::tc_fence_after();
                     const uint32_t colO = Layout<D>::col_o(t);
                     const uint64_t a2 = ptx::f2_pack(alpha, alpha);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < D; h += 32) {
                         uint32_t o[32];
                         ptx::tmem_ld32_at<0>(row_addr + colO + h, o);
@@ -826,65 +826,72 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 f[1] = ptx::ex2_approx(m[1] - ref);
                 ll = f[0] * l[0] + f[1] * l[1];
             }
-            const bool whole = x.buffer < 0;
-            const uint32_t col0 = Layout<D>::col_o(pair ? tile : 0), col1 = Layout<D>::col_o(1);
-            if (whole) {
+            const uint32_t col0 = Layout<D>::col_o(pair ? tile : 0);
+            if (x.buffer < 0) {
                 // l = 0 only for a row without a key: O = 0, LSE = -inf.
-                const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
+                const float inv = ll != 0.0f ? ptx::rcp_approx(ll) : 0.0f;
                 f[0] *= inv;
                 f[1] *= inv;
             }
-            // Columns c .. c + 16 of the row, pairs at v[0 .. 16).
+            // Columns c .. c + 16 of the row: of the tile's stream, or of both.
             auto load16 = [&](int c, float (&v)[16]) {
-                uint32_t a[16], b[16];
-                if (has[0]) tmem_ld16(row_addr + col0 + c, a);
-                if (has[1]) tmem_ld16(row_addr + col1 + c, b);
+                uint32_t a[16];
+                tmem_ld16(row_addr + col0 + c, a);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    v[k] = has[0] ? __uint_as_float(a[k]) * f[0] : 0.0f;
-                    if (has[1]) v[k] = fmaf(__uint_as_float(b[k]), f[1], v[k]);
-                    if (ll == 0.0f) v[k] = 0.0f;   // no key, whatever the values hold
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(a[k]) * f[0];
+                if (has[1]) {
+                    tmem_ld16(row_addr + Layout<D>::col_o(1) + c, a);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(a[k]), f[1], v[k]);
+                }
+                if (ll == 0.0f) {   // no key, whatever the values hold
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = 0.0f;
                 }
             };
             const long long tok0 = x.q0 + (pair ? tile * p.tok_tile : 0);
-            if (whole) {
+            if (x.buffer < 0) {
+                const long long line0 = tok0 * p.hq + x.h * p.group;
 #pragma unroll 1
                 for (int h = 0; h < D; h += 64) {
-                    uint32_t out[32];
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         float v[16];
                         load16(h + 16 * k, v);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) out[8 * k + e] = ptx::pack2<kBf16>(v[2 * e], v[2 * e + 1]);
+                        for (int e = 0; e < 2; ++e)
+                            put_piece(wslice, lane, 2 * k + e, ptx::pack2<kBf16>(v[8 * e], v[8 * e + 1]),
+                                      ptx::pack2<kBf16>(v[8 * e + 2], v[8 * e + 3]), ptx::pack2<kBf16>(v[8 * e + 4], v[8 * e + 5]),
+                                      ptx::pack2<kBf16>(v[8 * e + 6], v[8 * e + 7]));
                     }
-                    store_rows(out, wslice, lane, [&](int r) -> uint4* {
+                    store_lines(wslice, lane, [&](int r) -> uint4* {
                         r += 32 * q;
-                        if (r >= rows) return nullptr;
                         const int tk = by_group(r, inv_group);
-                        const long long line = (tok0 + tk) * p.hq + x.h * p.group + (r - tk * p.group);
-                        return reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + line * D + h);
+                        const long long line = line0 + static_cast<long long>(tk) * p.hq + (r - tk * p.group);
+                        return r < rows ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + line * D + h) : nullptr;
                     });
                 }
                 if (row < rows) {
                     const int tk = by_group(row, inv_group);
-                    p.lse[(tok0 + tk) * p.hq + x.h * p.group + (row - tk * p.group)] =
+                    p.lse[line0 + static_cast<long long>(tk) * p.hq + (row - tk * p.group)] =
                         ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
                 }
             } else {
                 const long long line0 = static_cast<long long>(x.buffer) * p.part_rows + tile * kBM;
 #pragma unroll 1
                 for (int h = 0; h < D; h += 32) {
-                    uint32_t out[32];
-#pragma unroll
+#pragma unroll 1
                     for (int k = 0; k < 2; ++k) {
                         float v[16];
                         load16(h + 16 * k, v);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) out[16 * k + e] = __float_as_uint(v[e]);
+                        for (int e = 0; e < 4; ++e)
+                            put_piece(wslice, lane, 4 * k + e, __float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                      __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
                     }
-                    store_rows(out, wslice, lane, [&](int r) -> uint4* {
+                    store_lines(wslice, lane, [&](int r) -> uint4* {
                         r += 32 * q;
                         return r < rows ? reinterpret_cast<uint4*>(p.part_o + (line0 + r) * D + h) : nullptr;
                     });
