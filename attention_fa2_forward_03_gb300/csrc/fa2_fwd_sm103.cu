@@ -1113,10 +1113,11 @@ fa2_status kv16_encode_q(CUtensorMap* m, const void* ptr, int T, int H_q, int d,
     return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
 }
 
-// Units (a row block against 128 keys) that T new tokens of B requests can have.
+// Row blocks that T new tokens of B requests can have, for each KV head, and
+// the units of all.
+long long kv16_blocks(int T, int B, int H_q, int H_kv) { return T / (2 * (128 / (H_q / H_kv))) + std::min(T, B); }
 long long kv16_units(int T, int B, int H_q, int H_kv, long long max_tokens) {
-    const long long block = 2 * (128 / (H_q / H_kv));
-    return (T / block + std::min(T, B)) * H_kv * ((max_tokens + 127) / 128);
+    return kv16_blocks(T, B, H_q, H_kv) * H_kv * (fa2::kv16::kStart + std::max(fa2::kv16::kPairUnits, fa2::kv16::kSingleUnits) * ((max_tokens + 127) / 128));
 }
 
 fa2_status kv16_check_sizes(int T, int B, int H_q, int H_kv, int d, int max_pages, int page_size) {
@@ -1125,8 +1126,7 @@ fa2_status kv16_check_sizes(int T, int B, int H_q, int H_kv, int d, int max_page
     if (st != FA2_OK) return st;
     if ((d != 64 && d != 128) || H_q / H_kv > 128) return FA2_ERR_UNSUPPORTED;
     if (static_cast<long long>(T) * H_q > 0x7FFFFFFFLL || B > 0x7FFFFFFF - 1024) return FA2_ERR_UNSUPPORTED;
-    const long long blocks = T / (2 * (128 / (H_q / H_kv))) + std::min(T, B);
-    if (blocks * H_kv > (1LL << 30) || kv16_units(T, B, H_q, H_kv, static_cast<long long>(max_pages) * page_size) > (1LL << 30))
+    if (kv16_blocks(T, B, H_q, H_kv) * H_kv > (1LL << 30) || kv16_units(T, B, H_q, H_kv, static_cast<long long>(max_pages) * page_size) > (1LL << 30))
         return FA2_ERR_UNSUPPORTED;
     return FA2_OK;
 }

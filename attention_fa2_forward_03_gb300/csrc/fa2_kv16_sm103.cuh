@@ -31,6 +31,7 @@
 #include "fa2.h"
 #include "fa2_fwd_sm103.cuh"
 #include "fa2_kv4_sm103.cuh"
+#include "fa2_kv4_tc_sm103.cuh"
 #include "ptx_sm103.cuh"
 
 namespace fa2 {
@@ -43,7 +44,17 @@ enum Site : int { kSiteRows = 53, kSitePart = 54 };
 
 constexpr int kMaxCtas = 160;
 constexpr int kSchedWarp = 14;
-constexpr int kMinRun = 2;        // units a CTA has at least
+// Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
+// for one, and every row block kStart more for its start and its end.
+#ifndef K16P
+#define K16P 3
+#define K16S 2
+#define K16B 4
+#define K16M 4
+#endif
+constexpr int kPairUnits = K16P, kSingleUnits = K16S;
+constexpr int kStart = K16B;
+constexpr int kMinRun = K16M;        // units of a run at least
 constexpr int kParts = 4;         // parts on their way from the scheduling warp
 constexpr int kPartUsers = 14;    // warps that read a part
 constexpr int kJoinY = 4, kJoinThreads = 256;
@@ -107,7 +118,8 @@ struct Lay {
     static constexpr int kRowOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // alpha[2][128], m[2][128], l[2][128]
     static constexpr int kPartOff = kRowOff + 6 * kBM * 4;
     static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
-    static constexpr int kMiscOff = kIdOff + 4 * 32 * 4;
+    static constexpr int kLineOff = kIdOff + 4 * 32 * 4;   // lines of a tile's rows in o, and 0 .. 127: those in a buffer
+    static constexpr int kMiscOff = kLineOff + 2 * kBM * 4;
     static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -119,15 +131,6 @@ struct BarSet : Bars<D> {
     __device__ uint32_t part_empty(int s) const { return this->base + 8 * (17 + 2 * S + kParts + s); }
 };
 
-// 16 columns of the thread's lane of tensor memory.
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(a));
-}
-
 // ---------------------------------------------------------------- the line of units
 
 // A request as the call may use it: what points outside q or the table counts
@@ -136,8 +139,8 @@ struct Request {
     int start, n, len, blocks;
 };
 
-__device__ __forceinline__ Request request(const Params& p, int b) {
-    Request r{p.q_starts[b], p.q_lens[b], p.seq_lens[b], 0};
+__device__ __forceinline__ Request request(const Params& p, int start, int n, int len) {
+    Request r{start, n, len, 0};
     if (r.n < 0 || r.start < 0 || r.start > p.T - max(r.n, 0)) {
         if (blockIdx.x == 0 && r.n != 0) report(kSiteRows);
         r.n = 0;
@@ -149,12 +152,13 @@ __device__ __forceinline__ Request request(const Params& p, int b) {
     r.blocks = r.n <= p.tok_tile ? (r.n > 0) : (r.n + 2 * p.tok_tile - 1) / (2 * p.tok_tile);
     return r;
 }
+__device__ __forceinline__ Request request(const Params& p, int b) { return request(p, p.q_starts[b], p.q_lens[b], p.seq_lens[b]); }
 
 __device__ __forceinline__ int tiles_in(int keys) { return keys <= 0 ? 0 : (keys + kBN - 1) / kBN; }
 
 // The sum of floor((a i + b) / m) over i < n, by Euclid's algorithm on (a, m).
-__device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned a, long long b) {
-    long long sum = 0;
+__device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+    unsigned sum = 0;
     while (n > 0) {
         if (a >= m) {
             sum += n * (n - 1) / 2 * (a / m);
@@ -164,7 +168,7 @@ __device__ __forceinline__ long long floor_sum(long long n, unsigned m, unsigned
             sum += n * (b / m);
             b %= m;
         }
-        const long long y = static_cast<long long>(a) * n + b;
+        const unsigned y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
@@ -180,17 +184,22 @@ __device__ __forceinline__ int first_block(const Params& p, const Request& r) {
     return p.causal && r.n > r.len ? (r.n - r.len) / (2 * p.tok_tile) : 0;
 }
 
-// Key tiles of the first x row blocks of one head.
-__device__ __forceinline__ long long tiles_before(const Params& p, const Request& r, int x) {
+// A row block's units: kStart, then its tiles' (none without a tile).
+__device__ __forceinline__ int weight(const Params& p, int ntok) { return ntok > p.tok_tile ? kPairUnits : kSingleUnits; }
+__device__ __forceinline__ int block_units(int tiles, int w) { return tiles > 0 ? kStart + tiles * w : 0; }
+
+// Units of the first x row blocks of one head (below 2^30: the host's bound).
+__device__ __forceinline__ int units_before(const Params& p, const Request& r, int x) {
     if (x <= 0 || r.len == 0) return 0;
-    if (!p.causal) return static_cast<long long>(x) * tiles_in(r.len);
-    const bool last = x >= r.blocks;
-    const int k0 = first_block(p, r), step = 2 * p.tok_tile;
-    long long sum = last ? tiles_in(r.len) : 0;   // its last row sees every key
-    const int full = last ? r.blocks - 1 : x;
-    // block k's last row sees len - n + (k + 1) step keys
-    if (full > k0)
-        sum += floor_sum(full - k0, kBN, step, static_cast<long long>(r.len) - r.n + static_cast<long long>(k0 + 1) * step + kBN - 1);
+    const int step = 2 * p.tok_tile, full = min(x, r.blocks - 1), k0 = first_block(p, r);
+    int sum = 0;
+    if (full > k0) {
+        int tiles = (full - k0) * tiles_in(r.len);
+        // block k's last row sees len - n + (k + 1) step keys
+        if (p.causal) tiles = floor_sum(full - k0, kBN, step, static_cast<unsigned>(r.len - r.n + (k0 + 1) * step) + kBN - 1);
+        sum = (full - k0) * kStart + kPairUnits * tiles;
+    }
+    if (x >= r.blocks) sum += block_units(tiles_in(r.len), weight(p, r.n - (r.blocks - 1) * step));   // its last row sees every key
     return sum;
 }
 
@@ -198,7 +207,7 @@ __device__ __forceinline__ long long tiles_before(const Params& p, const Request
 template <int D>
 __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const BarSet<D>& bars, const Waiter& w) {
     const int lane = threadIdx.x & 31;
-    volatile Part* ring = reinterpret_cast<Part*>(smem + Lay<D>::kPartOff);
+    const uint32_t ring = ptx::smem_addr(smem + Lay<D>::kPartOff);
     int n_part = 0;
     bool ok = true;
     auto put = [&](const Part& x) {
@@ -206,10 +215,11 @@ __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const 
         ok = __all_sync(~0u, w.wait(bars.part_empty(s), ((n_part / kParts) & 1) ^ 1, kSitePart));
         if (!ok) return;
         if (lane == 0) {
-            uint4* to = reinterpret_cast<uint4*>(const_cast<Part*>(&ring[s]));
-            const uint4* from = reinterpret_cast<const uint4*>(&x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = from[i];
+            const uint32_t to = ring + s * static_cast<int>(sizeof(Part));
+            ptx::st_shared_v4(to, x.kind, x.steps0, x.steps1, x.jb);
+            ptx::st_shared_v4(to + 16, x.n, x.len, x.b, x.h);
+            ptx::st_shared_v4(to + 32, x.q0, x.ntok, x.vis0, x.buffer);
+            ptx::st_shared_v4(to + 48, x.qslot, x.jmask0, x.jmask1, 0);
             ptx::mbar_arrive(bars.part_full(s));
         }
         __syncwarp();
@@ -218,69 +228,89 @@ __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const 
 
     // Units in front of each lane's share of the requests.
     const int chunk = (p.B + 31) / 32, b0 = min(lane * chunk, p.B), b1 = min(b0 + chunk, p.B);
-    long long mine = 0, rows = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Request r = request(p, b);
-        mine += tiles_before(p, r, r.blocks) * p.hkv;
-        rows += r.n;
+    int mine = 0, each = 0;   // each: units of a head of the last request looked at, r
+    long long rows = 0;
+    Request r{};
+    for (int b = b0; b < b1; b += 4) {   // four requests' numbers are read at once
+        int s[4], n[4], len[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] = n[e] = len[e] = 0;
+            if (b + e < b1) {
+                s[e] = p.q_starts[b + e];
+                n[e] = p.q_lens[b + e];
+                len[e] = p.seq_lens[b + e];
+            }
+        }
+#pragma unroll 1
+        for (int e = 0; e < min(4, b1 - b); ++e) {
+            r = request(p, s[0], n[0], len[0]);
+            each = units_before(p, r, r.blocks);
+            mine += each * p.hkv;
+            rows += r.n;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                s[k] = s[k + 1];
+                n[k] = n[k + 1];
+                len[k] = len[k + 1];
+            }
+        }
     }
-    long long to = mine;
+    int to = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(~0u, to, o);
+        const int y = __shfl_up_sync(~0u, to, o);
         if (lane >= o) to += y;
         rows += __shfl_xor_sync(~0u, rows, o);
     }
-    long long sum = __shfl_sync(~0u, to, 31);
-    if (rows > p.T) {   // requests name a row twice
+    int total = __shfl_sync(~0u, to, 31);   // below 2^30 if no row has two requests
+    if (rows > p.T) {
         if (blockIdx.x == 0 && lane == 0) report(kSiteRows);
-        sum = 0;
+        total = 0;
     }
-    const int total = static_cast<int>(sum);   // below 2^30: the host's bound for T rows
     const int per = max((total + p.ctas - 1) / p.ctas, kMinRun);
     int u = static_cast<int>(blockIdx.x) * per;
     const int begin = u, end = min(total, u + per);
     Begun begun{0, 0, 0, 0};
     if (u < end) {
-        long long at = to - mine;
-        int b = b0;
+        int at = to - mine, b = b0;
         const bool here = u >= at && u < to;
-        if (here)
+        if (here && chunk > 1)
             while (true) {
-                const Request r = request(p, b);
-                const long long t = tiles_before(p, r, r.blocks) * p.hkv;
-                if (u < at + t) break;
-                at += t;
+                r = request(p, b);
+                each = units_before(p, r, r.blocks);
+                if (u < at + each * p.hkv) break;
+                at += each * p.hkv;
                 ++b;
             }
         const int from = __ffs(__ballot_sync(~0u, here)) - 1;
         b = __shfl_sync(~0u, b, from);
-        const int rem = u - static_cast<int>(__shfl_sync(~0u, at, from));
-        Request r = request(p, b);
-        const int each = static_cast<int>(tiles_before(p, r, r.blocks));
-        int h = rem / each;
-        const int inside = rem - h * each;
+        each = __shfl_sync(~0u, each, from);
+        r = Request{__shfl_sync(~0u, r.start, from), __shfl_sync(~0u, r.n, from), __shfl_sync(~0u, r.len, from),
+                    __shfl_sync(~0u, r.blocks, from)};
+        const int rem = u - __shfl_sync(~0u, at, from);
+        int h = rem / each, inside = rem - h * each, rb = 0;
         // the row block: 32 candidates at a time
-        int lo = 0, hi = r.blocks;
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, x = lo + lane * step;
-            const uint32_t below = __ballot_sync(~0u, x < hi && tiles_before(p, r, x) <= inside);
-            lo += (31 - __clz(below)) * step;
-            hi = min(hi, lo + step);
+        for (int hi = r.blocks; hi - rb > 1;) {
+            const int step = (hi - rb + 31) / 32, x = rb + lane * step;
+            const uint32_t below = __ballot_sync(~0u, x < hi && units_before(p, r, x) <= inside);
+            rb += (31 - __clz(below)) * step;
+            hi = min(hi, rb + step);
         }
-        int rb = lo, tile = inside - static_cast<int>(tiles_before(p, r, rb));
+        if (rb > 0) inside -= units_before(p, r, rb);
         int first = first_block(p, r);
         int singles = 0;
         while (ok) {
             const int tok0 = rb * 2 * p.tok_tile, ntok = min(2 * p.tok_tile, r.n - tok0);
             const int vis0 = p.causal ? r.len - r.n + tok0 + 1 : r.len;
             const int more = p.causal ? 1 : 0;
-            const int tiles = tiles_in(vis0 + more * (ntok - 1));
-            const int n = min(end - u, tiles - tile), seg0 = u - tile, seg1 = seg0 + tiles;
+            const int tiles = tiles_in(vis0 + more * (ntok - 1)), wt = weight(p, ntok), units = block_units(tiles, wt);
+            const int seg0 = u - inside, upto = min(end - seg0, units);
+            // Tile j is that of the run with unit kStart + j wt of the block.
             Part x;
+            x.jb = max(inside - kStart + wt - 1, 0) / wt;
+            x.n = max(upto - kStart + wt - 1, 0) / wt - x.jb;
             x.kind = ntok > p.tok_tile ? kPair : kSingle;
-            x.jb = tile;
-            x.n = n;
             x.len = r.len;
             x.b = b;
             x.h = h;
@@ -289,26 +319,25 @@ __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const 
             x.vis0 = vis0;
             x.buffer = -1;
             x.qslot = 0;
-            x.pad = 0;
-            if (seg0 < begin || seg1 > end) {
-                const bool begins = seg0 >= begin;
-                x.buffer = 2 * static_cast<int>(blockIdx.x) + (begins ? 1 : 0);
-                if (begins) begun = Begun{(seg1 - 1) / per - static_cast<int>(blockIdx.x) + 1, x.q0, ntok, h};
-            }
-            if (x.kind == kPair) {
-                x.steps0 = max(min(tile + n, tiles_in(vis0 + more * (p.tok_tile - 1))) - tile, 0);
-                x.steps1 = n;
-                x.jmask1 = max(vis0 + more * p.tok_tile, 0) / kBN;
-            } else {
-                x.steps0 = (n + 1) / 2;
-                x.steps1 = n / 2;
-                x.jmask1 = max(vis0, 0) / kBN;
-                x.qslot = singles++ & 1;
+            const int tile0 = seg0 + kStart, tile1 = tile0 + (tiles - 1) * wt;   // units of the first and the last tile
+            if (tile0 < begin || tile1 >= end) {
+                x.buffer = 2 * static_cast<int>(blockIdx.x) + (tile0 >= begin ? 1 : 0);
+                if (x.jb == 0 && x.n > 0) begun = Begun{tile1 / per - static_cast<int>(blockIdx.x) + 1, x.q0, ntok, h};
             }
             x.jmask0 = max(vis0, 0) / kBN;
-            put(x);
-            u += n;
-            tile = 0;
+            if (x.kind == kPair) {
+                x.steps0 = max(min(x.jb + x.n, tiles_in(vis0 + more * (p.tok_tile - 1))) - x.jb, 0);
+                x.steps1 = x.n;
+                x.jmask1 = max(vis0 + more * p.tok_tile, 0) / kBN;
+            } else {
+                x.steps0 = (x.n + 1) / 2;
+                x.steps1 = x.n / 2;
+                x.jmask1 = x.jmask0;
+                if (x.n > 0) x.qslot = singles++ & 1;
+            }
+            if (x.n > 0) put(x);
+            u = seg0 + upto;
+            inside = 0;
             if (u >= end) break;
             if (++rb == r.blocks) {
                 if (++h == p.hkv) {
@@ -364,6 +393,47 @@ __device__ __forceinline__ void ring_entry(bool pair, int n, int k, int& value, 
 }
 __device__ __forceinline__ int value_entry(bool pair, int n, int tile) { return pair ? 2 * tile + 1 : min(2 + 2 * tile, 2 * n - 1); }
 
+// A query tile's place: loads of a part's tiles, and what an aborting CTA waits for.
+template <int D>
+struct Queries {
+    uint32_t phase = 0, ever = 0;   // a bit for each place: loads modulo 2, any load
+
+    static __device__ __forceinline__ bool has(const Part& x, int t) { return x.kind == kPair ? x.steps(t) > 0 : t == x.qslot; }
+
+    __device__ __forceinline__ bool free_now(const Part& x, const BarSet<D>& bars) const {
+        bool yes = true;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            if (has(x, t)) yes = yes && ptx::mbar_test_wait(bars.q_empty(t), ((phase >> t) & 1) ^ 1);
+        return __all_sync(~0u, yes);
+    }
+    __device__ __forceinline__ bool load(const CUtensorMap* tm, const Params& p, const Part& x, uint32_t sbase, const BarSet<D>& bars,
+                                         const Waiter& w) {
+        using L = Lay<D>;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (!has(x, t)) continue;
+            if (!__all_sync(~0u, w.wait(bars.q_empty(t), ((phase >> t) & 1) ^ 1, kSiteQEmpty))) return false;
+            if (!(p.debug_flags & 1) && (threadIdx.x & 31) == 0) {   // test hook: no query tiles
+                ptx::mbar_arrive_expect_tx(bars.q_full(t), p.tok_tile * p.group * (D * 2));
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    ptx::tma_load_3d(sbase + L::kQOff + t * L::kTileBytes + c * L::kBlkBytes, tm, c * 64, x.h * p.group,
+                                     x.q0 + (x.kind == kPair ? t * p.tok_tile : 0), bars.q_full(t));
+            }
+            phase ^= 1u << t;
+            ever |= 1u << t;
+        }
+        return true;
+    }
+    __device__ __forceinline__ void drain(const Params& p, const BarSet<D>& bars, const Waiter& w) const {
+        if (p.debug_flags & 1) return;
+        for (int t = 0; t < 2; ++t)
+            if ((ever >> t) & 1) w.drain(bars.q_full(t), ((phase >> t) & 1) ^ 1);
+    }
+};
+
+// A box for each page's 64 columns, each by a lane of its own.
 template <int D>
 __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p, uint8_t* smem,
                                          uint32_t sbase, const BarSet<D>& bars, const Waiter& w) {
@@ -371,15 +441,13 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
     constexpr int S = L::kStages, kBlks = D / 64;
     const int lane = threadIdx.x & 31;
     const int pages = kBN >> p.log2_page;          // of a tile
-    const int page_at = lane / kBlks, blk = lane % kBlks;   // a lane's box: a page's 64 columns
+    const int page_at = lane / kBlks, blk = lane % kBlks;
     const bool loads = page_at < pages;
     const uint32_t box = blk * L::kBlkBytes + page_at * (p.page * 128);
     int* ids = reinterpret_cast<int*>(smem + L::kIdOff) + lane;   // of the lane's page, tile modulo 4
-    const bool load_q = (p.debug_flags & 1) == 0;  // test hook
-    const uint32_t q_bytes = p.tok_tile * p.group * (D * 2);
     const int nothing = p.num_pages * p.hkv * 2;   // past the tensor: a box of zeros
     int ring = 0, n_part = 0;
-    uint32_t nq = 0, ever = 0;   // a bit for each query place: loads modulo 2, any load
+    Queries<D> queries;
     bool ok = true;
     Part x;
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
@@ -417,32 +485,20 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
             if (loads) ptx::tma_load_3d(sbase + L::kRingOff + s * L::kTileBytes + box, tmKV, blk * 64, 0, z, bars.kv_full(s));
             ++ring;
         };
-        // Keys first: their places free up before the query tiles' do.
-        const int pre = min(2, 2 * x.n);
-        for (int k = 0; k < pre && ok; ++k) load_kv(k);
-        for (int t = 0; t < 2 && ok; ++t) {
-            if (pair ? x.steps(t) == 0 : t != x.qslot) continue;
-            ok = __all_sync(~0u, w.wait(bars.q_empty(t), ((nq >> t) & 1) ^ 1, kSiteQEmpty));
-            if (!ok) break;
-            if (load_q && lane == 0) {
-                ptx::mbar_arrive_expect_tx(bars.q_full(t), q_bytes);
-#pragma unroll
-                for (int c = 0; c < kBlks; ++c)
-                    ptx::tma_load_3d(sbase + L::kQOff + t * L::kTileBytes + c * L::kBlkBytes, tmQ, c * 64, x.h * p.group,
-                                     x.q0 + (pair ? t * p.tok_tile : 0), bars.q_full(t));
-            }
-            nq ^= 1u << t;
-            ever |= 1u << t;
-        }
-        for (int k = pre; k < 2 * x.n && ok; ++k) load_kv(k);
+        // Query tiles whose places are free go before the keys, whose page ids are
+        // on their way; others behind two tiles of the ring, which finds room earlier.
+        constexpr int kPre = 2;
+        const bool early = queries.free_now(x, bars);
+        if (early) ok = queries.load(tmQ, p, x, sbase, bars, w);
+        for (int k = 0; k < kPre && ok; ++k) load_kv(k);
+        if (!early && ok) ok = queries.load(tmQ, p, x, sbase, bars, w);
+        for (int k = kPre; k < 2 * x.n && ok; ++k) load_kv(k);
         if (!ok) break;
     }
     if (!ok) {   // aborting: every copy that this CTA started lands before it exits
         const int first = ring > S ? ring - S : 0;
         for (int r = first; r < ring; ++r) w.drain(bars.kv_full(r % S), (r / S) & 1);
-        if (load_q)
-            for (int t = 0; t < 2; ++t)
-                if ((ever >> t) & 1) w.drain(bars.q_full(t), ((nq >> t) & 1) ^ 1);
+        queries.drain(p, bars, w);
     }
     __syncwarp();
 }
@@ -627,7 +683,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
                 ptx::fence_proxy_async_smem();
             }
             if (!live) {   // no row of this warp is a query's: its lanes of P and O may hold anything
-                ptx::mbar_arrive(bars.alpha_ready(t));
+                if (i > 0) ptx::mbar_arrive(bars.alpha_ready(t));
                 if (i + 1 == steps) {
                     ok = w.wait(bars.stats_free(t), (n_item & 1) ^ 1, kSiteStats);
                     if (!__all_sync(~0u, ok)) {
@@ -642,26 +698,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             ptx::tc_fence_after();
             uint32_t s[kBN];
             float m_tile;
-            if (j >= jmask) {
-                ptx::tmem_ld32_at<0>(row_addr + colS + 0, s);
-                ptx::tmem_ld32_at<32>(row_addr + colS + 32, s);
-                ptx::tmem_ld32_at<64>(row_addr + colS + 64, s);
-                ptx::tmem_ld32_at<96>(row_addr + colS + 96, s);
-                ptx::tmem_wait_ld();
-                const int lim = kend - j * kBN;
-#pragma unroll
-                for (int k = 0; k < kBN; ++k) s[k] = k < lim ? s[k] : 0xFF800000u;
-                float mx[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    float a = __uint_as_float(s[k]);
-#pragma unroll
-                    for (int e = 1; e < 15; e += 2)
-                        a = ptx::max3(a, __uint_as_float(s[k + 8 * e]), __uint_as_float(s[k + 8 * (e + 1)]));
-                    mx[k] = fmaxf(a, __uint_as_float(s[k + 120]));
-                }
-                m_tile = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), ptx::max3(mx[3], mx[4], ptx::max3(mx[5], mx[6], mx[7]))) * c;
-            } else {
+            {
                 float mq[4];
                 ptx::tmem_ld32_max_at<0>(row_addr + colS + 0, s, mq[0]);
                 ptx::tmem_ld32_max_at<32>(row_addr + colS + 32, s, mq[1]);
@@ -670,11 +707,24 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
                 ptx::tmem_wait_ld();
                 m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
             }
+            if (j >= jmask) {   // some row does not see all of these keys
+                const int lim = kend - j * kBN;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < kBN; k += 2) {
+                    s[k] = k < lim ? s[k] : 0xFF800000u;
+                    s[k + 1] = k + 1 < lim ? s[k + 1] : 0xFF800000u;
+                    mx[k / 2 % 4] = ptx::max3(mx[k / 2 % 4], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                }
+                m_tile = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+            }
             const float m_new = fmaxf(m, m_tile);
-            const float alpha = (i == 0 || m_new == m) ? 1.0f : ptx::ex2_approx(m - m_new);
-            alpha_buf[row] = alpha;
-            ptx::mbar_arrive(bars.alpha_ready(t));
-            l *= alpha;
+            if (i > 0) {
+                const float alpha = m_new == m ? 1.0f : ptx::ex2_approx(m - m_new);
+                alpha_buf[row] = alpha;
+                ptx::mbar_arrive(bars.alpha_ready(t));
+                l *= alpha;
+            }
             m = m_new;
             // A row with no key so far keeps m = -inf; its weights are exp2(-inf - 0) = 0.
             const float m_use = m == -INFINITY ? 0.0f : m;
@@ -719,21 +769,22 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
 
 // The warp's 4 KB staging slice holds 128 bytes of each of its 32 rows, as in
 // store_o_rows: each lane puts 16-byte pieces of its own row, then the warp
-// stores whole lines.
+// stores whole lines, of four rows at a time.
 __device__ __forceinline__ void put_piece(uint32_t wslice, int lane, int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     ptx::st_shared_v4(wslice + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(c) ^ (lane & 7u)) << 4), x, y, z, w);
 }
-// to(r): where row r of the 32 goes, NULL for nowhere.
-template <typename To>
-__device__ __forceinline__ void store_lines(uint32_t wslice, int lane, To to) {
+// to: where column 0 of the 128 bytes of line 0 goes; line[r]: the line of row r
+// of the 32, in shared memory; rows: how many of them there are.
+template <int kLineBytes>
+__device__ __forceinline__ void store_lines(uint32_t wslice, int lane, char* to, const int* line, int rows) {
     __syncwarp();
     const int r0 = lane >> 3;
     const uint32_t rd = wslice + static_cast<uint32_t>(r0) * 128u + (static_cast<uint32_t>((lane & 7) ^ r0) << 4);
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
+        if (4 * i >= rows) break;
         const uint4 x = ptx::ld_shared_v4((rd ^ ((i & 1) << 6)) + static_cast<uint32_t>(i) * 512u);
-        uint4* at = to(4 * i + r0);
-        if (at) at[lane & 7] = x;
+        if (4 * i + r0 < rows) *reinterpret_cast<uint4*>(to + static_cast<long long>(line[4 * i + r0]) * kLineBytes + (lane & 7) * 16) = x;
     }
     __syncwarp();   // before the slice is written again
 }
@@ -748,16 +799,28 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
     const uint32_t row_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const float* rowbuf = reinterpret_cast<const float*>(smem + L::kRowOff);  // alpha | m | l
     const uint32_t wslice = sbase + L::kStageOff + static_cast<uint32_t>(q) * (32u * 128u);
-    const uint32_t inv_group = (65536u + p.group - 1) / p.group;
+    int* lines = reinterpret_cast<int*>(smem + L::kLineOff);
+    {
+        const int tk = by_group(row, (65536u + p.group - 1) / p.group);
+        lines[row] = tk * p.hq + (row - tk * p.group);
+        lines[kBM + row] = row;
+    }
+    __syncwarp();   // a warp reads those of its own rows
+    lines += 32 * q;
+    const int* ident = lines + kBM;
 
     uint32_t n_s = 0, n_items = 0;   // a bit for each stream: steps, parts, modulo 2
     int n_part = 0;
     bool ok = true;
     Part x;
+    // At a part's first step O is overwritten, not rescaled: what the PV product
+    // waits for is that the O of the stream's last part has been read. That
+    // arrival is made here and, from then on, by the epilogue.
+    for (int t = 0; t < 2; ++t) ptx::mbar_arrive(bars.p_full(t));
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
         const bool pair = x.kind == kPair;
         const int most = max(x.steps0, x.steps1);
-        for (int i = 0; i < most && ok; ++i) {
+        for (int i = 1; i < most && ok; ++i) {
             for (int t = 0; t < 2; ++t) {
                 if (i >= x.steps(t)) continue;
                 ok = w.wait(bars.alpha_ready(t), (n_s >> t) & 1, kSiteAlpha);
@@ -768,7 +831,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 n_s ^= 1u << t;
                 const bool live = 32 * q < stream_tokens(p, x, t) * p.group;
                 const float alpha = live ? rowbuf[t * kBM + row] : 1.0f;
-                if (i > 0 && __any_sync(~0u, alpha != 1.0f)) {
+                if (__any_sync(~0u, alpha != 1.0f)) {
                     ptx::tc_fence_after();
                     const uint32_t colO = Layout<D>::col_o(t);
                     const uint64_t a2 = ptx::f2_pack(alpha, alpha);
@@ -793,8 +856,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 ptx::mbar_arrive(bars.p_full(t));
             }
         }
-        // Epilogue. The next part's first PV overwrites O only behind this
-        // warpgroup's next p_full arrival, which comes after these loads.
+        // Epilogue.
         for (int tile = 0; tile < (pair ? 2 : 1) && ok; ++tile) {
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // of the streams that have this tile's rows
             bool has[2];
@@ -817,7 +879,20 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
             if (!ok) break;
             ptx::tc_fence_after();
             const int rows = stream_tokens(p, x, tile) * p.group;
-            if (32 * q >= rows) continue;
+            // The next part's first PV products may overwrite the streams' O.
+            auto release = [&] {
+                ptx::tc_fence_before();
+                if (pair) {
+                    if (has[0]) ptx::mbar_arrive(bars.p_full(tile));
+                } else {
+                    ptx::mbar_arrive(bars.p_full(0));
+                    if (has[1]) ptx::mbar_arrive(bars.p_full(1));
+                }
+            };
+            if (32 * q >= rows) {
+                release();
+                continue;
+            }
             float mm = m[0], ll = l[0], f[2] = {1.0f, 0.0f};
             if (has[1]) {
                 mm = fmaxf(m[0], m[1]);
@@ -833,73 +908,65 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 f[0] *= inv;
                 f[1] *= inv;
             }
-            // Columns c .. c + 16 of the row: of the tile's stream, or of both.
-            auto load16 = [&](int c, float (&v)[16]) {
-                uint32_t a[16];
-                tmem_ld16(row_addr + col0 + c, a);
+            // 32 columns of the row from c on: of the tile's stream, or of both.
+            auto load32 = [&](int c, uint32_t (&v)[32]) {
+                ptx::tmem_ld32_at<0>(row_addr + col0 + c, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(a[k]) * f[0];
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f[0]);
                 if (has[1]) {
-                    tmem_ld16(row_addr + Layout<D>::col_o(1) + c, a);
-                    ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = fmaf(__uint_as_float(a[k]), f[1], v[k]);
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t u[8];
+                        kv4::tc::tmem_ld8(row_addr + Layout<D>::col_o(1) + c + e, u);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[e + k] = __float_as_uint(fmaf(__uint_as_float(u[k]), f[1], __uint_as_float(v[e + k])));
+                    }
                 }
                 if (ll == 0.0f) {   // no key, whatever the values hold
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+                    for (int k = 0; k < 32; ++k) v[k] = 0;
                 }
             };
-            const long long tok0 = x.q0 + (pair ? tile * p.tok_tile : 0);
             if (x.buffer < 0) {
-                const long long line0 = tok0 * p.hq + x.h * p.group;
+                const long long line0 = static_cast<long long>(x.q0 + (pair ? tile * p.tok_tile : 0)) * p.hq + x.h * p.group;
+                char* to = static_cast<char*>(p.o) + line0 * (2 * D);
 #pragma unroll 1
-                for (int h = 0; h < D; h += 64) {
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        float v[16];
-                        load16(h + 16 * k, v);
+                for (int h = 0; h < D; h += 64, to += 128) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            put_piece(wslice, lane, 2 * k + e, ptx::pack2<kBf16>(v[8 * e], v[8 * e + 1]),
-                                      ptx::pack2<kBf16>(v[8 * e + 2], v[8 * e + 3]), ptx::pack2<kBf16>(v[8 * e + 4], v[8 * e + 5]),
-                                      ptx::pack2<kBf16>(v[8 * e + 6], v[8 * e + 7]));
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[32];
+                        load32(h + 32 * k, v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+                                w[s] = ptx::pack2<kBf16>(__uint_as_float(v[8 * e + 2 * s]), __uint_as_float(v[8 * e + 2 * s + 1]));
+                            put_piece(wslice, lane, 4 * k + e, w[0], w[1], w[2], w[3]);
+                        }
                     }
-                    store_lines(wslice, lane, [&](int r) -> uint4* {
-                        r += 32 * q;
-                        const int tk = by_group(r, inv_group);
-                        const long long line = line0 + static_cast<long long>(tk) * p.hq + (r - tk * p.group);
-                        return r < rows ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + line * D + h) : nullptr;
-                    });
+                    if (h + 64 >= D) release();
+                    store_lines<2 * D>(wslice, lane, to, lines, rows - 32 * q);
                 }
-                if (row < rows) {
-                    const int tk = by_group(row, inv_group);
-                    p.lse[line0 + static_cast<long long>(tk) * p.hq + (row - tk * p.group)] =
-                        ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
-                }
+                if (row < rows)
+                    p.lse[line0 + lines[lane]] = ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
             } else {
                 const long long line0 = static_cast<long long>(x.buffer) * p.part_rows + tile * kBM;
+                char* to = reinterpret_cast<char*>(p.part_o + line0 * D);
 #pragma unroll 1
-                for (int h = 0; h < D; h += 32) {
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {
-                        float v[16];
-                        load16(h + 16 * k, v);
+                for (int h = 0; h < D; h += 32, to += 128) {
+                    uint32_t v[32];
+                    load32(h, v);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            put_piece(wslice, lane, 4 * k + e, __float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
-                                      __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-                    }
-                    store_lines(wslice, lane, [&](int r) -> uint4* {
-                        r += 32 * q;
-                        return r < rows ? reinterpret_cast<uint4*>(p.part_o + (line0 + r) * D + h) : nullptr;
-                    });
+                    for (int e = 0; e < 8; ++e) put_piece(wslice, lane, e, v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    if (h + 32 >= D) release();
+                    store_lines<4 * D>(wslice, lane, to, ident, rows - 32 * q);
                 }
                 if (row < rows) *reinterpret_cast<float2*>(p.part_ml + 2 * (line0 + row)) = make_float2(mm, ll);
             }
         }
-        ptx::tc_fence_before();
         if (!ok) break;
     }
 }
