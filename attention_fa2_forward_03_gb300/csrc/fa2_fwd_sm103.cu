@@ -1235,8 +1235,9 @@ fa2_status fa2_kv16_append(const void* q, const void* k, const void* v, const in
 int64_t fa2_fwd_kv16_workspace(int T, int B, int H_q, int H_kv, int d, int max_pages, int page_size) {
     if (kv16_check_sizes(T, B, H_q, H_kv, d, max_pages, page_size) != FA2_OK) return -1;
     const int64_t ctas = kv16_ctas(T, B, H_q, H_kv, static_cast<long long>(max_pages) * page_size, fa2::kv16::kMaxCtas);
-    return ctas * (2LL * kv16_part_rows(T, H_q / H_kv) * (d + 2) * static_cast<int64_t>(sizeof(float)) +
-                   static_cast<int64_t>(sizeof(fa2::kv16::Begun)));
+    // 16 more: the partial results begin at a multiple of 32 bytes
+    return 16 + ctas * (2LL * kv16_part_rows(T, H_q / H_kv) * (d + 2) * static_cast<int64_t>(sizeof(float)) +
+                        static_cast<int64_t>(sizeof(fa2::kv16::Begun)));
 }
 
 fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
@@ -1287,7 +1288,7 @@ fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_t
     p.num_pages = num_pages;
     p.causal = causal;
     p.ctas = kv16_ctas(T, B, H_q, H_kv, p.max_tokens, std::min(sm_count(dev), fa2::kv16::kMaxCtas));
-    p.part_o = static_cast<float*>(workspace);
+    p.part_o = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 16) & ~static_cast<uintptr_t>(31));
     p.part_ml = p.part_o + 2LL * p.ctas * p.part_rows * d;
     p.begun = reinterpret_cast<fa2::kv16::Begun*>(p.part_ml + 4LL * p.ctas * p.part_rows);
     p.debug_flags = g_debug_flags.load();

@@ -46,6 +46,11 @@ constexpr int kMaxCtas = 160;
 constexpr int kSchedWarp = 14;
 // Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
 // for one, and every row block kStart more for its start and its end.
+#ifndef R16S
+#define R16S 168
+#define R16C 120
+#define R16O 56
+#endif
 #ifndef K16P
 #define K16P 3
 #define K16S 2
@@ -95,7 +100,7 @@ struct __align__(16) Part {
     int buffer;                   // of partial results, or -1: the whole block
     int qslot;                    // single: the place of its query tile
     int jmask0, jmask1;           // first key tile that some row of the stream does not see whole
-    int pad;
+    int ring;                     // entry of the ring that its first tile has, modulo 16
 
     __device__ __forceinline__ int steps(int t) const { return t ? steps1 : steps0; }
     __device__ __forceinline__ int jmask(int t) const { return t ? jmask1 : jmask0; }
@@ -110,16 +115,16 @@ struct Lay {
     static constexpr int kStages = Layout<D>::kStages;
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = 2 * kTileBytes;
-    static constexpr int kStageOff = kRingOff + kStages * kTileBytes;   // the epilogue's staging
-    static constexpr int kBarOff = kStageOff + kBM * 128;
+    static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
     // q_full[2] q_empty[2] kv_full[S] kv_empty[S] s_full[2] alpha[2] stats[2] p_full[2] o_full[2] mma_done
-    // stats_free[2] part_full[4] part_empty[4]
-    static constexpr int kNumBars = 2 * kStages + 17 + 2 * kParts;
+    // stats_free[2] part_full[4] part_empty[4] p_rest[2]
+    static constexpr int kNumBars = 2 * kStages + 19 + 2 * kParts;
     static constexpr int kRowOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // alpha[2][128], m[2][128], l[2][128]
     static constexpr int kPartOff = kRowOff + 6 * kBM * 4;
     static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
-    static constexpr int kLineOff = kIdOff + 4 * 32 * 4;   // lines of a tile's rows in o, and 0 .. 127: those in a buffer
-    static constexpr int kMiscOff = kLineOff + 2 * kBM * 4;
+    static constexpr int kLineOff = kIdOff + 4 * 32 * 4;   // lines of a tile's rows in o
+    static constexpr int kFirstOff = kLineOff + kBM * 4;   // page ids of the first two tiles of a part [kParts][16]
+    static constexpr int kMiscOff = kFirstOff + kParts * 16 * 4;
     static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -129,7 +134,35 @@ struct BarSet : Bars<D> {
     static constexpr int S = Layout<D>::kStages;
     __device__ uint32_t part_full(int s) const { return this->base + 8 * (17 + 2 * S + s); }
     __device__ uint32_t part_empty(int s) const { return this->base + 8 * (17 + 2 * S + kParts + s); }
+    // P in two halves: p_full is for the weights of a tile's first 64 keys (and a rescaled O), p_rest for the others'.
+    __device__ uint32_t p_rest(int t) const { return this->base + 8 * (17 + 2 * S + 2 * kParts + t); }
 };
+
+// One arrival for the warp, behind what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
+
+// O (+)= P V over one half of a tile's keys, in four steps of 16: P from TMEM
+// (8 columns a step), V MN-major (2048 bytes a step).
+__device__ __forceinline__ void mma_half(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 blo, bhi, t0, t1;\n\t.reg .b64 b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\t"
+        "setp.eq.b32 pt, %4, %4;\n\t"
+        "mov.b64 {blo, bhi}, %2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+        "add.u32 t0, %1, 8;\n\tadd.u32 t1, blo, 128;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+        "add.u32 t0, %1, 16;\n\tadd.u32 t1, blo, 256;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+        "add.u32 t0, %1, 24;\n\tadd.u32 t1, blo, 384;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
+        "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
 
 // ---------------------------------------------------------------- the line of units
 
@@ -207,99 +240,111 @@ __device__ __forceinline__ int units_before(const Params& p, const Request& r, i
 template <int D>
 __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const BarSet<D>& bars, const Waiter& w) {
     const int lane = threadIdx.x & 31;
-    const uint32_t ring = ptx::smem_addr(smem + Lay<D>::kPartOff);
+    const uint32_t slots = ptx::smem_addr(smem + Lay<D>::kPartOff);
     int n_part = 0;
     bool ok = true;
+    int* first_ids = reinterpret_cast<int*>(smem + Lay<D>::kFirstOff);
+    const int pages = kBN >> p.log2_page;   // of a tile
     auto put = [&](const Part& x) {
         const int s = n_part % kParts;
+        // The page ids that its loads begin with, on their way before the place is free.
+        const int entry = x.jb * pages + lane;
+        int id = -1;
+        if (lane < pages * min(x.n, 2) && entry < (x.len + p.page - 1) >> p.log2_page)
+            id = p.block_table[static_cast<long long>(x.b) * p.max_pages + entry];
         ok = __all_sync(~0u, w.wait(bars.part_empty(s), ((n_part / kParts) & 1) ^ 1, kSitePart));
         if (!ok) return;
+        if (lane < 16) first_ids[16 * s + lane] = id;
+        __syncwarp();
         if (lane == 0) {
-            const uint32_t to = ring + s * static_cast<int>(sizeof(Part));
+            const uint32_t to = slots + s * static_cast<int>(sizeof(Part));
             ptx::st_shared_v4(to, x.kind, x.steps0, x.steps1, x.jb);
             ptx::st_shared_v4(to + 16, x.n, x.len, x.b, x.h);
             ptx::st_shared_v4(to + 32, x.q0, x.ntok, x.vis0, x.buffer);
-            ptx::st_shared_v4(to + 48, x.qslot, x.jmask0, x.jmask1, 0);
+            ptx::st_shared_v4(to + 48, x.qslot, x.jmask0, x.jmask1, x.ring);
             ptx::mbar_arrive(bars.part_full(s));
         }
         __syncwarp();
         ++n_part;
     };
 
-    // Units in front of each lane's share of the requests.
-    const int chunk = (p.B + 31) / 32, b0 = min(lane * chunk, p.B), b1 = min(b0 + chunk, p.B);
-    int mine = 0, each = 0;   // each: units of a head of the last request looked at, r
-    long long rows = 0;
+    // The request at which the run begins: units in front of each lane's share
+    // of the requests; then the same within the share that has the run's start.
+    int total = 0, per = kMinRun, u = 0, end = 0;
+    int at = 0, each = 0, b = 0;   // units in front of the request, of one of its heads, its number
     Request r{};
-    for (int b = b0; b < b1; b += 4) {   // four requests' numbers are read at once
-        int s[4], n[4], len[4];
+    for (int lo = 0, hi = p.B, chunk = 0; chunk != 1;) {
+        chunk = (hi - lo + 31) / 32;
+        const int b0 = min(lo + lane * chunk, hi), b1 = min(b0 + chunk, hi);
+        int mine = 0;
+        long long rows = 0;
+        for (int i = b0; i < b1; i += 4) {   // four requests' numbers are read at once
+            int s[4], n[4], len[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[e] = n[e] = len[e] = 0;
-            if (b + e < b1) {
-                s[e] = p.q_starts[b + e];
-                n[e] = p.q_lens[b + e];
-                len[e] = p.seq_lens[b + e];
+            for (int e = 0; e < 4; ++e) {
+                s[e] = n[e] = len[e] = 0;
+                if (i + e < b1) {
+                    s[e] = p.q_starts[i + e];
+                    n[e] = p.q_lens[i + e];
+                    len[e] = p.seq_lens[i + e];
+                }
             }
-        }
 #pragma unroll 1
-        for (int e = 0; e < min(4, b1 - b); ++e) {
-            r = request(p, s[0], n[0], len[0]);
-            each = units_before(p, r, r.blocks);
-            mine += each * p.hkv;
-            rows += r.n;
+            for (int e = 0; e < min(4, b1 - i); ++e) {
+                r = request(p, s[0], n[0], len[0]);
+                each = units_before(p, r, r.blocks);
+                mine += each * p.hkv;
+                rows += r.n;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                s[k] = s[k + 1];
-                n[k] = n[k + 1];
-                len[k] = len[k + 1];
+                for (int k = 0; k < 3; ++k) {
+                    s[k] = s[k + 1];
+                    n[k] = n[k + 1];
+                    len[k] = len[k + 1];
+                }
             }
         }
-    }
-    int to = mine;
+        int to = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(~0u, to, o);
-        if (lane >= o) to += y;
-        rows += __shfl_xor_sync(~0u, rows, o);
-    }
-    int total = __shfl_sync(~0u, to, 31);   // below 2^30 if no row has two requests
-    if (rows > p.T) {
-        if (blockIdx.x == 0 && lane == 0) report(kSiteRows);
-        total = 0;
-    }
-    const int per = max((total + p.ctas - 1) / p.ctas, kMinRun);
-    int u = static_cast<int>(blockIdx.x) * per;
-    const int begin = u, end = min(total, u + per);
-    Begun begun{0, 0, 0, 0};
-    if (u < end) {
-        int at = to - mine, b = b0;
-        const bool here = u >= at && u < to;
-        if (here && chunk > 1)
-            while (true) {
-                r = request(p, b);
-                each = units_before(p, r, r.blocks);
-                if (u < at + each * p.hkv) break;
-                at += each * p.hkv;
-                ++b;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, to, o);
+            if (lane >= o) to += y;
+            rows += __shfl_xor_sync(~0u, rows, o);
+        }
+        if (total == 0) {   // all requests
+            total = __shfl_sync(~0u, to, 31);   // below 2^30 if no row has two requests
+            if (rows > p.T) {
+                if (blockIdx.x == 0 && lane == 0) report(kSiteRows);
+                total = 0;
             }
-        const int from = __ffs(__ballot_sync(~0u, here)) - 1;
-        b = __shfl_sync(~0u, b, from);
+            per = max((total + p.ctas - 1) / p.ctas, kMinRun);
+            u = static_cast<int>(blockIdx.x) * per;
+            end = min(total, u + per);
+            if (u >= end) break;
+        }
+        const int from = __ffs(__ballot_sync(~0u, u >= at + to - mine && u < at + to)) - 1;
+        at += __shfl_sync(~0u, to - mine, from);
+        lo = b = __shfl_sync(~0u, b0, from);
+        hi = min(lo + chunk, hi);
         each = __shfl_sync(~0u, each, from);
         r = Request{__shfl_sync(~0u, r.start, from), __shfl_sync(~0u, r.n, from), __shfl_sync(~0u, r.len, from),
                     __shfl_sync(~0u, r.blocks, from)};
-        const int rem = u - __shfl_sync(~0u, at, from);
-        int h = rem / each, inside = rem - h * each, rb = 0;
+    }
+    const int begin = u;
+    Begun begun{0, 0, 0, 0};
+    if (u < end) {
+        int h = (u - at) / each, inside = u - at - h * each, rb = 0;
         // the row block: 32 candidates at a time
+        int before = 0;
         for (int hi = r.blocks; hi - rb > 1;) {
-            const int step = (hi - rb + 31) / 32, x = rb + lane * step;
-            const uint32_t below = __ballot_sync(~0u, x < hi && units_before(p, r, x) <= inside);
-            rb += (31 - __clz(below)) * step;
+            const int step = (hi - rb + 31) / 32, x = rb + lane * step, units = units_before(p, r, x);
+            const int top = 31 - __clz(__ballot_sync(~0u, x < hi && units <= inside));
+            before = __shfl_sync(~0u, units, top);
+            rb += top * step;
             hi = min(hi, rb + step);
         }
-        if (rb > 0) inside -= units_before(p, r, rb);
+        inside -= before;
         int first = first_block(p, r);
-        int singles = 0;
+        int singles = 0, ring = 0;
         while (ok) {
             const int tok0 = rb * 2 * p.tok_tile, ntok = min(2 * p.tok_tile, r.n - tok0);
             const int vis0 = p.causal ? r.len - r.n + tok0 + 1 : r.len;
@@ -335,6 +380,8 @@ __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const 
                 x.jmask1 = x.jmask0;
                 if (x.n > 0) x.qslot = singles++ & 1;
             }
+            x.ring = ring & 15;
+            ring += 2 * x.n;
             if (x.n > 0) put(x);
             u = seg0 + upto;
             inside = 0;
@@ -357,8 +404,13 @@ __device__ __forceinline__ void scheduler(const Params& p, uint8_t* smem, const 
 }
 
 // The next part; false behind the last one or if the CTA is aborting (`ok`).
-template <int D>
-__device__ __forceinline__ bool next_part(uint8_t* smem, const BarSet<D>& bars, const Waiter& w, int& n_part, Part& x, bool& ok) {
+// `before`: what else is read of its place.
+struct Nothing {
+    __device__ __forceinline__ void operator()(int) const {}
+};
+template <int D, typename Before = Nothing>
+__device__ __forceinline__ bool next_part(uint8_t* smem, const BarSet<D>& bars, const Waiter& w, int& n_part, Part& x, bool& ok,
+                                          Before before = Before{}) {
     const int s = n_part % kParts;
     ok = __all_sync(~0u, w.wait(bars.part_full(s), (n_part / kParts) & 1, kSitePart));
     if (!ok) return false;
@@ -366,6 +418,7 @@ __device__ __forceinline__ bool next_part(uint8_t* smem, const BarSet<D>& bars, 
     uint4* to = reinterpret_cast<uint4*>(&x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) to[i] = ptx::ld_shared_v4(at + 16 * i);
+    before(s);
     __syncwarp();
     if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bars.part_empty(s));
     ++n_part;
@@ -410,7 +463,7 @@ struct Queries {
     __device__ __forceinline__ bool load(const CUtensorMap* tm, const Params& p, const Part& x, uint32_t sbase, const BarSet<D>& bars,
                                          const Waiter& w) {
         using L = Lay<D>;
-#pragma unroll
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             if (!has(x, t)) continue;
             if (!__all_sync(~0u, w.wait(bars.q_empty(t), ((phase >> t) & 1) ^ 1, kSiteQEmpty))) return false;
@@ -448,9 +501,15 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
     const int nothing = p.num_pages * p.hkv * 2;   // past the tensor: a box of zeros
     int ring = 0, n_part = 0;
     Queries<D> queries;
+    const int* first_ids = reinterpret_cast<const int*>(smem + L::kFirstOff);
+    int ahead[2];   // page ids of the next two tiles of keys
     bool ok = true;
     Part x;
-    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+    while (next_part<D>(smem, bars, w, n_part, x, ok, [&](int s) {
+        if (loads)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) ahead[e] = *const_cast<const volatile int*>(first_ids + 16 * s + e * pages + page_at);
+    })) {
         const bool pair = x.kind == kPair;
         const int* table = p.block_table + static_cast<long long>(x.b) * p.max_pages;
         const int used = (x.len + p.page - 1) >> p.log2_page;   // pages of the request
@@ -459,7 +518,6 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
             const int e = entry0 + tile * pages;
             return loads && tile < x.n && e < used ? __ldg(table + e) : -1;
         };
-        int ahead[2] = {look(0), look(1)};   // page ids of the next two tiles of keys
         auto load_kv = [&](int k) {
             int value, tile;
             ring_entry(pair, x.n, k, value, tile);
@@ -486,13 +544,13 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
             ++ring;
         };
         // Query tiles whose places are free go before the keys, whose page ids are
-        // on their way; others behind two tiles of the ring, which finds room earlier.
-        constexpr int kPre = 2;
-        const bool early = queries.free_now(x, bars);
-        if (early) ok = queries.load(tmQ, p, x, sbase, bars, w);
-        for (int k = 0; k < kPre && ok; ++k) load_kv(k);
-        if (!early && ok) ok = queries.load(tmQ, p, x, sbase, bars, w);
-        for (int k = kPre; k < 2 * x.n && ok; ++k) load_kv(k);
+        // on their way; others behind the first tile, for which there is room earlier.
+        const int when = queries.free_now(x, bars) ? 0 : 1;
+#pragma unroll 1
+        for (int k = 0; k < 2 * x.n && ok; ++k) {
+            if (k == when && !(ok = queries.load(tmQ, p, x, sbase, bars, w))) break;
+            load_kv(k);
+        }
         if (!ok) break;
     }
     if (!ok) {   // aborting: every copy that this CTA started lands before it exits
@@ -520,11 +578,17 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
         qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
         ptx::tc_commit_elect(bars.s_full(t));
     };
-    auto issue_pv = [&](int t, int v_ring, bool acc) {
-        const uint64_t vd = ptx::desc_sw128(stage_addr(v_ring), L::kBlkBytes, 1024);
-        pv_kloop(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
-    };
     auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
+    // P V of a tile whose p_full has completed: its halves as their weights are there.
+    auto issue_pv = [&](int t, int v_ring, bool acc, uint32_t parity) {
+        const uint64_t vd = ptx::desc_sw128(stage_addr(v_ring), L::kBlkBytes, 1024);
+        ptx::tc_fence_after();
+        mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
+        if (!wait_u(bars.p_rest(t), parity, kSitePFull)) return false;
+        ptx::tc_fence_after();
+        mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t) + 32, vd + 512, kIdO, 1u);
+        return true;
+    };
     auto wait_ring = [&](int r) { return wait_u(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull); };
     auto release = [&](int r) { ptx::tc_commit_elect(bars.kv_empty(r % S)); };
 
@@ -533,83 +597,52 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
     bool ok = true;
     Part x;
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
-        if (x.kind == kPair) {
-            // As the forward kernel's general mode: at key tile j the streams with j < steps[t] take part.
-            for (int t = 0; t < 2 && ok; ++t)
-                if (x.steps(t) > 0) ok = wait_u(bars.q_full(t), (nq >> t) & 1, kSiteQFull);
-            if (!ok || !(ok = wait_ring(ring))) break;
+        // Pair: both streams work on every tile of keys that they have (stream 1
+        // on all). Single: on every other one. So QK of tile j + ahead follows PV of
+        // tile j.
+        const bool pair = x.kind == kPair;
+        const int ahead = pair ? 1 : 2;
+        auto place = [&](int t) { return pair ? t : x.qslot; };   // of the stream's query tile
+        if (pair && x.steps0 > 0) ok = wait_u(bars.q_full(0), nq & 1, kSiteQFull);
+        if (ok) ok = wait_u(bars.q_full(place(1)), (nq >> place(1)) & 1, kSiteQFull);
+        for (int e = 0; ok && e < min(ahead, x.n); ++e) {
+            if (!(ok = wait_ring(ring))) break;
             ptx::tc_fence_after();
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-                if (x.steps(t) == 0) continue;
-                issue_qk(t, t, ring);
-                if (x.steps(t) == 1) ptx::tc_commit_elect(bars.q_empty(t));
+                if (pair ? x.steps(t) == 0 : t != e) continue;
+                issue_qk(t, place(t), ring);
+                if (pair ? x.steps(t) == 1 : e + 1 == x.n) ptx::tc_commit_elect(bars.q_empty(place(t)));
             }
-            release(ring);
-            int k_ring = ring++;
-            for (int j = 0; j < x.n; ++j) {
-                const bool more = j + 1 < x.n;
-                const int v_ring = ring++;
-                if (more) k_ring = ring++;
-                const int t0 = j < x.steps0 ? 0 : 1;
-                const int kr = more ? k_ring : v_ring;
-                const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(kr % S), bars.p_full(t0)};
-                const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((kr / S) & 1),
-                                        (np >> t0) & 1};
-                if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
-                for (int t = 0; t < 2; ++t) {   // stream 1 takes part in every tile
-                    if (t < t0) continue;
-                    if (t != t0 && !(ok = wait_u(bars.p_full(t), (np >> t) & 1, kSitePFull))) break;
-                    np ^= 1u << t;
-                    ptx::tc_fence_after();
-                    issue_pv(t, v_ring, j > 0);
-                    if (t == 1) release(v_ring);
-                    if (j + 1 < x.steps(t)) {
-                        issue_qk(t, t, k_ring);
-                        if (j + 2 == x.steps(t)) ptx::tc_commit_elect(bars.q_empty(t));
-                        if (t == 1) release(k_ring);
-                    } else {
-                        ptx::tc_commit_elect(bars.o_full(t));
-                    }
-                }
-                if (!ok) break;
-            }
-            if (!ok) break;
-            for (int t = 0; t < 2; ++t)
-                if (x.steps(t) > 0) nq ^= 1u << t;
-        } else {
-            const int n = x.n;
-            if (!(ok = wait_u(bars.q_full(x.qslot), (nq >> x.qslot) & 1, kSiteQFull))) break;
-            for (int t = 0; t < min(n, 2) && ok; ++t) {
-                if (!(ok = wait_ring(ring))) break;
-                ptx::tc_fence_after();
-                issue_qk(t, x.qslot, ring);
-                if (t + 1 == n) ptx::tc_commit_elect(bars.q_empty(x.qslot));
-                release(ring++);
-            }
-            if (!ok) break;
-            for (int j = 0; j < n; ++j) {
-                const int t = j & 1;
-                const bool more = j + 2 < n;   // the stream's next keys
-                const int v_ring = ring++, k_ring = more ? ring++ : v_ring;
-                const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(k_ring % S), bars.p_full(t)};
-                const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((k_ring / S) & 1),
-                                        (np >> t) & 1};
-                if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
+            release(ring++);
+        }
+        for (int j = 0; ok && j < x.n; ++j) {
+            const bool more = j + ahead < x.n;
+            const int v_ring = ring++, k_ring = more ? ring++ : v_ring;
+            const int t0 = pair ? (j < x.steps0 ? 0 : 1) : j & 1, t1 = pair ? 1 : t0;   // streams that take part
+            // V_j, the next keys and the first weights of the first stream are waited for together.
+            const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(k_ring % S), bars.p_full(t0)};
+            const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((k_ring / S) & 1), (np >> t0) & 1};
+            if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
+#pragma unroll 1
+            for (int t = t0; t <= t1; ++t) {
+                if (t != t0 && !(ok = wait_u(bars.p_full(t), (np >> t) & 1, kSitePFull))) break;
+                if (!(ok = issue_pv(t, v_ring, j >= ahead, (np >> t) & 1))) break;
                 np ^= 1u << t;
-                ptx::tc_fence_after();
-                issue_pv(t, v_ring, j > 1);
-                release(v_ring);
-                if (more) {
-                    issue_qk(t, x.qslot, k_ring);
-                    release(k_ring);
-                    if (j + 3 == n) ptx::tc_commit_elect(bars.q_empty(x.qslot));
+                if (t == t1) release(v_ring);
+                const int mine = pair ? x.steps(t) : x.n;
+                if (j + ahead < mine) {
+                    issue_qk(t, place(t), k_ring);
+                    if (j + ahead + 1 == mine) ptx::tc_commit_elect(bars.q_empty(place(t)));
+                    if (t == t1) release(k_ring);
                 } else {
                     ptx::tc_commit_elect(bars.o_full(t));
                 }
             }
-            if (!ok) break;
-            nq ^= 1u << x.qslot;
         }
+        if (!ok) break;
+        if (pair && x.steps0 > 0) nq ^= 1u;
+        nq ^= 1u << place(1);
     }
     // Every MMA issued above finishes before the CTA frees its TMEM.
     ptx::tc_commit_elect(bars.mma_done());
@@ -643,86 +676,102 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
     const uint64_t c2 = ptx::f2_pack(c, c);
     const int tok = by_group(row, (65536u + p.group - 1) / p.group);   // the row's token in the tile
 
-    int n_s = 0, n_item = 0, n_part = 0, ring = 0;
+    uint32_t n_s = 0, n_item = 0;   // parities: steps, parts of the stream
+    int n_part = 0;
     bool ok = true;
     Part x;
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
         const bool pair = x.kind == kPair;
-        const int steps = x.steps(t), jmask = x.jmask(t);
-        const int ring0 = ring;
-        ring += 2 * x.n;
+        const int steps = x.steps(t);
         if (steps == 0) continue;
-        const int rows = stream_tokens(p, x, t) * p.group;
-        const bool live = (row & ~31) < rows;   // of the warp: some row is a query's
-        const int kend = min(x.len, x.vis0 + (p.causal ? tok + (pair ? t * p.tok_tile : 0) : 0));
+        // The stream's step i is the part's tile i (pair) or 2 i + t (single).
+        const int every = pair ? 1 : 2, from = x.jb + (pair ? 0 : t);
+        const bool live = (row & ~31) < stream_tokens(p, x, t) * p.group;   // of the warp: some row is a query's
+        // Keys of the step's tile that the row sees, and the first step at which that may be fewer than all.
+        int lim = min(x.len, x.vis0 + (p.causal ? tok + (pair ? t * p.tok_tile : 0) : 0)) - from * kBN;
+        const int mask_from = (x.jmask(t) - from + every - 1) / every;
+        // The step in whose tile the request ends, if it has it; how many of the tile's keys there are, and its V.
+        int tail_step = -1, tail = 0;
+        {
+            const int last = x.len / kBN - from;
+            if (x.len % kBN != 0 && last >= 0 && last % every == 0) {
+                tail_step = last / every;
+                tail = (x.ring + value_entry(pair, x.n, last + from - x.jb)) * 128 + x.len % kBN;
+            }
+        }
         float m = -INFINITY;  // running row max of the scaled scores, log2 units
         float l = 0.0f;       // running sum of exp2(s*c - m)
-        for (int i = 0; i < steps; ++i, ++n_s) {
-            const int jj = pair ? i : 2 * i + t, j = x.jb + jj;
-            ok = w.wait(bars.s_full(t), n_s & 1, kSiteSFull);
+        for (int i = 0; i < steps; ++i, n_s ^= 1, lim -= every * kBN) {
+            ok = w.wait(bars.s_full(t), n_s, kSiteSFull);
             if (!__all_sync(~0u, ok)) {
                 ok = false;
                 break;
             }
-            const int valid = x.len - j * kBN;
-            if (valid < kBN) {
-                // The request ends inside this tile. What lies behind it in its last page has weight 0, but may be
-                // anything, NaN too: those rows of V become zeros. (Two streams that share the tile write the same.)
-                const int r = ring0 + value_entry(pair, x.n, jj);
+            if (i == tail_step) {
+                // What lies behind the request in its last page has weight 0, but may be anything, NaN too:
+                // those rows of V become zeros. (Two streams that share the tile write the same.)
+                const int r = tail / 128;
                 ok = w.wait(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
                 }
-                if (row >= valid) {
+                if (row >= tail % 128) {
                     const uint32_t at = sbase + L::kRingOff + (r % S) * L::kTileBytes + row * 128;
-#pragma unroll
+#pragma unroll 4
                     for (int k = 0; k < D / 8; ++k)
                         ptx::st_shared_v4(at + (k / 8) * L::kBlkBytes + (((k ^ row) & 7) << 4), 0, 0, 0, 0);
                 }
                 ptx::fence_proxy_async_smem();
             }
             if (!live) {   // no row of this warp is a query's: its lanes of P and O may hold anything
-                if (i > 0) ptx::mbar_arrive(bars.alpha_ready(t));
+                if (i > 0) warp_arrive(bars.alpha_ready(t));
                 if (i + 1 == steps) {
-                    ok = w.wait(bars.stats_free(t), (n_item & 1) ^ 1, kSiteStats);
+                    ok = w.wait(bars.stats_free(t), n_item ^ 1, kSiteStats);
                     if (!__all_sync(~0u, ok)) {
                         ok = false;
                         break;
                     }
-                    ptx::mbar_arrive(bars.stats_ready(t));
+                    warp_arrive(bars.stats_ready(t));
                 }
-                ptx::mbar_arrive(bars.p_full(t));
+                warp_arrive(bars.p_full(t));
+                warp_arrive(bars.p_rest(t));
                 continue;
             }
             ptx::tc_fence_after();
-            uint32_t s[kBN];
+            const bool masked = i >= mask_from;   // some row does not see all of these keys
+            // The last 64 scores are read for the maximum and, when the first 64
+            // weights are done, once more: all 128 and the rest of the state do not
+            // fit the registers.
+            uint32_t s[kBN / 2];
             float m_tile;
             {
+                uint32_t s2[kBN / 2];
                 float mq[4];
+                ptx::tmem_ld32_max_at<0>(row_addr + colS + 64, s2, mq[2]);
+                ptx::tmem_ld32_max_at<32>(row_addr + colS + 96, s2, mq[3]);
                 ptx::tmem_ld32_max_at<0>(row_addr + colS + 0, s, mq[0]);
                 ptx::tmem_ld32_max_at<32>(row_addr + colS + 32, s, mq[1]);
-                ptx::tmem_ld32_max_at<64>(row_addr + colS + 64, s, mq[2]);
-                ptx::tmem_ld32_max_at<96>(row_addr + colS + 96, s, mq[3]);
                 ptx::tmem_wait_ld();
-                m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
-            }
-            if (j >= jmask) {   // some row does not see all of these keys
-                const int lim = kend - j * kBN;
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (masked) {
 #pragma unroll
-                for (int k = 0; k < kBN; k += 2) {
-                    s[k] = k < lim ? s[k] : 0xFF800000u;
-                    s[k + 1] = k + 1 < lim ? s[k + 1] : 0xFF800000u;
-                    mx[k / 2 % 4] = ptx::max3(mx[k / 2 % 4], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < kBN / 2; k += 2) {
+                        s[k] = k < lim ? s[k] : 0xFF800000u;
+                        s[k + 1] = k + 1 < lim ? s[k + 1] : 0xFF800000u;
+                        mq[k / 2 % 2] = ptx::max3(mq[k / 2 % 2], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                        mq[2 + k / 2 % 2] = ptx::max3(mq[2 + k / 2 % 2], k + 64 < lim ? __uint_as_float(s2[k]) : -INFINITY,
+                                                      k + 65 < lim ? __uint_as_float(s2[k + 1]) : -INFINITY);
+                    }
                 }
-                m_tile = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+                m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
             }
             const float m_new = fmaxf(m, m_tile);
             if (i > 0) {
                 const float alpha = m_new == m ? 1.0f : ptx::ex2_approx(m - m_new);
                 alpha_buf[row] = alpha;
-                ptx::mbar_arrive(bars.alpha_ready(t));
+                warp_arrive(bars.alpha_ready(t));
                 l *= alpha;
             }
             m = m_new;
@@ -730,63 +779,71 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             const float m_use = m == -INFINITY ? 0.0f : m;
             const uint64_t nm2 = ptx::f2_pack(-m_use, -m_use);
             uint64_t acc[4] = {0, 0, 0, 0};
-            uint32_t pk[kBN / 2];
+            auto weights = [&](const uint32_t (&v)[kBN / 2], uint32_t (&pk)[32], int k0) {   // of v's scores k0 .. k0 + 32
 #pragma unroll
-            for (int k = 0; k < kBN / 2; ++k) {
-                float x0, x1;
-                ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), c2, nm2), x0, x1);
-                x0 = ptx::ex2_approx(x0);
-                x1 = ptx::ex2_approx(x1);
-                acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(x0, x1));
-                pk[k] = ptx::pack2<kBf16>(x0, x1);
+                for (int k = k0 / 2; k < k0 / 2 + 16; ++k) {
+                    float x0, x1;
+                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, nm2), x0, x1);
+                    x0 = ptx::ex2_approx(x0);
+                    x1 = ptx::ex2_approx(x1);
+                    acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(x0, x1));
+                    pk[k] = ptx::pack2<kBf16>(x0, x1);
+                }
+            };
+            uint32_t pk[32];
+            weights(s, pk, 0);
+            uint32_t s2[kBN / 2];
+            ptx::tmem_ld32_at<0>(row_addr + colS + 64, s2);
+            weights(s, pk, 32);
+            ptx::tmem_ld32_at<32>(row_addr + colS + 96, s2);
+            ptx::tmem_st32_at<0>(row_addr + colS, pk);
+            ptx::tmem_wait_ld();
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            warp_arrive(bars.p_full(t));
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < kBN / 2; ++k) s2[k] = k + 64 < lim ? s2[k] : 0xFF800000u;
             }
+            weights(s2, pk, 0);
+            weights(s2, pk, 32);
+            ptx::tmem_st32_at<0>(row_addr + colS + 32, pk);
             float a0, a1;
             ptx::f2_unpack(ptx::f2_add(ptx::f2_add(acc[0], acc[1]), ptx::f2_add(acc[2], acc[3])), a0, a1);
             l += a0 + a1;
-            ptx::tmem_st32_at<0>(row_addr + colS, pk);
-            ptx::tmem_st32_at<32>(row_addr + colS + 32, pk);
             if (i + 1 == steps) {
                 // the epilogue has read the stream's last m and l
-                ok = w.wait(bars.stats_free(t), (n_item & 1) ^ 1, kSiteStats);
+                ok = w.wait(bars.stats_free(t), n_item ^ 1, kSiteStats);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
                 }
                 m_buf[row] = m;
                 l_buf[row] = l;
-                ptx::mbar_arrive(bars.stats_ready(t));
+                warp_arrive(bars.stats_ready(t));
             }
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(bars.p_full(t));
+            warp_arrive(bars.p_rest(t));
         }
         if (!ok) break;
-        ++n_item;
+        n_item ^= 1;
     }
 }
 
 // ---------------------------------------------------------------- correction + epilogue
 
-// The warp's 4 KB staging slice holds 128 bytes of each of its 32 rows, as in
-// store_o_rows: each lane puts 16-byte pieces of its own row, then the warp
-// stores whole lines, of four rows at a time.
-__device__ __forceinline__ void put_piece(uint32_t wslice, int lane, int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    ptx::st_shared_v4(wslice + static_cast<uint32_t>(lane) * 128u + ((static_cast<uint32_t>(c) ^ (lane & 7u)) << 4), x, y, z, w);
-}
-// to: where column 0 of the 128 bytes of line 0 goes; line[r]: the line of row r
-// of the 32, in shared memory; rows: how many of them there are.
-template <int kLineBytes>
-__device__ __forceinline__ void store_lines(uint32_t wslice, int lane, char* to, const int* line, int rows) {
-    __syncwarp();
-    const int r0 = lane >> 3;
-    const uint32_t rd = wslice + static_cast<uint32_t>(r0) * 128u + (static_cast<uint32_t>((lane & 7) ^ r0) << 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (4 * i >= rows) break;
-        const uint4 x = ptx::ld_shared_v4((rd ^ ((i & 1) << 6)) + static_cast<uint32_t>(i) * 512u);
-        if (4 * i + r0 < rows) *reinterpret_cast<uint4*>(to + static_cast<long long>(line[4 * i + r0]) * kLineBytes + (lane & 7) * 16) = x;
+// 32 bytes to global memory, one sector; as two stores where the output is
+// aligned to 16 bytes only.
+__device__ __forceinline__ void store32(char* to, bool wide, const uint32_t* v) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
-    __syncwarp();   // before the slice is written again
 }
 
 template <int D, bool kBf16>
@@ -798,16 +855,12 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
     const int row = 32 * q + lane;
     const uint32_t row_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const float* rowbuf = reinterpret_cast<const float*>(smem + L::kRowOff);  // alpha | m | l
-    const uint32_t wslice = sbase + L::kStageOff + static_cast<uint32_t>(q) * (32u * 128u);
-    int* lines = reinterpret_cast<int*>(smem + L::kLineOff);
+    int row_line;   // of the row in o, from its tile's first on
     {
         const int tk = by_group(row, (65536u + p.group - 1) / p.group);
-        lines[row] = tk * p.hq + (row - tk * p.group);
-        lines[kBM + row] = row;
+        row_line = tk * p.hq + (row - tk * p.group);
     }
-    __syncwarp();   // a warp reads those of its own rows
-    lines += 32 * q;
-    const int* ident = lines + kBM;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 
     uint32_t n_s = 0, n_items = 0;   // a bit for each stream: steps, parts, modulo 2
     int n_part = 0;
@@ -816,11 +869,12 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
     // At a part's first step O is overwritten, not rescaled: what the PV product
     // waits for is that the O of the stream's last part has been read. That
     // arrival is made here and, from then on, by the epilogue.
-    for (int t = 0; t < 2; ++t) ptx::mbar_arrive(bars.p_full(t));
+    for (int t = 0; t < 2; ++t) warp_arrive(bars.p_full(t));
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
         const bool pair = x.kind == kPair;
         const int most = max(x.steps0, x.steps1);
         for (int i = 1; i < most && ok; ++i) {
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
                 if (i >= x.steps(t)) continue;
                 ok = w.wait(bars.alpha_ready(t), (n_s >> t) & 1, kSiteAlpha);
@@ -853,10 +907,11 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                     ptx::tmem_wait_st();
                 }
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(bars.p_full(t));
+                warp_arrive(bars.p_full(t));
             }
         }
         // Epilogue.
+#pragma unroll 1
         for (int tile = 0; tile < (pair ? 2 : 1) && ok; ++tile) {
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // of the streams that have this tile's rows
             bool has[2];
@@ -874,7 +929,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 n_items ^= 1u << t;
                 m[e] = rowbuf[(2 + t) * kBM + row];
                 l[e] = rowbuf[(4 + t) * kBM + row];
-                ptx::mbar_arrive(bars.stats_free(t));
+                warp_arrive(bars.stats_free(t));
             }
             if (!ok) break;
             ptx::tc_fence_after();
@@ -883,10 +938,10 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
             auto release = [&] {
                 ptx::tc_fence_before();
                 if (pair) {
-                    if (has[0]) ptx::mbar_arrive(bars.p_full(tile));
+                    if (has[0]) warp_arrive(bars.p_full(tile));
                 } else {
-                    ptx::mbar_arrive(bars.p_full(0));
-                    if (has[1]) ptx::mbar_arrive(bars.p_full(1));
+                    warp_arrive(bars.p_full(0));
+                    if (has[1]) warp_arrive(bars.p_full(1));
                 }
             };
             if (32 * q >= rows) {
@@ -908,8 +963,13 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 f[0] *= inv;
                 f[1] *= inv;
             }
-            // 32 columns of the row from c on: of the tile's stream, or of both.
-            auto load32 = [&](int c, uint32_t (&v)[32]) {
+            const bool whole = x.buffer < 0;
+            const long long line = whole ? static_cast<long long>(x.q0 + (pair ? tile * p.tok_tile : 0)) * p.hq + x.h * p.group + row_line
+                                         : static_cast<long long>(x.buffer) * p.part_rows + tile * kBM + row;
+            char* to = whole ? static_cast<char*>(p.o) + line * (2 * D) : reinterpret_cast<char*>(p.part_o) + line * (4 * D);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {   // columns of the tile's stream, or of both
+                uint32_t v[32];
                 ptx::tmem_ld32_at<0>(row_addr + col0 + c, v);
                 ptx::tmem_wait_ld();
 #pragma unroll
@@ -924,47 +984,31 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                             v[e + k] = __float_as_uint(fmaf(__uint_as_float(u[k]), f[1], __uint_as_float(v[e + k])));
                     }
                 }
+                if (c + 32 >= D) release();
                 if (ll == 0.0f) {   // no key, whatever the values hold
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = 0;
                 }
-            };
-            if (x.buffer < 0) {
-                const long long line0 = static_cast<long long>(x.q0 + (pair ? tile * p.tok_tile : 0)) * p.hq + x.h * p.group;
-                char* to = static_cast<char*>(p.o) + line0 * (2 * D);
-#pragma unroll 1
-                for (int h = 0; h < D; h += 64, to += 128) {
+                if (row < rows) {
+                    if (whole) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t v[32];
-                        load32(h + 32 * k, v);
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t y[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                w[s] = ptx::pack2<kBf16>(__uint_as_float(v[8 * e + 2 * s]), __uint_as_float(v[8 * e + 2 * s + 1]));
-                            put_piece(wslice, lane, 4 * k + e, w[0], w[1], w[2], w[3]);
+                            for (int s = 0; s < 8; ++s)
+                                y[s] = ptx::pack2<kBf16>(__uint_as_float(v[16 * e + 2 * s]), __uint_as_float(v[16 * e + 2 * s + 1]));
+                            store32(to + 2 * c + 32 * e, wide, y);
                         }
-                    }
-                    if (h + 64 >= D) release();
-                    store_lines<2 * D>(wslice, lane, to, lines, rows - 32 * q);
-                }
-                if (row < rows)
-                    p.lse[line0 + lines[lane]] = ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
-            } else {
-                const long long line0 = static_cast<long long>(x.buffer) * p.part_rows + tile * kBM;
-                char* to = reinterpret_cast<char*>(p.part_o + line0 * D);
-#pragma unroll 1
-                for (int h = 0; h < D; h += 32, to += 128) {
-                    uint32_t v[32];
-                    load32(h, v);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) put_piece(wslice, lane, e, v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                    if (h + 32 >= D) release();
-                    store_lines<4 * D>(wslice, lane, to, ident, rows - 32 * q);
+                        for (int e = 0; e < 4; ++e) store32(to + 4 * c + 32 * e, true, v + 8 * e);
+                    }
                 }
-                if (row < rows) *reinterpret_cast<float2*>(p.part_ml + 2 * (line0 + row)) = make_float2(mm, ll);
+                __syncwarp();
+            }
+            if (row < rows) {
+                if (whole) p.lse[line] = ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
+                else *reinterpret_cast<float2*>(p.part_ml + 2 * line) = make_float2(mm, ll);
             }
         }
         if (!ok) break;
@@ -988,20 +1032,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(bars.q_full(t), 1);
             ptx::mbar_init(bars.q_empty(t), 1);
             ptx::mbar_init(bars.s_full(t), 1);
-            ptx::mbar_init(bars.alpha_ready(t), kBM);
-            ptx::mbar_init(bars.stats_ready(t), kBM);
-            ptx::mbar_init(bars.stats_free(t), kBM);
-            ptx::mbar_init(bars.p_full(t), 2 * kBM);
+            ptx::mbar_init(bars.alpha_ready(t), 4);   // a warp's arrival each
+            ptx::mbar_init(bars.stats_ready(t), 4);
+            ptx::mbar_init(bars.stats_free(t), 4);
+            ptx::mbar_init(bars.p_full(t), 8);
+            ptx::mbar_init(bars.p_rest(t), 4);
             ptx::mbar_init(bars.o_full(t), 1);
         }
+#pragma unroll 1
         for (int s = 0; s < L::kStages; ++s) {
             ptx::mbar_init(bars.kv_full(s), 1);
             ptx::mbar_init(bars.kv_empty(s), 1);
         }
+#pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
             ptx::mbar_init(bars.part_full(s), 1);
             ptx::mbar_init(bars.part_empty(s), kPartUsers);
@@ -1026,13 +1074,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter w{abort_flag, p.wait_limit_ns};
 
     if (warp < kCorrWarp0) {
-        ptx::setmaxnreg_inc<kRegSoftmax>();
+        ptx::setmaxnreg_inc<R16S>();
         softmax_role<D, kBf16>(p, tmem, smem, sbase, bars, w, warp / 4);
     } else if (warp < kLoadWarp) {
-        ptx::setmaxnreg_dec<kRegCorr>();
+        ptx::setmaxnreg_dec<R16C>();
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
     } else {
-        ptx::setmaxnreg_dec<kRegOther>();
+        ptx::setmaxnreg_dec<R16O>();
         if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
         else if (warp == kMmaWarp) mma_issuer<D, kBf16>(p, smem, sbase, tmem, bars, w);
         else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
