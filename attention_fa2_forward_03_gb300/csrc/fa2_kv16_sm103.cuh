@@ -122,8 +122,7 @@ struct Lay {
     static constexpr int kRowOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;   // alpha[2][128], m[2][128], l[2][128]
     static constexpr int kPartOff = kRowOff + 6 * kBM * 4;
     static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
-    static constexpr int kLineOff = kIdOff + 4 * 32 * 4;   // lines of a tile's rows in o
-    static constexpr int kFirstOff = kLineOff + kBM * 4;   // page ids of the first two tiles of a part [kParts][16]
+    static constexpr int kFirstOff = kIdOff + 4 * 32 * 4;   // page ids of the first two tiles of a part [kParts][16]
     static constexpr int kMiscOff = kFirstOff + kParts * 16 * 4;
     static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -571,17 +570,18 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
     constexpr uint32_t kAB = kBf16 ? 1u : 0u;
     constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kBN);
     constexpr uint32_t kIdO = ptx::idesc_f16(kAB, 0, 1, kBM, D);
-    auto stage_addr = [&](int r) { return sbase + L::kRingOff + (r % S) * L::kTileBytes; };
-    auto issue_qk = [&](int t, int qslot, int k_ring) {
-        const uint64_t qd = ptx::desc_sw128(sbase + L::kQOff + qslot * L::kTileBytes, 16, 1024);
-        const uint64_t kd = ptx::desc_sw128(stage_addr(k_ring), 16, 1024);
+    // Descriptors of the ring's first place as keys and as values, and of the
+    // query tiles' first; others lie kTileBytes / 16 further on.
+    constexpr uint32_t kNext = L::kTileBytes >> 4;
+    const uint64_t keys = ptx::desc_sw128(sbase + L::kRingOff, 16, 1024), values = ptx::desc_sw128(sbase + L::kRingOff, L::kBlkBytes, 1024),
+                   query = ptx::desc_sw128(sbase + L::kQOff, 16, 1024);
+    auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
+    auto issue_qk = [&](int t, uint64_t qd, uint64_t kd) {
         qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
         ptx::tc_commit_elect(bars.s_full(t));
     };
-    auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
     // P V of a tile whose p_full has completed: its halves as their weights are there.
-    auto issue_pv = [&](int t, int v_ring, bool acc, uint32_t parity) {
-        const uint64_t vd = ptx::desc_sw128(stage_addr(v_ring), L::kBlkBytes, 1024);
+    auto issue_pv = [&](int t, uint64_t vd, bool acc, uint32_t parity) {
         ptx::tc_fence_after();
         mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
         if (!wait_u(bars.p_rest(t), parity, kSitePFull)) return false;
@@ -589,60 +589,85 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
         mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t) + 32, vd + 512, kIdO, 1u);
         return true;
     };
-    auto wait_ring = [&](int r) { return wait_u(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull); };
     auto release = [&](int r) { ptx::tc_commit_elect(bars.kv_empty(r % S)); };
+    // Waits for two entries of the ring and one more barrier together.
+    auto wait_three = [&](int r0, int r1, uint32_t bar, uint32_t parity) {
+        const uint32_t wb[3] = {bars.kv_full(r0 % S), bars.kv_full(r1 % S), bar};
+        const uint32_t wp[3] = {static_cast<uint32_t>((r0 / S) & 1), static_cast<uint32_t>((r1 / S) & 1), parity & 1};
+        return __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull));
+    };
 
     int ring = 0, n_part = 0;
     uint32_t nq = 0, np = 0;   // a bit for each place: query tiles used, P tiles consumed, modulo 2
     bool ok = true;
     Part x;
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
-        // Pair: both streams work on every tile of keys that they have (stream 1
-        // on all). Single: on every other one. So QK of tile j + ahead follows PV of
-        // tile j.
-        const bool pair = x.kind == kPair;
-        const int ahead = pair ? 1 : 2;
-        auto place = [&](int t) { return pair ? t : x.qslot; };   // of the stream's query tile
-        if (pair && x.steps0 > 0) ok = wait_u(bars.q_full(0), nq & 1, kSiteQFull);
-        if (ok) ok = wait_u(bars.q_full(place(1)), (nq >> place(1)) & 1, kSiteQFull);
-        for (int e = 0; ok && e < min(ahead, x.n); ++e) {
-            if (!(ok = wait_ring(ring))) break;
+        if (x.kind == kPair) {
+            // As the forward kernel's general mode: at key tile j the streams with
+            // j < steps(t) take part, stream 1 in all.
+            if (x.steps0 > 0) ok = wait_u(bars.q_full(0), nq & 1, kSiteQFull);
+            if (!ok || !(ok = wait_three(ring, ring, bars.q_full(1), nq >> 1))) break;
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-                if (pair ? x.steps(t) == 0 : t != e) continue;
-                issue_qk(t, place(t), ring);
-                if (pair ? x.steps(t) == 1 : e + 1 == x.n) ptx::tc_commit_elect(bars.q_empty(place(t)));
+                if (x.steps(t) == 0) continue;
+                issue_qk(t, query + t * kNext, keys + (ring % S) * kNext);
+                if (x.steps(t) == 1) ptx::tc_commit_elect(bars.q_empty(t));
             }
             release(ring++);
-        }
-        for (int j = 0; ok && j < x.n; ++j) {
-            const bool more = j + ahead < x.n;
-            const int v_ring = ring++, k_ring = more ? ring++ : v_ring;
-            const int t0 = pair ? (j < x.steps0 ? 0 : 1) : j & 1, t1 = pair ? 1 : t0;   // streams that take part
-            // V_j, the next keys and the first weights of the first stream are waited for together.
-            const uint32_t wb[3] = {bars.kv_full(v_ring % S), bars.kv_full(k_ring % S), bars.p_full(t0)};
-            const uint32_t wp[3] = {static_cast<uint32_t>((v_ring / S) & 1), static_cast<uint32_t>((k_ring / S) & 1), (np >> t0) & 1};
-            if (!(ok = __all_sync(~0u, w.wait_all<3>(wb, wp, kSiteKvFull)))) break;
+            for (int j = 0; j < x.n; ++j) {
+                const bool more = j + 1 < x.n;
+                const int v_ring = ring++, k_ring = more ? ring++ : v_ring;
+                const uint64_t vd = values + (v_ring % S) * kNext, kd = keys + (k_ring % S) * kNext;
+                const int t0 = j < x.steps0 ? 0 : 1;
+                // V_j, K_{j+1} and the first stream's first weights are waited for together.
+                if (!(ok = wait_three(v_ring, k_ring, bars.p_full(t0), np >> t0))) break;
 #pragma unroll 1
-            for (int t = t0; t <= t1; ++t) {
-                if (t != t0 && !(ok = wait_u(bars.p_full(t), (np >> t) & 1, kSitePFull))) break;
-                if (!(ok = issue_pv(t, v_ring, j >= ahead, (np >> t) & 1))) break;
-                np ^= 1u << t;
-                if (t == t1) release(v_ring);
-                const int mine = pair ? x.steps(t) : x.n;
-                if (j + ahead < mine) {
-                    issue_qk(t, place(t), k_ring);
-                    if (j + ahead + 1 == mine) ptx::tc_commit_elect(bars.q_empty(place(t)));
-                    if (t == t1) release(k_ring);
+                for (int t = 0; t < 2; ++t) {
+                    if (t < t0) continue;
+                    if (t != t0 && !(ok = wait_u(bars.p_full(t), (np >> t) & 1, kSitePFull))) break;
+                    if (!(ok = issue_pv(t, vd, j > 0, (np >> t) & 1))) break;
+                    np ^= 1u << t;
+                    if (t == 1) release(v_ring);
+                    if (j + 1 < x.steps(t)) {
+                        issue_qk(t, query + t * kNext, kd);
+                        if (j + 2 == x.steps(t)) ptx::tc_commit_elect(bars.q_empty(t));
+                        if (t == 1) release(k_ring);
+                    } else {
+                        ptx::tc_commit_elect(bars.o_full(t));
+                    }
+                }
+                if (!ok) break;
+            }
+            if (!ok) break;
+            nq ^= x.steps0 > 0 ? 3u : 2u;
+        } else {
+            // Every other tile of keys for each stream: QK of tile j + 2 follows PV of
+            // tile j; the first two, behind no PV, count as steps -2 and -1.
+            const uint64_t qd = query + x.qslot * kNext;
+            for (int j = -2; j < x.n; ++j) {
+                const bool first = j < 0, more = j + 2 < x.n;
+                if (first && !more) continue;   // n = 1
+                const int t = j & 1, v_ring = first ? ring : ring++, k_ring = more ? ring++ : v_ring;
+                const uint64_t vd = values + (v_ring % S) * kNext, kd = keys + (k_ring % S) * kNext;
+                if (!(ok = wait_three(v_ring, k_ring, first ? bars.q_full(x.qslot) : bars.p_full(t), first ? nq >> x.qslot : np >> t))) break;
+                ptx::tc_fence_after();
+                if (!first) {
+                    if (!(ok = issue_pv(t, vd, j > 1, (np >> t) & 1))) break;
+                    np ^= 1u << t;
+                    release(v_ring);
+                }
+                if (more) {
+                    issue_qk(t, qd, kd);
+                    if (j + 3 == x.n) ptx::tc_commit_elect(bars.q_empty(x.qslot));
+                    release(k_ring);
                 } else {
                     ptx::tc_commit_elect(bars.o_full(t));
                 }
             }
+            if (!ok) break;
+            nq ^= 1u << x.qslot;
         }
-        if (!ok) break;
-        if (pair && x.steps0 > 0) nq ^= 1u;
-        nq ^= 1u << place(1);
     }
     // Every MMA issued above finishes before the CTA frees its TMEM.
     ptx::tc_commit_elect(bars.mma_done());
