@@ -137,6 +137,35 @@ struct BarSet : Bars<D> {
     __device__ uint32_t p_rest(int t) const { return this->base + 8 * (17 + 2 * S + 2 * kParts + t); }
 };
 
+// Where a tile's 128 keys lie in a place of the ring, and in which order they are
+// the columns of S and P. Pages of 32 tokens and more: in order, D / 64 blocks of
+// 64 columns one after another, each filled by a box of a page's rows. Pages of 16
+// (with two blocks): that takes 32 boxes for a tile of keys and values, about 100
+// cycles each whatever their size, which bounds the copies (64 requests of up to
+// 16384 tokens at 5.3 TB/s). There a box has both blocks of a page, which lie behind
+// one another, and the groups of eight rows that one product reads have to be a
+// constant distance apart: first come the pages' first eight tokens, then their
+// last eight.
+template <int D, bool kSmall>
+struct Tiles {
+    static_assert(!kSmall || D == 128, "pages of 16 with two blocks");
+    static constexpr int kBlkBytes = kSmall ? 2048 : Layout<D>::kBlkBytes;   // from a block to the next
+    static constexpr int kGroupBytes = kSmall ? 4096 : 1024;                 // from a product's eight keys to the next
+    static constexpr int kHalfBytes = kSmall ? 1024 : 8192;                  // from the first 64 columns' keys to the others'
+    // Key of column c, and the place of key r's row in its block.
+    static __host__ __device__ constexpr int key_of(int c) { return kSmall ? c % 64 / 8 * 16 + c / 64 * 8 + c % 8 : c; }
+    static __device__ __forceinline__ int row_bytes(int r) { return kSmall ? (r >> 4) * 4096 + (r & 15) * 128 : r * 128; }
+};
+
+// 4-D tiled copy global -> shared.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int u, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        : "memory");
+}
+
 // One arrival for the warp, behind what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -144,7 +173,8 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 // O (+)= P V over one half of a tile's keys, in four steps of 16: P from TMEM
-// (8 columns a step), V MN-major (2048 bytes a step).
+// (8 columns a step), V MN-major (kStep * 16 bytes a step).
+template <int kStep>
 __device__ __forceinline__ void mma_half(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 blo, bhi, t0, t1;\n\t.reg .b64 b;\n\t"
@@ -153,13 +183,13 @@ __device__ __forceinline__ void mma_half(uint32_t d_tmem, uint32_t a_tmem, uint6
         "setp.eq.b32 pt, %4, %4;\n\t"
         "mov.b64 {blo, bhi}, %2;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
-        "add.u32 t0, %1, 8;\n\tadd.u32 t1, blo, 128;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "add.u32 t0, %1, 8;\n\tadd.u32 t1, blo, %5;\n\tmov.b64 b, {t1, bhi};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
-        "add.u32 t0, %1, 16;\n\tadd.u32 t1, blo, 256;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "add.u32 t0, %1, 16;\n\tadd.u32 t1, blo, %6;\n\tmov.b64 b, {t1, bhi};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
-        "add.u32 t0, %1, 24;\n\tadd.u32 t1, blo, 384;\n\tmov.b64 b, {t1, bhi};\n\t"
+        "add.u32 t0, %1, 24;\n\tadd.u32 t1, blo, %7;\n\tmov.b64 b, {t1, bhi};\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t0], b, %3, pt;\n\t"
-        "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        "}" ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep)
         : "memory");
 }
 
@@ -485,17 +515,17 @@ struct Queries {
     }
 };
 
-// A box for each page's 64 columns, each by a lane of its own.
-template <int D>
+// A box for each page's 64 columns (kSmall: for each page), each by a lane of its own.
+template <int D, bool kSmall>
 __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p, uint8_t* smem,
                                          uint32_t sbase, const BarSet<D>& bars, const Waiter& w) {
     using L = Lay<D>;
-    constexpr int S = L::kStages, kBlks = D / 64;
+    constexpr int S = L::kStages, kBlks = kSmall ? 1 : D / 64;
     const int lane = threadIdx.x & 31;
     const int pages = kBN >> p.log2_page;          // of a tile
     const int page_at = lane / kBlks, blk = lane % kBlks;
     const bool loads = page_at < pages;
-    const uint32_t box = blk * L::kBlkBytes + page_at * (p.page * 128);
+    const uint32_t box = kSmall ? page_at * 4096 : blk * L::kBlkBytes + page_at * (p.page * 128);
     int* ids = reinterpret_cast<int*>(smem + L::kIdOff) + lane;   // of the lane's page, tile modulo 4
     const int nothing = p.num_pages * p.hkv * 2;   // past the tensor: a box of zeros
     int ring = 0, n_part = 0;
@@ -539,7 +569,11 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
             }
             if (lane == 0) ptx::mbar_arrive_expect_tx(bars.kv_full(s), L::kTileBytes);
             __syncwarp();
-            if (loads) ptx::tma_load_3d(sbase + L::kRingOff + s * L::kTileBytes + box, tmKV, blk * 64, 0, z, bars.kv_full(s));
+            const uint32_t dst = sbase + L::kRingOff + s * L::kTileBytes + box;
+            if (loads) {
+                if constexpr (kSmall) tma_load_4d(dst, tmKV, 0, 0, 0, z, bars.kv_full(s));
+                else ptx::tma_load_3d(dst, tmKV, blk * 64, 0, z, bars.kv_full(s));
+            }
             ++ring;
         };
         // Query tiles whose places are free go before the keys, whose page ids are
@@ -562,31 +596,41 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
 
 // ---------------------------------------------------------------- MMA issuer
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSmall>
 __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint32_t sbase, uint32_t tmem, const BarSet<D>& bars,
                                            const Waiter& w) {
     using L = Lay<D>;
     constexpr int S = L::kStages;
     constexpr uint32_t kAB = kBf16 ? 1u : 0u;
-    constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kBN);
+    using T = Tiles<D, kSmall>;
+    constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kSmall ? kBN / 2 : kBN);
     constexpr uint32_t kIdO = ptx::idesc_f16(kAB, 0, 1, kBM, D);
     // Descriptors of the ring's first place as keys and as values, and of the
     // query tiles' first; others lie kTileBytes / 16 further on.
     constexpr uint32_t kNext = L::kTileBytes >> 4;
-    const uint64_t keys = ptx::desc_sw128(sbase + L::kRingOff, 16, 1024), values = ptx::desc_sw128(sbase + L::kRingOff, L::kBlkBytes, 1024),
+    const uint64_t keys = ptx::desc_sw128(sbase + L::kRingOff, 16, T::kGroupBytes),
+                   values = ptx::desc_sw128(sbase + L::kRingOff, T::kBlkBytes, T::kGroupBytes),
                    query = ptx::desc_sw128(sbase + L::kQOff, 16, 1024);
     auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
     auto issue_qk = [&](int t, uint64_t qd, uint64_t kd) {
-        qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
+        if constexpr (kSmall) {
+            constexpr uint32_t kQ = L::kBlkBytes >> 4, kK = T::kBlkBytes >> 4;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+                ptx::mma_ss_kloop<2, 4, 6, kQ, kQ + 2, kQ + 4, kQ + 6, 2, 4, 6, kK, kK + 2, kK + 4, kK + 6, 8>(
+                    tmem + Layout<D>::col_s(t) + 64 * h, qd, kd + h * (T::kHalfBytes >> 4), kIdS, 0u);
+        } else {
+            qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
+        }
         ptx::tc_commit_elect(bars.s_full(t));
     };
     // P V of a tile whose p_full has completed: its halves as their weights are there.
     auto issue_pv = [&](int t, uint64_t vd, bool acc, uint32_t parity) {
         ptx::tc_fence_after();
-        mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
+        mma_half<T::kGroupBytes / 8>(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t), vd, kIdO, acc ? 1u : 0u);
         if (!wait_u(bars.p_rest(t), parity, kSitePFull)) return false;
         ptx::tc_fence_after();
-        mma_half(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t) + 32, vd + 512, kIdO, 1u);
+        mma_half<T::kGroupBytes / 8>(tmem + Layout<D>::col_o(t), tmem + Layout<D>::col_s(t) + 32, vd + (T::kHalfBytes >> 4), kIdO, 1u);
         return true;
     };
     auto release = [&](int r) { ptx::tc_commit_elect(bars.kv_empty(r % S)); };
@@ -686,10 +730,11 @@ __device__ __forceinline__ int stream_tokens(const Params& p, const Part& x, int
 // group / 2^16 of a quotient, so r / group by less than 1 / group.
 __device__ __forceinline__ int by_group(int r, uint32_t inv) { return static_cast<int>((static_cast<uint32_t>(r) * inv) >> 16); }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSmall>
 __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars,
                                              const Waiter& w, int t) {
     using L = Lay<D>;
+    using T = Tiles<D, kSmall>;
     constexpr int S = L::kStages;
     const int row = threadIdx.x & 127;          // row of the query tile = TMEM lane
     const uint32_t row_addr = tmem + (static_cast<uint32_t>(row & ~31) << 16);
@@ -742,10 +787,10 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
                     break;
                 }
                 if (row >= tail % 128) {
-                    const uint32_t at = sbase + L::kRingOff + (r % S) * L::kTileBytes + row * 128;
+                    const uint32_t at = sbase + L::kRingOff + (r % S) * L::kTileBytes + T::row_bytes(row);
 #pragma unroll 4
                     for (int k = 0; k < D / 8; ++k)
-                        ptx::st_shared_v4(at + (k / 8) * L::kBlkBytes + (((k ^ row) & 7) << 4), 0, 0, 0, 0);
+                        ptx::st_shared_v4(at + (k / 8) * T::kBlkBytes + (((k ^ row) & 7) << 4), 0, 0, 0, 0);
                 }
                 ptx::fence_proxy_async_smem();
             }
@@ -783,11 +828,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
                     for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < kBN / 2; k += 2) {
-                        s[k] = k < lim ? s[k] : 0xFF800000u;
-                        s[k + 1] = k + 1 < lim ? s[k + 1] : 0xFF800000u;
+                        s[k] = T::key_of(k) < lim ? s[k] : 0xFF800000u;
+                        s[k + 1] = T::key_of(k + 1) < lim ? s[k + 1] : 0xFF800000u;
                         mq[k / 2 % 2] = ptx::max3(mq[k / 2 % 2], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                        mq[2 + k / 2 % 2] = ptx::max3(mq[2 + k / 2 % 2], k + 64 < lim ? __uint_as_float(s2[k]) : -INFINITY,
-                                                      k + 65 < lim ? __uint_as_float(s2[k + 1]) : -INFINITY);
+                        mq[2 + k / 2 % 2] = ptx::max3(mq[2 + k / 2 % 2], T::key_of(k + 64) < lim ? __uint_as_float(s2[k]) : -INFINITY,
+                                                      T::key_of(k + 65) < lim ? __uint_as_float(s2[k + 1]) : -INFINITY);
                     }
                 }
                 m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
@@ -828,7 +873,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             warp_arrive(bars.p_full(t));
             if (masked) {
 #pragma unroll
-                for (int k = 0; k < kBN / 2; ++k) s2[k] = k + 64 < lim ? s2[k] : 0xFF800000u;
+                for (int k = 0; k < kBN / 2; ++k) s2[k] = T::key_of(k + 64) < lim ? s2[k] : 0xFF800000u;
             }
             weights(s2, pk, 0);
             weights(s2, pk, 32);
@@ -1042,7 +1087,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
 
 // ---------------------------------------------------------------- kernels
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
     fa2_kv16_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV, const Params p) {
     using L = Lay<D>;
@@ -1100,14 +1145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<R16S>();
-        softmax_role<D, kBf16>(p, tmem, smem, sbase, bars, w, warp / 4);
+        softmax_role<D, kBf16, kSmall>(p, tmem, smem, sbase, bars, w, warp / 4);
     } else if (warp < kLoadWarp) {
         ptx::setmaxnreg_dec<R16C>();
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
     } else {
         ptx::setmaxnreg_dec<R16O>();
-        if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
-        else if (warp == kMmaWarp) mma_issuer<D, kBf16>(p, smem, sbase, tmem, bars, w);
+        if (warp == kLoadWarp) producer<D, kSmall>(&tmQ, &tmKV, p, smem, sbase, bars, w);
+        else if (warp == kMmaWarp) mma_issuer<D, kBf16, kSmall>(p, smem, sbase, tmem, bars, w);
         else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
     }
 
