@@ -1019,20 +1019,20 @@ fa2_status rope_check(const void* positions, const void* inv_freq, const void* a
 }
 bool rope_sizes(int d, int rot_dim, int n_axes) { return (d == 64 || d == 128) && rot_dim <= d && rot_dim % 16 == 0 && n_axes <= 8; }
 
-// Eight tokens a block where that gives every SM four blocks or more: their
-// angles are made eight at a time. Else one, which spreads few tokens wider.
+// Several tokens a block where that gives every SM four blocks or more: their
+// angles are made together. Else one, which spreads few tokens wider.
 template <bool kCache>
 fa2_status rope_launch(int dev, const fa2::rope::Params& p, int d, bool bf, cudaStream_t stream) {
     using namespace fa2::rope;
-    const long long eights = (static_cast<long long>(p.tokens) + 7) / 8;
-    const bool many = eights >= 4LL * sm_count(dev);
-    const long long grid = many ? eights : p.tokens;
+    const long long blocks = (static_cast<long long>(p.tokens) + kTokens - 1) / kTokens;
+    const bool many = blocks >= 4LL * sm_count(dev);
+    const long long grid = many ? blocks : p.tokens;
     auto go = [&](auto few, auto many_k) { return kv4_launch_kernel(many ? +many_k : +few, grid, kThreads, 0, stream, p); };
     if (d == 128)
-        return bf ? go(fa2_rope_kernel<128, true, kCache, 1>, fa2_rope_kernel<128, true, kCache, 8>)
-                  : go(fa2_rope_kernel<128, false, kCache, 1>, fa2_rope_kernel<128, false, kCache, 8>);
-    return bf ? go(fa2_rope_kernel<64, true, kCache, 1>, fa2_rope_kernel<64, true, kCache, 8>)
-              : go(fa2_rope_kernel<64, false, kCache, 1>, fa2_rope_kernel<64, false, kCache, 8>);
+        return bf ? go(fa2_rope_kernel<128, true, kCache, 1>, fa2_rope_kernel<128, true, kCache, kTokens>)
+                  : go(fa2_rope_kernel<128, false, kCache, 1>, fa2_rope_kernel<128, false, kCache, kTokens>);
+    return bf ? go(fa2_rope_kernel<64, true, kCache, 1>, fa2_rope_kernel<64, true, kCache, kTokens>)
+              : go(fa2_rope_kernel<64, false, kCache, 1>, fa2_rope_kernel<64, false, kCache, kTokens>);
 }
 
 fa2_status rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,

@@ -45,21 +45,17 @@ enum Site : int { kSiteRows = 53, kSitePart = 54 };
 constexpr int kMaxCtas = 160;
 constexpr int kSchedWarp = 14;
 // Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
-// for one, and every row block kStart more for its start and its end.
-#ifndef R16S
-#define R16S 168
-#define R16C 120
-#define R16O 56
-#endif
-#ifndef K16P
-#define K16P 3
-#define K16S 2
-#define K16B 4
-#define K16M 4
-#endif
-constexpr int kPairUnits = K16P, kSingleUnits = K16S;
-constexpr int kStart = K16B;
-constexpr int kMinRun = K16M;        // units of a run at least
+// for one, and every row block kStart more for its start and its end. A step of 24
+// decoding requests and 3 chunks up to 512 tokens, contexts up to 8192, takes 173 us
+// (224 with pages of 16); with 4, 3 and 5 units 177 (235), with 2, 1 and 2 179 (257). A
+// prompt of 4096 tokens, whose row blocks are of all lengths, takes 138 us; 144 with
+// kStart = 2, and with 8 the step with pages of 16 takes 228.
+constexpr int kPairUnits = 3, kSingleUnits = 2, kStart = 4;
+constexpr int kMinRun = 4;        // units of a run at least
+// Registers a thread. What spills is waited for as long as keys are: the cache
+// that shared memory leaves is small. With 176 and 104 for the softmax and the
+// epilogue the prompt takes 137 us instead of 136, with 184 and 88 210.
+constexpr uint32_t kRegSoft = 168, kRegOut = 120, kRegRest = 56;   // 2 x 168 + 120 + 56 = 512
 constexpr int kParts = 4;         // parts on their way from the scheduling warp
 constexpr int kPartUsers = 14;    // warps that read a part
 constexpr int kJoinY = 4, kJoinThreads = 256;
@@ -1144,13 +1140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter w{abort_flag, p.wait_limit_ns};
 
     if (warp < kCorrWarp0) {
-        ptx::setmaxnreg_inc<R16S>();
+        ptx::setmaxnreg_inc<kRegSoft>();
         softmax_role<D, kBf16, kSmall>(p, tmem, smem, sbase, bars, w, warp / 4);
     } else if (warp < kLoadWarp) {
-        ptx::setmaxnreg_dec<R16C>();
+        ptx::setmaxnreg_dec<kRegOut>();
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
     } else {
-        ptx::setmaxnreg_dec<R16O>();
+        ptx::setmaxnreg_dec<kRegRest>();
         if (warp == kLoadWarp) producer<D, kSmall>(&tmQ, &tmKV, p, smem, sbase, bars, w);
         else if (warp == kMmaWarp) mma_issuer<D, kBf16, kSmall>(p, smem, sbase, tmem, bars, w);
         else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);

@@ -29,7 +29,11 @@ namespace rope {
 
 constexpr int kSiteAxis = 52;   // an entry of `axes` outside 0 .. n_axes - 1
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;       // items (32 bytes) of a thread in flight
+// Tokens of a block where there are many, items (32 bytes) of a thread in flight
+// and blocks an SM. 8191 tokens of 48 heads take 38.9 us; 45.1 with 8, 4 and 3
+// (what 80 registers allow), 41.0 with 2, 2 and 5; 4, 3 and 4 take as long, but 18.4 us
+// for 2000 tokens instead of 16.4.
+constexpr int kTokens = 4, kBatch = 2, kBlocks = 5;
 
 struct Params {
     const void* in[3];          // queries, keys, values (values: the append alone)
@@ -66,7 +70,7 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
 // The rows of one block: kTok tokens of every head. An item is 16 elements of
 // a row: the eight pairs that share a table entry, or 16 neighbours behind R.
 template <int D, bool kBf16, bool kCache, int kTok>
-__global__ void __launch_bounds__(kThreads) fa2_rope_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) fa2_rope_kernel(const Params p) {
     constexpr int kItems = D / 16;   // of a row
     __shared__ float4 table[kTok][4][kItems];   // cos, sin of pairs 8c + 2k and 8c + 2k + 1 at [k][c]
     __shared__ int2 place[kTok];                // batch entry and token of it
