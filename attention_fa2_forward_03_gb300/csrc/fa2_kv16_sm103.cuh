@@ -40,10 +40,10 @@ namespace kv16 {
 using kv4::report;
 
 // Sites of the status word (page ids and lengths as for the 4-bit cache).
-enum Site : int { kSiteRows = 53, kSitePart = 54 };
+enum Site : int { kSiteRows = 53, kSitePart = 54, kSiteGuard = 55 };
 
 constexpr int kMaxCtas = 160;
-constexpr int kSchedWarp = 14;
+constexpr int kSchedWarp = 14, kGuardWarp = 15;
 // Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
 // for one, and every row block kStart more for its start and its end. A step of 24
 // decoding requests and 3 chunks up to 512 tokens, contexts up to 8192, takes 173 us
@@ -57,7 +57,7 @@ constexpr int kMinRun = 4;        // units of a run at least
 // epilogue the prompt takes 137 us instead of 136, with 184 and 88 210.
 constexpr uint32_t kRegSoft = 168, kRegOut = 120, kRegRest = 56;   // 2 x 168 + 120 + 56 = 512
 constexpr int kParts = 4;         // parts on their way from the scheduling warp
-constexpr int kPartUsers = 14;    // warps that read a part
+constexpr int kPartUsers = 15;    // warps that read a part
 constexpr int kJoinY = 4, kJoinThreads = 256;
 
 struct Begun {                    // the row block that begins in a CTA's run and ends behind it
@@ -119,8 +119,12 @@ struct Lay {
     static constexpr int kPartOff = kRowOff + 6 * kBM * 4;
     static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
     static constexpr int kFirstOff = kIdOff + 4 * 32 * 4;   // page ids of the first two tiles of a part [kParts][16]
-    static constexpr int kMiscOff = kFirstOff + kParts * 16 * 4;
-    static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+    // Of a part (modulo 8): whether a value that is not finite was taken out, and
+    // the position of the first one in each column [8][D].
+    static constexpr int kFlagOff = kFirstOff + kParts * 16 * 4;
+    static constexpr int kBadOff = kFlagOff + 8 * 4;
+    static constexpr int kMiscOff = kBadOff + 8 * D * 4;
+    static constexpr int kSmemBytes = kMiscOff + 32 + 1024;   // + TMEM address, abort flag, the guard's counters
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
@@ -590,6 +594,144 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
     __syncwarp();
 }
 
+// ---------------------------------------------------------------- guard
+
+// The guard and the softmax: a stream's first warp lets the guard go on to a tile
+// when it has seen the tile's scores, or of a pair the scores before (then the values' place in the ring holds no
+// older tile that could be taken for them), and waits for the guard before it hands
+// over the tile's first weights. Tiles are counted, those of all parts.
+struct Gate {
+    uint32_t at;   // in shared memory: go of each stream, done
+    __device__ __forceinline__ void init() const {
+        for (int i = 0; i < 3; ++i) asm volatile("st.shared.b32 [%0], 0;" ::"r"(at + 4 * i) : "memory");
+    }
+    __device__ __forceinline__ int read(int i) const {
+        int v;
+        asm volatile("ld.acquire.cta.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * i) : "memory");
+        return v;
+    }
+    __device__ __forceinline__ void set(int i, int v) const { asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(at + 4 * i), "r"(v) : "memory"); }
+    __device__ __forceinline__ void set_go(int t, int n) const { set(t, n); }
+    __device__ __forceinline__ void set_done(int n) const { set(2, n); }
+    template <typename Done>
+    __device__ __forceinline__ bool spin(const Waiter& w, Done done) const {
+        bool ok = true;
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (!done()) {
+            if (*w.abort_flag) ok = false;
+            if (static_cast<long long>(ptx::globaltimer_ns() - t0) > w.limit_ns) {
+                *w.abort_flag = 1;
+                atomicCAS(&g_fa2_status, 0, FA2_ERR_TIMEOUT | (kSiteGuard << 8));
+                ok = false;
+            }
+            if (!ok) break;
+        }
+        return __all_sync(~0u, ok);
+    }
+    __device__ __forceinline__ bool wait_go(int n, const Waiter& w) const { return spin(w, [&] { return max(read(0), read(1)) >= n; }); }
+    __device__ __forceinline__ bool wait_done(int n, const Waiter& w) const { return spin(w, [&] { return read(2) >= n; }); }
+};
+
+// A weight of 0 does not keep out a value that is not finite: 0 * NaN is NaN. So
+// the values of tiles that some row does not see whole are gone over before they
+// are used. What lies behind the request's end, of whoever had the page before,
+// becomes zeros. Values that are not finite behind the first row's last key
+// become zeros too, and the epilogue gives NaN to the rows that do see them.
+// Where all rows of a block see the same keys (one token, or no mask), only
+// the end is to be seen to, which the softmax does itself: it is there sooner.
+__device__ __forceinline__ bool rows_differ(const Params& p, const Part& x) { return p.causal && x.ntok > 1; }
+__device__ __forceinline__ int guarded_from(const Params& p, const Part& x) {   // first tile of the part that the guard goes over
+    return rows_differ(p, x) ? max(x.jmask0 - x.jb, 0) : x.n;
+}
+
+// sum + 0 * x for a pair.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t sum) {
+    uint32_t r;
+    if constexpr (kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    return r;
+}
+
+template <int D, bool kBf16, bool kSmall>
+__device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars, const Waiter& w, const Gate& gate) {
+    using L = Lay<D>;
+    using T = Tiles<D, kSmall>;
+    constexpr int S = L::kStages, kPieces = D / 8, kRows = 32 / kPieces;   // pieces of 16 bytes of a row, rows at a time
+    constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
+    const int lane = threadIdx.x & 31, piece = lane % kPieces;
+    int n_part = 0, ring = 0, seen = 0;   // seen: tiles
+    bool ok = true;
+    Part x;
+    while (next_part<D>(smem, bars, w, n_part, x, ok)) {
+        // Eight parts back the epilogue is done: part n + 4 is not handed out before it has taken part n.
+        volatile int* flag = reinterpret_cast<int*>(smem + L::kFlagOff) + (n_part & 7);
+        int* first_bad = reinterpret_cast<int*>(smem + L::kBadOff) + (n_part & 7) * D;
+        if (lane == 0) *flag = 0;
+        __syncwarp();
+        const int ring0 = ring;
+        ring += 2 * x.n;
+        for (int j = guarded_from(p, x); j < x.n; ++j) {
+            const int r = ring0 + value_entry(x.kind == kPair, x.n, j), at = (x.jb + j) * kBN;
+            ok = gate.wait_go(++seen, w);
+            ok = __all_sync(~0u, ok && w.wait(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull));
+            if (!ok) break;
+            const int valid = x.len - at;
+            const uint32_t tile = sbase + L::kRingOff + (r % S) * L::kTileBytes + (piece / 8) * T::kBlkBytes;
+            auto place = [&](int row) { return tile + T::row_bytes(row) + (((piece ^ row) & 7) << 4); };
+            for (int row = valid / kRows * kRows + lane / kPieces; row < kBN; row += kRows)
+                if (row >= valid) ptx::st_shared_v4(place(row), 0, 0, 0, 0);
+            __syncwarp();
+            // Rows that the first row sees are seen by all. 0 * x is a zero where x is finite.
+            const int low = max(x.vis0 - at, 0), high = min(valid, kBN);
+            uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 1
+            for (int row0 = low / (8 * kRows) * (8 * kRows); row0 < high; row0 += 8 * kRows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint4 v = ptx::ld_shared_v4(place(row0 + e * kRows + lane / kPieces));
+                    sum[0] = zero_times<kBf16>(v.x, sum[0]);
+                    sum[1] = zero_times<kBf16>(v.y, sum[1]);
+                    sum[2] = zero_times<kBf16>(v.z, sum[2]);
+                    sum[3] = zero_times<kBf16>(v.w, sum[3]);
+                }
+            }
+            if (__any_sync(~0u, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)) {
+                if (*flag == 0) {
+                    for (int c = lane; c < D; c += 32) first_bad[c] = 0x7FFFFFFF;
+                    __syncwarp();
+                    if (lane == 0) *flag = 1;
+                }
+                __syncwarp();
+                for (int row = low + lane / kPieces; row < high; row += kRows) {
+                    uint4 v = ptx::ld_shared_v4(place(row));
+                    uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // an exponent of all ones, and one more, carries into the sign's place
+                        const uint32_t bad = ((word[k] & kExp) + kOne) & 0x80008000u;
+                        if (bad & 0x8000u) {
+                            atomicMin(first_bad + piece * 8 + 2 * k, at + row);
+                            word[k] &= 0xFFFF0000u;
+                        }
+                        if (bad & 0x80000000u) {
+                            atomicMin(first_bad + piece * 8 + 2 * k + 1, at + row);
+                            word[k] &= 0xFFFFu;
+                        }
+                    }
+                    ptx::st_shared_v4(place(row), v.x, v.y, v.z, v.w);
+                }
+                __syncwarp();
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) gate.set_done(seen);
+        }
+        if (!ok) break;
+    }
+    __syncwarp();
+}
+
 // ---------------------------------------------------------------- MMA issuer
 
 template <int D, bool kBf16, bool kSmall>
@@ -727,11 +869,12 @@ __device__ __forceinline__ int stream_tokens(const Params& p, const Part& x, int
 __device__ __forceinline__ int by_group(int r, uint32_t inv) { return static_cast<int>((static_cast<uint32_t>(r) * inv) >> 16); }
 
 template <int D, bool kBf16, bool kSmall>
-__device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars,
-                                             const Waiter& w, int t) {
+__device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uint8_t* smem, const BarSet<D>& bars, const Waiter& w,
+                                             const Gate& gate, int t) {
     using L = Lay<D>;
     using T = Tiles<D, kSmall>;
     constexpr int S = L::kStages;
+    const uint32_t ring0 = ptx::smem_addr(smem + L::kRingOff);
     const int row = threadIdx.x & 127;          // row of the query tile = TMEM lane
     const uint32_t row_addr = tmem + (static_cast<uint32_t>(row & ~31) << 16);
     const uint32_t colS = Layout<D>::col_s(t);
@@ -743,47 +886,48 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
     const int tok = by_group(row, (65536u + p.group - 1) / p.group);   // the row's token in the tile
 
     uint32_t n_s = 0, n_item = 0;   // parities: steps, parts of the stream
-    int n_part = 0;
+    int n_part = 0, guarded = 0;    // guarded: tiles that the guard goes over, of the parts so far
     bool ok = true;
     Part x;
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
         const bool pair = x.kind == kPair;
-        const int steps = x.steps(t);
+        const int steps = x.steps(t), g0 = guarded_from(p, x);
+        guarded += max(x.n - g0, 0);
         if (steps == 0) continue;
         // The stream's step i is the part's tile i (pair) or 2 i + t (single).
         const int every = pair ? 1 : 2, from = x.jb + (pair ? 0 : t);
+        int tile = guarded - x.n + from - x.jb + 1;   // the step's, as the guard counts
         const bool live = (row & ~31) < stream_tokens(p, x, t) * p.group;   // of the warp: some row is a query's
         // Keys of the step's tile that the row sees, and the first step at which that may be fewer than all.
         int lim = min(x.len, x.vis0 + (p.causal ? tok + (pair ? t * p.tok_tile : 0) : 0)) - from * kBN;
         const int mask_from = (x.jmask(t) - from + every - 1) / every;
-        // The step in whose tile the request ends, if it has it; how many of the tile's keys there are, and its V.
+        const bool gated = rows_differ(p, x);
+        // Without a guard: the step in whose tile the request ends, if it has it; the tile's V, and how many keys it has.
         int tail_step = -1, tail = 0;
-        {
+        if (!gated && x.len % kBN != 0) {
             const int last = x.len / kBN - from;
-            if (x.len % kBN != 0 && last >= 0 && last % every == 0) {
+            if (last >= 0 && last % every == 0) {
                 tail_step = last / every;
-                tail = (x.ring + value_entry(pair, x.n, last + from - x.jb)) * 128 + x.len % kBN;
+                tail = (x.ring + value_entry(pair, x.n, last + from - x.jb)) * kBN + x.len % kBN;
             }
         }
         float m = -INFINITY;  // running row max of the scaled scores, log2 units
         float l = 0.0f;       // running sum of exp2(s*c - m)
-        for (int i = 0; i < steps; ++i, n_s ^= 1, lim -= every * kBN) {
+        for (int i = 0; i < steps; ++i, n_s ^= 1, lim -= every * kBN, tile += every) {
             ok = w.wait(bars.s_full(t), n_s, kSiteSFull);
             if (!__all_sync(~0u, ok)) {
                 ok = false;
                 break;
             }
-            if (i == tail_step) {
-                // What lies behind the request in its last page has weight 0, but may be anything, NaN too:
-                // those rows of V become zeros. (Two streams that share the tile write the same.)
-                const int r = tail / 128;
+            if (i == tail_step) {   // zeros behind the end; two streams that share the tile write the same
+                const int r = tail / kBN;
                 ok = w.wait(bars.kv_full(r % S), (r / S) & 1, kSiteKvFull);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
                 }
-                if (row >= tail % 128) {
-                    const uint32_t at = sbase + L::kRingOff + (r % S) * L::kTileBytes + T::row_bytes(row);
+                if (row >= tail % kBN) {
+                    const uint32_t at = ring0 + (r % S) * L::kTileBytes + T::row_bytes(row);
 #pragma unroll 4
                     for (int k = 0; k < D / 8; ++k)
                         ptx::st_shared_v4(at + (k / 8) * T::kBlkBytes + (((k ^ row) & 7) << 4), 0, 0, 0, 0);
@@ -806,6 +950,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             }
             ptx::tc_fence_after();
             const bool masked = i >= mask_from;   // some row does not see all of these keys
+            if (gated && row == 0) {
+                // A pair's scores of a tile are behind the values of the tile before the last: the next one's place is seen to.
+                if (pair && i + 1 >= mask_from && i + 1 < steps) gate.set_go(t, tile + 1);
+                else if (masked) gate.set_go(t, tile);
+            }
             // The last 64 scores are read for the maximum and, when the first 64
             // weights are done, once more: all 128 and the rest of the state do not
             // fit the registers.
@@ -866,6 +1015,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             ptx::tmem_wait_ld();
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
+            if (masked && gated && row < 32 && !(ok = gate.wait_done(tile, w))) break;
             warp_arrive(bars.p_full(t));
             if (masked) {
 #pragma unroll
@@ -921,11 +1071,8 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
     const int row = 32 * q + lane;
     const uint32_t row_addr = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const float* rowbuf = reinterpret_cast<const float*>(smem + L::kRowOff);  // alpha | m | l
-    int row_line;   // of the row in o, from its tile's first on
-    {
-        const int tk = by_group(row, (65536u + p.group - 1) / p.group);
-        row_line = tk * p.hq + (row - tk * p.group);
-    }
+    const int row_tok = by_group(row, (65536u + p.group - 1) / p.group);   // the row's token in its tile,
+    const int row_line = row_tok * p.hq + (row - row_tok * p.group);       // its line in o, from the tile's first on
     const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
 
     uint32_t n_s = 0, n_items = 0;   // a bit for each stream: steps, parts, modulo 2
@@ -1029,6 +1176,8 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 f[0] *= inv;
                 f[1] *= inv;
             }
+            // The guard was here before the products with the tiles that it goes over; else its flag may be an old one.
+            const bool bad = guarded_from(p, x) < x.n && reinterpret_cast<const volatile int*>(smem + L::kFlagOff)[n_part & 7] != 0;
             const bool whole = x.buffer < 0;
             const long long line = whole ? static_cast<long long>(x.q0 + (pair ? tile * p.tok_tile : 0)) * p.hq + x.h * p.group + row_line
                                          : static_cast<long long>(x.buffer) * p.part_rows + tile * kBM + row;
@@ -1054,6 +1203,13 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                 if (ll == 0.0f) {   // no key, whatever the values hold
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = 0;
+                }
+                if (bad) {   // values that are not finite
+                    const volatile int* first_bad = reinterpret_cast<const volatile int*>(smem + L::kBadOff) + (n_part & 7) * D + c;
+                    const int seen = x.vis0 + (p.causal ? row_tok + (pair ? tile * p.tok_tile : 0) : 0);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (seen > first_bad[k]) v[k] = 0x7FFFFFFFu;
                 }
                 if (row < rows) {
                     if (whole) {
@@ -1094,6 +1250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bars.base = sbase + L::kBarOff;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
+    const Gate gate{sbase + L::kMiscOff + 8};
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
 
@@ -1122,6 +1279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(bars.mma_done(), 1);
         *abort_flag = 0;
+        gate.init();
         ptx::fence_mbar_init();
     }
     if (warp == kLoadWarp && lane == 0) {
@@ -1141,7 +1299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<kRegSoft>();
-        softmax_role<D, kBf16, kSmall>(p, tmem, smem, sbase, bars, w, warp / 4);
+        softmax_role<D, kBf16, kSmall>(p, tmem, smem, bars, w, gate, warp / 4);
     } else if (warp < kLoadWarp) {
         ptx::setmaxnreg_dec<kRegOut>();
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
@@ -1150,6 +1308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) producer<D, kSmall>(&tmQ, &tmKV, p, smem, sbase, bars, w);
         else if (warp == kMmaWarp) mma_issuer<D, kBf16, kSmall>(p, smem, sbase, tmem, bars, w);
         else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
+        else guard<D, kBf16, kSmall>(p, smem, sbase, bars, w, gate);
     }
 
     ptx::tc_fence_before();

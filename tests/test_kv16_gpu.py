@@ -143,3 +143,59 @@ CASES = [
 def test_every_element(gpu_lib, reqs, Hq, Hkv, d, page, causal, dtype):
     s = Step(3 + len(reqs) + Hq + d, reqs, Hq, Hkv, d, page, dtype)
     s.check(*s.run(gpu_lib, causal), causal)
+
+
+def poison(s, b, pos, part, head, col, value):
+    s.cache[int(s.table[b, pos // s.page]), head, part, pos % s.page, col] = value
+
+
+@pytest.mark.parametrize("d,page,dtype,G,new,L", [
+    (128, 64, "bf16", 4, 70, 300), (128, 16, "fp16", 1, 300, 300), (64, 32, "bf16", 2, 200, 513), (128, 128, "bf16", 8, 5, 129),
+    (64, 16, "fp16", 4, 33, 40),
+])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_what_is_not_finite_reaches_only_rows_that_see_it(gpu_lib, d, page, dtype, G, new, L, value):
+    """Keys and values of some new tokens are not finite: rows that do not see
+    them by the mask keep every bit. Of the values, only the column is lost."""
+    fa2 = gpu_lib
+    reqs = [(1, 200), (new, L), (2, 9)]
+    for part in (0, 1):
+        s = Step(17 + d + new, reqs, 2 * G, 2, d, page, dtype)
+        o, lse = s.run(fa2)
+        at = [L - 1, L - new // 2, L - new + 1]   # the last new token's position, ...
+        for pos, col in zip(at, (5, d - 1, 5)):
+            poison(s, 1, pos, part, 1, col, value)
+        o2, lse2 = s.run(fa2)
+        rows = np.arange(s.starts[1], s.starts[1] + new)
+        seen = L - new + np.arange(new)           # the last position that a row sees
+        same = torch.ones(s.T, 2 * G, d, dtype=torch.bool)
+        if part:
+            for pos, col in zip(at, (5, d - 1, 5)):
+                same[rows[seen >= pos], G:, col] = False
+            assert torch.equal(lse2, lse)
+            assert not torch.isfinite(o2.cpu()[~same]).any()
+        else:
+            hit = seen >= min(at)
+            same[rows[hit], G:] = False
+            keep = torch.ones(s.T, 2 * G, dtype=torch.bool)
+            keep[rows[hit], G:] = False
+            assert torch.equal(lse2.cpu()[keep], lse.cpu()[keep])
+            # an infinite product with the row is no NaN where it is -inf: that key has no weight
+            if math.isnan(value):
+                assert lse2.cpu()[~keep].isnan().all() and o2.cpu()[~same].isnan().all()
+        assert torch.equal(o2.cpu()[same], o.cpu()[same])
+
+
+def test_rows_of_q_that_are_not_finite_stay_alone(gpu_lib):
+    fa2 = gpu_lib
+    s = Step(23, [(1, 300), (40, 200), (150, 150)], 8, 2, 128, 64, "bf16")
+    o, lse = s.run(fa2)
+    bad = [(0, 3), (20, 0), (100, 7), (s.starts[2] + 149, 4)]
+    for t, h in bad:
+        s.q[t, h, 17] = math.nan
+    o2, lse2 = s.run(fa2)
+    keep = torch.ones(s.T, 8, dtype=torch.bool)
+    for t, h in bad:
+        keep[t, h] = False
+    assert o2.cpu()[~keep].isnan().all() and lse2.cpu()[~keep].isnan().all()
+    assert torch.equal(o2.cpu()[keep], o.cpu()[keep]) and torch.equal(lse2.cpu()[keep], lse.cpu()[keep])
