@@ -236,3 +236,112 @@ def test_slots_outside_the_cache_are_reported(gpu_lib):
     assert fa2.fa2_check_status(torch.cuda.current_stream().cuda_stream) == fa2.FA2_ERR_BOUNDS
     assert (cache[1, 0, :, 15] == 1).all() and float(cache.float().sum()) == 128
     ok(fa2)
+
+
+# ------------------------------------------------------------------ as a training step uses them
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_attention_and_their_gradients(gpu_lib, inter):
+    """rope, fa2_fwd_ex, fa2_bwd and rope_bwd in turn, against the gradients of
+    the same function in 64 bits on the same projection's output."""
+    fa2 = gpu_lib
+    rng = np.random.default_rng(9)
+    B, Hq, Hkv, N, d = 2, 4, 2, 150, 64
+    x = torch.tensor(rng.standard_normal((B, N, Hq + 2 * Hkv, d))).to(torch.bfloat16).cuda()
+    dout = torch.tensor(rng.standard_normal((B, Hq, N, d))).to(torch.bfloat16).cuda()
+    pos, f = rng.integers(0, 3000, (3, B, N)), freqs(d)
+    axes = sections(d)
+    P, F, A = i32(pos), torch.tensor(f).cuda(), i32(axes)
+    y = x.transpose(1, 2)
+    v = y[:, Hq + Hkv:].contiguous()
+    q, k = fa2.fa2_rope(y[:, :Hq], y[:, Hq: Hq + Hkv], P, F, A, inter)
+    o, lse = fa2.fa2_fwd_ex(q, k, v, causal=True)
+    dq, dk, dv = fa2.fa2_bwd(q, k, v, o, lse, dout, causal=True)
+    dx = torch.zeros_like(x)
+    to = dx.transpose(1, 2)
+    fa2.fa2_rope_bwd(dq, dk, P, F, A, inter, dq=to[:, :Hq], dk=to[:, Hq: Hq + Hkv])
+    to[:, Hq + Hkv:] = dv
+    ok(fa2)
+    # 64 bits, by autograd on elementary operations
+    z = x.double().cpu().requires_grad_()
+    i = np.arange(d // 2)
+    ia, ib = (2 * i, 2 * i + 1) if inter else (i, i + d // 2)
+    angle = torch.tensor(pos[axes].transpose(1, 2, 0) * f.astype(np.float64))[:, :, None]
+    c, s = angle.cos(), angle.sin()
+
+    def turn(t):
+        out = torch.empty_like(t)
+        out[..., ia] = t[..., ia] * c - t[..., ib] * s
+        out[..., ib] = t[..., ib] * c + t[..., ia] * s
+        return out.transpose(1, 2)
+
+    qq, kk, vv = turn(z[:, :, :Hq]), turn(z[:, :, Hq: Hq + Hkv]), z[:, :, Hq + Hkv:].transpose(1, 2)
+    kk, vv = (t.repeat_interleave(Hq // Hkv, 1) for t in (kk, vv))
+    sc = (qq @ kk.transpose(2, 3)) * d ** -0.5
+    sc = sc.masked_fill(torch.ones(N, N, dtype=torch.bool).triu(1), -torch.inf)
+    (sc.softmax(-1) @ vv * dout.double().cpu()).sum().backward()
+    want = z.grad
+    err = (dx.double().cpu() - want).abs()
+    # q, k, o, weights, their gradients and the results are rounded to bf16, each half a step of a
+    # term no larger than the largest: eight of them
+    scale = want.abs().amax()
+    assert err.max() <= 8 * U["bf16"] * scale
+    assert err.pow(2).mean().sqrt() <= 2 * U["bf16"] * want.pow(2).mean().sqrt()
+
+
+def test_captured_rotation_and_its_gradient(gpu_lib):
+    fa2 = gpu_lib
+    rng = np.random.default_rng(10)
+    x = torch.tensor(rng.standard_normal((2, 6, 90, 128))).to(torch.float16).cuda()
+    pos, f = i32(rng.integers(0, 999, (2, 90))), torch.tensor(freqs(128)).cuda()
+    y, z, g = torch.empty_like(x), torch.empty_like(x), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        fa2.fa2_rope(x, None, pos, f, q_out=y)
+        fa2.fa2_rope_bwd(y, None, pos, f, dq=z)
+    for _ in range(3):
+        x.copy_(torch.randn(x.shape, device="cuda"))
+        pos.add_(17)
+        g.replay()
+        a, _ = fa2.fa2_rope(x, None, pos, f)
+        b, _ = fa2.fa2_rope_bwd(a, None, pos, f)
+        assert torch.equal(a, y) and torch.equal(b, z)
+    ok(fa2)
+
+
+def test_refusals(gpu_lib):
+    fa2 = gpu_lib
+    dev = "cuda"
+    q, k = torch.zeros(2, 4, 5, 64, dtype=torch.bfloat16, device=dev), torch.zeros(2, 2, 5, 64, dtype=torch.bfloat16, device=dev)
+    pos, f = torch.zeros(2, 5, dtype=torch.int32, device=dev), torch.zeros(32, device=dev)
+    good = [q, k, pos, f]
+    fa2.fa2_rope(*good)
+    bad = [(0, q.float()), (0, q[0]), (0, q.transpose(2, 3)), (0, torch.zeros(2, 4, 5, 96, dtype=torch.bfloat16, device=dev)),
+           (0, torch.zeros(2, 4, 5, 68, dtype=torch.bfloat16, device=dev)[..., :64]),
+           (0, torch.zeros(2, 4, 5, 72, dtype=torch.bfloat16, device=dev)[..., 4:68]), (0, q.cpu()), (1, k.half()), (1, k[:1]), (1, k[:, :, :4]),
+           (1, k.cpu()), (2, pos.long()), (2, pos[:, :4]), (2, pos.cpu()), (2, torch.zeros(9, 2, 5, dtype=torch.int32, device=dev)),
+           (3, f.double()), (3, f[:7]), (3, torch.zeros(40, device=dev)), (3, f[:0]), (3, f.cpu())]
+    for i, x in bad:
+        args = list(good)
+        args[i] = x
+        for call in (fa2.fa2_rope, fa2.fa2_rope_bwd):
+            with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
+                call(*args)
+    for kw in (dict(axes=torch.zeros(31, dtype=torch.int32, device=dev)), dict(axes=torch.zeros(32, device=dev)),
+               dict(q_out=torch.zeros(2, 4, 5, 64, device=dev)), dict(q_out=q[:, :3]), dict(k_out=q),
+               dict(q_out=torch.zeros(1, 4, 5, 64, dtype=torch.bfloat16, device=dev).expand(2, 4, 5, 64))):
+        with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
+            fa2.fa2_rope(*good, **kw)
+    with pytest.raises(ValueError):
+        fa2.fa2_rope(q, None, pos, f, k_out=k)
+    c = torch.zeros(fa2.fa2_kv16_cache_shape(2, 2, 16, 64), dtype=torch.bfloat16, device=dev)
+    t, slots = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=dev), i32([0, 1, 2])
+    for args, kw in (((t, t, slots.long(), c), {}), ((t, t.half(), slots, c), {}), ((t, t[:2], slots, c), {}), ((t, t, slots[:2], c), {}),
+                     ((t, t, slots, c[:, :1]), {}), ((t, t, slots, c.half()), {}), ((t[None], t[None], slots, c), {}),
+                     ((t, t, slots, c), dict(q=t)), ((t, t, slots, c), dict(inv_freq=f)), ((t, t, slots, c), dict(q_out=t)),
+                     ((t, t, slots, c), dict(positions=slots)), ((t, t, slots, c), dict(positions=slots[:2], inv_freq=f)),
+                     ((t, t, slots, c), dict(q=t[:2], positions=slots, inv_freq=f)),
+                     ((t, t, slots, c), dict(q=t, positions=slots, inv_freq=f, q_out=t.float()))):
+        with pytest.raises((ValueError, TypeError, fa2.FA2Error)):
+            fa2.fa2_kv16_append(*args, **kw)
+    ok(fa2)
