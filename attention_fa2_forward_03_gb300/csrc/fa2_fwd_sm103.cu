@@ -1365,9 +1365,9 @@ int fa2_set_tile_config(int config) {
 }
 
 #ifdef FA2_DEBUG
-const char* fa2_version(void) { return "fa2-sm103a 0.4.0 debug"; }
+const char* fa2_version(void) { return "fa2-sm103a 0.5.0 debug"; }
 #else
-const char* fa2_version(void) { return "fa2-sm103a 0.4.0"; }
+const char* fa2_version(void) { return "fa2-sm103a 0.5.0"; }
 #endif
 
 }  // extern "C"

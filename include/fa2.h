@@ -29,8 +29,8 @@
  * Every pointer must be 16-byte aligned. Outputs are fully overwritten.
  *
  * Execution. Calls are asynchronous on `stream` (0 = legacy default stream);
- * each forward call launches exactly one kernel, fa2_bwd three (in stream
- * order). The library allocates no memory per call;
+ * each forward call launches exactly one kernel, fa2_fwd_kv16 two and fa2_bwd
+ * three (in stream order). The library allocates no memory per call;
  * it owns one status word per device (a __device__ variable), which the
  * kernel sets if one of its bounded waits gives up.
  *
@@ -453,11 +453,12 @@ fa2_status fa2_kv16_append(const void* q, const void* k, const void* v, const in
  * Query heads that share a KV head: up to 128. Both products take 16-bit operands:
  * the softmax's weights are rounded to the cache's type (bf16 2^-8, fp16 2^-11);
  * scores, sums and partial results are fp32. What lies in a request's pages behind
- * its last token has no effect, whatever it is. A page that is skipped reads as
- * zeros.
- * T * H_q < 2^31, num_pages * H_kv < 2^30 - 1, and the blocks of two tiles of 128
- * query rows times H_kv times the tiles of 128 keys of a full table up to 2^30. Two
- * launches.
+ * its last token has no effect, whatever it is. A key or value that is not finite
+ * affects the rows that see it, a row of q that is not finite itself alone. A
+ * page that is skipped reads as zeros.
+ * T * H_q < 2^31, num_pages * H_kv < 2^30 - 1, and H_kv times the blocks of 256 query
+ * rows (T tokens fill 256 / (H_q / H_kv) of them each, one more a request) times
+ * (4 + 3 tiles of 128 keys of a full table) up to 2^30. Two launches.
  */
 fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
                         const int32_t* q_starts, const int32_t* q_lens, void* o, float* lse, void* workspace,
@@ -521,7 +522,7 @@ int fa2_set_debug_flags(int flags);
  */
 int fa2_set_tile_config(int config);
 
-/* Library version string, e.g. "fa2-sm103a 0.4.0" ("... debug" for the
+/* Library version string, e.g. "fa2-sm103a 0.5.0" ("... debug" for the
  * FA2_DEBUG build, libfa2_debug.so). */
 const char* fa2_version(void);
 
