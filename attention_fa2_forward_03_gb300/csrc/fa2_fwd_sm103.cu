@@ -65,7 +65,7 @@ constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
 // 4-bit cache 20-43, over the 16-bit cache 44-49.
-constexpr int kKernelSlots = 50;
+constexpr int kKernelSlots = 48;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
 // device at once store the same values.
@@ -1087,28 +1087,17 @@ fa2_status rope(const void* q, const void* k, void* q_out, void* k_out, const in
     return rope_launch<false>(dev, p, d, dtype == FA2_BF16, stream);
 }
 
-// Pages of 16 tokens with heads of 128 are loaded a whole page of keys or
-// values at a time (Tiles in fa2_kv16_sm103.cuh).
-constexpr bool kv16_small(int page_size, int d) { return page_size == 16 && d == 128; }
-
-// Pages of the 16-bit cache as matrices [page_size, d]: boxes of a page's 64
-// columns, or of all. A coordinate past the last one reads as zeros.
+// Pages of the 16-bit cache as matrices [page_size, d] in boxes of a whole one,
+// in the order of shared memory (Tiles in fa2_kv16_sm103.cuh): columns of a block, tokens of a group of
+// eight, blocks, groups. A coordinate past the last page reads as zeros.
 fa2_status kv16_encode_cache(CUtensorMap* m, const void* ptr, uint64_t mats, int page_size, int d) {
-    if (kv16_small(page_size, d)) {
-        cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(page_size), 2, mats};
-        cuuint64_t strides[3] = {256, 128, static_cast<cuuint64_t>(page_size) * 256};
-        cuuint32_t box[4] = {64, static_cast<cuuint32_t>(page_size), 2, 1};
-        cuuint32_t es[4] = {1, 1, 1, 1};
-        CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(ptr), dims, strides, box, es,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
-    }
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size), mats};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(page_size) * d * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(page_size), 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+    const cuuint32_t blocks = static_cast<cuuint32_t>(d / 64), groups = static_cast<cuuint32_t>(page_size / 8);
+    cuuint64_t dims[5] = {64, 8, blocks, groups, mats};
+    cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(page_size) * row};
+    cuuint32_t box[5] = {64, 8, blocks, groups, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void*>(ptr), dims, strides, box, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA2_OK : FA2_ERR_CUDA;
@@ -1153,12 +1142,12 @@ int kv16_ctas(int T, int B, int H_q, int H_kv, long long max_tokens, int most) {
     return static_cast<int>(std::min<long long>(most, (units + fa2::kv16::kMinRun - 1) / fa2::kv16::kMinRun));
 }
 
-template <int D, bool kBf16, bool kSmall = false>
+template <int D, bool kBf16>
 fa2_status kv16_launch(int dev, const CUtensorMap& mq, const CUtensorMap& mkv, const fa2::kv16::Params& p, cudaStream_t stream) {
     using namespace fa2::kv16;
     constexpr int kSmem = Lay<D>::kSmemBytes;
-    auto kern = fa2_kv16_fwd_kernel<D, kBf16, kSmall>;
-    const fa2_status st = set_smem(dev, 44 + (kSmall ? 4 : D == 128 ? 0 : 2) + (kBf16 ? 0 : 1), kern, kSmem);
+    auto kern = fa2_kv16_fwd_kernel<D, kBf16>;
+    const fa2_status st = set_smem(dev, 44 + (D == 128 ? 0 : 2) + (kBf16 ? 0 : 1), kern, kSmem);
     if (st != FA2_OK) return st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1309,8 +1298,6 @@ fa2_status fa2_fwd_kv16(const void* q, const void* cache, const int32_t* block_t
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
     p.wait_limit_ns = g_wait_limit_ns.load();
     const bool bf = dtype == FA2_BF16;
-    if (kv16_small(page_size, d))
-        return bf ? kv16_launch<128, true, true>(dev, mq, mkv, p, stream) : kv16_launch<128, false, true>(dev, mq, mkv, p, stream);
     if (d == 128) return bf ? kv16_launch<128, true>(dev, mq, mkv, p, stream) : kv16_launch<128, false>(dev, mq, mkv, p, stream);
     return bf ? kv16_launch<64, true>(dev, mq, mkv, p, stream) : kv16_launch<64, false>(dev, mq, mkv, p, stream);
 }

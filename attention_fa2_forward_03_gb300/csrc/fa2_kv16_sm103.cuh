@@ -138,32 +138,26 @@ struct BarSet : Bars<D> {
     __device__ uint32_t p_rest(int t) const { return this->base + 8 * (17 + 2 * S + 2 * kParts + t); }
 };
 
-// Where a tile's 128 keys lie in a place of the ring, and in which order they are
-// the columns of S and P. Pages of 32 tokens and more: in order, D / 64 blocks of
-// 64 columns one after another, each filled by a box of a page's rows. Pages of 16
-// (with two blocks): that takes 32 boxes for a tile of keys and values, about 100
-// cycles each whatever their size, which bounds the copies (64 requests of up to
-// 16384 tokens at 5.3 TB/s). There a box has both blocks of a page, which lie behind
-// one another, and the groups of eight rows that one product reads have to be a
-// constant distance apart: first come the pages' first eight tokens, then their
-// last eight.
-template <int D, bool kSmall>
+// Where a tile's 128 keys lie in a place of the ring: in order, groups of eight
+// (which the swizzle and the products' descriptors go by) behind one another, of a
+// group first the first 64 columns, then the others. So a page is one box of
+// [groups][D / 64][8][64] elements. (A box costs the copies about 100 cycles whatever
+// its size: with one for each 64 columns, 64 requests of up to 16384 tokens in pages of
+// 16 take 554 us, 472 so.)
+template <int D>
 struct Tiles {
-    static_assert(!kSmall || D == 128, "pages of 16 with two blocks");
-    static constexpr int kBlkBytes = kSmall ? 2048 : Layout<D>::kBlkBytes;   // from a block to the next
-    static constexpr int kGroupBytes = kSmall ? 4096 : 1024;                 // from a product's eight keys to the next
-    static constexpr int kHalfBytes = kSmall ? 1024 : 8192;                  // from the first 64 columns' keys to the others'
-    // Key of column c, and the place of key r's row in its block.
-    static __host__ __device__ constexpr int key_of(int c) { return kSmall ? c % 64 / 8 * 16 + c / 64 * 8 + c % 8 : c; }
-    static __device__ __forceinline__ int row_bytes(int r) { return kSmall ? (r >> 4) * 4096 + (r & 15) * 128 : r * 128; }
+    static constexpr int kBlkBytes = 1024;                  // from a block of 64 columns to the next
+    static constexpr int kGroupBytes = D / 64 * kBlkBytes;  // from a group of eight keys to the next
+    static constexpr int kHalfBytes = 8 * kGroupBytes;      // from the first 64 keys to the others
+    static __device__ __forceinline__ int row_bytes(int r) { return (r >> 3) * kGroupBytes + (r & 7) * 128; }
 };
 
-// 4-D tiled copy global -> shared.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int u, uint32_t bar) {
+// 5-D tiled copy global -> shared.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int x, int y, int z, int u, int v, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
         : "memory");
 }
 
@@ -517,17 +511,17 @@ struct Queries {
     }
 };
 
-// A box for each page's 64 columns (kSmall: for each page), each by a lane of its own.
-template <int D, bool kSmall>
+// A box for each page, each by a lane of its own.
+template <int D>
 __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const Params& p, uint8_t* smem,
                                          uint32_t sbase, const BarSet<D>& bars, const Waiter& w) {
     using L = Lay<D>;
-    constexpr int S = L::kStages, kBlks = kSmall ? 1 : D / 64;
+    constexpr int S = L::kStages;
     const int lane = threadIdx.x & 31;
     const int pages = kBN >> p.log2_page;          // of a tile
-    const int page_at = lane / kBlks, blk = lane % kBlks;
+    const int page_at = lane;
     const bool loads = page_at < pages;
-    const uint32_t box = kSmall ? page_at * 4096 : blk * L::kBlkBytes + page_at * (p.page * 128);
+    const uint32_t box = page_at * (p.page * D * 2);
     int* ids = reinterpret_cast<int*>(smem + L::kIdOff) + lane;   // of the lane's page, tile modulo 4
     const int nothing = p.num_pages * p.hkv * 2;   // past the tensor: a box of zeros
     int ring = 0, n_part = 0;
@@ -572,10 +566,7 @@ __device__ __forceinline__ void producer(const CUtensorMap* tmQ, const CUtensorM
             if (lane == 0) ptx::mbar_arrive_expect_tx(bars.kv_full(s), L::kTileBytes);
             __syncwarp();
             const uint32_t dst = sbase + L::kRingOff + s * L::kTileBytes + box;
-            if (loads) {
-                if constexpr (kSmall) tma_load_4d(dst, tmKV, 0, 0, 0, z, bars.kv_full(s));
-                else ptx::tma_load_3d(dst, tmKV, blk * 64, 0, z, bars.kv_full(s));
-            }
+            if (loads) tma_load_5d(dst, tmKV, 0, 0, 0, 0, z, bars.kv_full(s));
             ++ring;
         };
         // Query tiles whose places are free go before the keys, whose page ids are
@@ -655,10 +646,10 @@ __device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t sum) {
     return r;
 }
 
-template <int D, bool kBf16, bool kSmall>
+template <int D, bool kBf16>
 __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t sbase, const BarSet<D>& bars, const Waiter& w, const Gate& gate) {
     using L = Lay<D>;
-    using T = Tiles<D, kSmall>;
+    using T = Tiles<D>;
     constexpr int S = L::kStages, kPieces = D / 8, kRows = 32 / kPieces;   // pieces of 16 bytes of a row, rows at a time
     constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
     const int lane = threadIdx.x & 31, piece = lane % kPieces;
@@ -736,14 +727,14 @@ __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t s
 
 // ---------------------------------------------------------------- MMA issuer
 
-template <int D, bool kBf16, bool kSmall>
+template <int D, bool kBf16>
 __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint32_t sbase, uint32_t tmem, const BarSet<D>& bars,
                                            const Waiter& w) {
     using L = Lay<D>;
     constexpr int S = L::kStages;
     constexpr uint32_t kAB = kBf16 ? 1u : 0u;
-    using T = Tiles<D, kSmall>;
-    constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kSmall ? kBN / 2 : kBN);
+    using T = Tiles<D>;
+    constexpr uint32_t kIdS = ptx::idesc_f16(kAB, 0, 0, kBM, kBN);
     constexpr uint32_t kIdO = ptx::idesc_f16(kAB, 0, 1, kBM, D);
     // Descriptors of the ring's first place as keys and as values, and of the
     // query tiles' first; others lie kTileBytes / 16 further on.
@@ -752,16 +743,12 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
                    values = ptx::desc_sw128(sbase + L::kRingOff, T::kBlkBytes, T::kGroupBytes),
                    query = ptx::desc_sw128(sbase + L::kQOff, 16, 1024);
     auto wait_u = [&](uint32_t bar, uint32_t parity, int site) { return __all_sync(~0u, w.wait(bar, parity, site)); };
+    constexpr uint32_t kQ = L::kBlkBytes >> 4, kK = T::kBlkBytes >> 4;   // from 64 columns to the next
     auto issue_qk = [&](int t, uint64_t qd, uint64_t kd) {
-        if constexpr (kSmall) {
-            constexpr uint32_t kQ = L::kBlkBytes >> 4, kK = T::kBlkBytes >> 4;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h)
-                ptx::mma_ss_kloop<2, 4, 6, kQ, kQ + 2, kQ + 4, kQ + 6, 2, 4, 6, kK, kK + 2, kK + 4, kK + 6, 8>(
-                    tmem + Layout<D>::col_s(t) + 64 * h, qd, kd + h * (T::kHalfBytes >> 4), kIdS, 0u);
-        } else {
-            qk_kloop<D>(tmem + Layout<D>::col_s(t), qd, kd, kIdS);
-        }
+        if constexpr (D == 128)
+            ptx::mma_ss_kloop<2, 4, 6, kQ, kQ + 2, kQ + 4, kQ + 6, 2, 4, 6, kK, kK + 2, kK + 4, kK + 6, 8>(tmem + Layout<D>::col_s(t), qd, kd, kIdS, 0u);
+        else
+            ptx::mma_ss_kloop<2, 4, 6, 0, 0, 0, 0, 2, 4, 6, 0, 0, 0, 0, 4>(tmem + Layout<D>::col_s(t), qd, kd, kIdS, 0u);
         ptx::tc_commit_elect(bars.s_full(t));
     };
     // P V of a tile whose p_full has completed: its halves as their weights are there.
@@ -778,13 +765,9 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
     // rest. (For two, whose products are waited for, these are slower: a chunk of 2048
     // tokens over 32768 takes 785 us instead of 705.)
     auto issue_qk_single = [&](int t, uint64_t qd, uint64_t kd) {
-        constexpr uint32_t kQ = L::kBlkBytes >> 4, kK = T::kBlkBytes >> 4;
 #pragma unroll 1
-        for (int h = 0; h < (kSmall ? 2 : 1) * (D / 64); ++h) {
-            const int blk = h % (D / 64), half = h / (D / 64);
-            ptx::mma_ss_kloop<2, 4, 6, 0, 0, 0, 0, 2, 4, 6, 0, 0, 0, 0, 4>(
-                tmem + Layout<D>::col_s(t) + 64 * half, qd + blk * kQ, kd + blk * kK + half * (T::kHalfBytes >> 4), kIdS, blk);
-        }
+        for (int blk = 0; blk < D / 64; ++blk)
+            ptx::mma_ss_kloop<2, 4, 6, 0, 0, 0, 0, 2, 4, 6, 0, 0, 0, 0, 4>(tmem + Layout<D>::col_s(t), qd + blk * kQ, kd + blk * kK, kIdS, blk);
         ptx::tc_commit_elect(bars.s_full(t));
     };
     auto issue_pv_single = [&](int t, uint64_t vd, bool acc, uint32_t parity) {
@@ -894,11 +877,11 @@ __device__ __forceinline__ int stream_tokens(const Params& p, const Part& x, int
 // group / 2^16 of a quotient, so r / group by less than 1 / group.
 __device__ __forceinline__ int by_group(int r, uint32_t inv) { return static_cast<int>((static_cast<uint32_t>(r) * inv) >> 16); }
 
-template <int D, bool kBf16, bool kSmall>
+template <int D, bool kBf16>
 __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uint8_t* smem, const BarSet<D>& bars, const Waiter& w,
                                              const Gate& gate, int t) {
     using L = Lay<D>;
-    using T = Tiles<D, kSmall>;
+    using T = Tiles<D>;
     constexpr int S = L::kStages;
     const uint32_t ring0 = ptx::smem_addr(smem + L::kRingOff);
     const int row = threadIdx.x & 127;          // row of the query tile = TMEM lane
@@ -999,11 +982,11 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
                     for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < kBN / 2; k += 2) {
-                        s[k] = T::key_of(k) < lim ? s[k] : 0xFF800000u;
-                        s[k + 1] = T::key_of(k + 1) < lim ? s[k + 1] : 0xFF800000u;
+                        s[k] = k < lim ? s[k] : 0xFF800000u;
+                        s[k + 1] = k + 1 < lim ? s[k + 1] : 0xFF800000u;
                         mq[k / 2 % 2] = ptx::max3(mq[k / 2 % 2], __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
-                        mq[2 + k / 2 % 2] = ptx::max3(mq[2 + k / 2 % 2], T::key_of(k + 64) < lim ? __uint_as_float(s2[k]) : -INFINITY,
-                                                      T::key_of(k + 65) < lim ? __uint_as_float(s2[k + 1]) : -INFINITY);
+                        mq[2 + k / 2 % 2] = ptx::max3(mq[2 + k / 2 % 2], k + 64 < lim ? __uint_as_float(s2[k]) : -INFINITY,
+                                                      k + 65 < lim ? __uint_as_float(s2[k + 1]) : -INFINITY);
                     }
                 }
                 m_tile = fmaxf(ptx::max3(mq[0], mq[1], mq[2]), mq[3]) * c;
@@ -1045,7 +1028,7 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             warp_arrive(bars.p_full(t));
             if (masked) {
 #pragma unroll
-                for (int k = 0; k < kBN / 2; ++k) s2[k] = T::key_of(k + 64) < lim ? s2[k] : 0xFF800000u;
+                for (int k = 0; k < kBN / 2; ++k) s2[k] = k + 64 < lim ? s2[k] : 0xFF800000u;
             }
             weights(s2, pk, 0);
             weights(s2, pk, 32);
@@ -1265,7 +1248,7 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
 
 // ---------------------------------------------------------------- kernels
 
-template <int D, bool kBf16, bool kSmall>
+template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     fa2_kv16_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKV, const Params p) {
     using L = Lay<D>;
@@ -1325,16 +1308,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<kRegSoft>();
-        softmax_role<D, kBf16, kSmall>(p, tmem, smem, bars, w, gate, warp / 4);
+        softmax_role<D, kBf16>(p, tmem, smem, bars, w, gate, warp / 4);
     } else if (warp < kLoadWarp) {
         ptx::setmaxnreg_dec<kRegOut>();
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
     } else {
         ptx::setmaxnreg_dec<kRegRest>();
-        if (warp == kLoadWarp) producer<D, kSmall>(&tmQ, &tmKV, p, smem, sbase, bars, w);
-        else if (warp == kMmaWarp) mma_issuer<D, kBf16, kSmall>(p, smem, sbase, tmem, bars, w);
+        if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
+        else if (warp == kMmaWarp) mma_issuer<D, kBf16>(p, smem, sbase, tmem, bars, w);
         else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
-        else guard<D, kBf16, kSmall>(p, smem, sbase, bars, w, gate);
+        else guard<D, kBf16>(p, smem, sbase, bars, w, gate);
     }
 
     ptx::tc_fence_before();
