@@ -47,16 +47,18 @@ constexpr int kMaxCtas = 160;
 constexpr int kSchedWarp = 14, kGuardWarp = 15;
 // Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
 // for one, and every row block kStart more for its start and its end. A step of 24
-// decoding requests and 3 chunks up to 512 tokens, contexts up to 8192, takes 173 us
-// (224 with pages of 16); with 4, 3 and 5 units 177 (235), with 2, 1 and 2 179 (257). A
-// prompt of 4096 tokens, whose row blocks are of all lengths, takes 138 us; 144 with
-// kStart = 2, and with 8 the step with pages of 16 takes 228.
+// decoding requests and 3 chunks up to 512 tokens, contexts up to 8192, takes 167 us
+// (218 with pages of 16); with 4, 3 and 5 units 174 (215), with 2, 1 and 2 175 (259). A
+// prompt of 4096 tokens, whose row blocks are of all lengths, takes 139 us; 146 with
+// kStart = 2, 136 with 8, which costs two such prompts with heads of 64 189 us instead of 185.
 constexpr int kPairUnits = 3, kSingleUnits = 2, kStart = 4;
 constexpr int kMinRun = 4;        // units of a run at least
 // Registers a thread. What spills is waited for as long as keys are: the cache
 // that shared memory leaves is small. With 176 and 104 for the softmax and the
-// epilogue the prompt takes 137 us instead of 136, with 184 and 88 210.
-constexpr uint32_t kRegSoft = 168, kRegOut = 120, kRegRest = 56;   // 2 x 168 + 120 + 56 = 512
+// epilogue the prompt takes 142 us instead of 139, with 184 and 88 150.
+constexpr uint32_t kRegSoft = 168, kRegOut = 120, kRegRest = 56;
+static_assert(2 * kRegSoft + kRegOut + kRegRest == 65536 / 128 && kRegSoft >= 128 && kRegOut <= 128 && kRegRest <= 128,
+              "shares of the 128 registers a thread that the launch has");
 constexpr int kParts = 4;         // parts on their way from the scheduling warp
 constexpr int kPartUsers = 15;    // warps that read a part
 constexpr int kJoinY = 4, kJoinThreads = 256;
