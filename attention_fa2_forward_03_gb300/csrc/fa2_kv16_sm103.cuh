@@ -1308,6 +1308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     const Waiter w{abort_flag, p.wait_limit_ns};
 
+    // The roles' loops share an instruction cache that their program does not fit, so their
+    // order counts: a prompt of 4096 tokens takes 139 us in this one, 142 to 175 in others.
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<kRegSoft>();
         softmax_role<D, kBf16>(p, tmem, smem, bars, w, gate, warp / 4);

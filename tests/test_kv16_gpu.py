@@ -219,6 +219,28 @@ def test_long_contexts_are_split_and_joined(gpu_lib, d, page, dtype, reqs, Hq, H
     s.check(*s.run(gpu_lib))
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+def test_page_size_makes_no_difference(gpu_lib, d, dtype):
+    """The same tokens in pages of every size, tables of the same number of
+    tokens: every bit is the same."""
+    fa2 = gpu_lib
+    s = Step(57 + d, [(1, 700), (150, 600), (33, 257), (1, 16)], 8, 2, d, 128, dtype)
+    first = None
+    for page in (128, 64, 32, 16):
+        each = 128 // page
+        args = s.args()
+        P, Hkv = s.cache.shape[:2]
+        args[1] = args[1].view(P, Hkv, 2, each, page, d).permute(0, 3, 1, 2, 4, 5).reshape(P * each, Hkv, 2, page, d).contiguous()
+        args[2] = i32(np.where(s.table[:, :, None] < 0, -1, s.table[:, :, None] * each + np.arange(each)).reshape(len(s.reqs), -1))
+        used = s.T - 3   # rows that belong to a request
+        o, lse = fa2.fa2_fwd_kv16(*args, scale=s.scale, causal=True)
+        ok(fa2)
+        got = o[:used].cpu(), lse[:used].cpu()
+        if first is None:
+            first = got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
 def test_sharp_scores(gpu_lib):
     s = Step(5, [(1, 900), (70, 411)], 8, 2, 128, 64, "bf16", amp=8.0)
     s.check(*s.run(gpu_lib))
