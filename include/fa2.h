@@ -363,8 +363,9 @@ int64_t fa2_fwd_kv4_workspace(int B, int H_q, int H_kv, int N_q, int d, int max_
  * rot_dim / 2 pairs: pair i is elements i and i + rot_dim / 2, or 2i and 2i + 1
  * with interleaved = 1. Its angle is positions[axes[i]][b, n] * inv_freq[i], and
  *     y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
- * in fp32, rounded once; elements behind rot_dim are copied. Angles are exact
- * in a turn to 2^-32 of it for every position, far ones too.
+ * in fp32, rounded once; elements behind rot_dim are copied. Angles are formed
+ * exactly to 2^-32 of a turn for every position, far ones too (inv_freq up to 1),
+ * and taken within a turn as fp32.
  *   q, q_out : [B, H_q, N, d] bf16 or fp16; k, k_out : [B, H_kv, N, d], or both
  *              NULL with H_kv = 0. Elements of a row adjacent
  *   strides  : 12 numbers in host memory, read during the call: the strides of
