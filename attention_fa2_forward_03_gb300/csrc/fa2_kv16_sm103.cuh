@@ -123,10 +123,11 @@ struct Lay {
     static constexpr int kIdOff = kPartOff + kParts * static_cast<int>(sizeof(Part));   // page ids [4][32]
     static constexpr int kFirstOff = kIdOff + 4 * 32 * 4;   // page ids of the first two tiles of a part [kParts][16]
     // Of a part (modulo 8): whether a value that is not finite was taken out, and
-    // the position of the first one in each column [8][D].
+    // in each column the positions of the first +inf and of the first -inf [8][2][D] (a
+    // NaN counts as both).
     static constexpr int kFlagOff = kFirstOff + kParts * 16 * 4;
     static constexpr int kBadOff = kFlagOff + 8 * 4;
-    static constexpr int kMiscOff = kBadOff + 8 * D * 4;
+    static constexpr int kMiscOff = kBadOff + 8 * 2 * D * 4;
     static constexpr int kSmemBytes = kMiscOff + 32 + 1024;   // + TMEM address, abort flag, the guard's counters
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -631,7 +632,8 @@ struct Gate {
 // the values of tiles that some row does not see whole are gone over before they
 // are used. What lies behind the request's end, of whoever had the page before,
 // becomes zeros. Values that are not finite behind the first row's last key
-// become zeros too, and the epilogue gives NaN to the rows that do see them.
+// become zeros too, and the epilogue adds them to the rows that do see them: an
+// infinity whatever its weight, +inf and -inf for a NaN.
 // Where all rows of a block see the same keys (one token, or no mask), only
 // the end is to be seen to, which the softmax does itself: it is there sooner.
 __device__ __forceinline__ bool rows_differ(const Params& p, const Part& x) { return p.causal && x.ntok > 1; }
@@ -653,7 +655,7 @@ __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t s
     using L = Lay<D>;
     using T = Tiles<D>;
     constexpr int S = L::kStages, kPieces = D / 8, kRows = 32 / kPieces;   // pieces of 16 bytes of a row, rows at a time
-    constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
+    constexpr uint32_t kInf = kBf16 ? 0x7F80u : 0x7C00u;
     const int lane = threadIdx.x & 31, piece = lane % kPieces;
     int n_part = 0, ring = 0, seen = 0;   // seen: tiles
     bool ok = true;
@@ -661,7 +663,7 @@ __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t s
     while (next_part<D>(smem, bars, w, n_part, x, ok)) {
         // Eight parts back the epilogue is done: part n + 4 is not handed out before it has taken part n.
         volatile int* flag = reinterpret_cast<int*>(smem + L::kFlagOff) + (n_part & 7);
-        int* first_bad = reinterpret_cast<int*>(smem + L::kBadOff) + (n_part & 7) * D;
+        int* first_bad = reinterpret_cast<int*>(smem + L::kBadOff) + (n_part & 7) * (2 * D);
         if (lane == 0) *flag = 0;
         __syncwarp();
         const int ring0 = ring;
@@ -693,7 +695,7 @@ __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t s
             }
             if (__any_sync(~0u, ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7FFF7FFFu) != 0)) {
                 if (*flag == 0) {
-                    for (int c = lane; c < D; c += 32) first_bad[c] = 0x7FFFFFFF;
+                    for (int c = lane; c < 2 * D; c += 32) first_bad[c] = 0x7FFFFFFF;
                     __syncwarp();
                     if (lane == 0) *flag = 1;
                 }
@@ -701,17 +703,18 @@ __device__ __forceinline__ void guard(const Params& p, uint8_t* smem, uint32_t s
                 for (int row = low + lane / kPieces; row < high; row += kRows) {
                     uint4 v = ptx::ld_shared_v4(place(row));
                     uint32_t* word = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // an exponent of all ones, and one more, carries into the sign's place
-                        const uint32_t bad = ((word[k] & kExp) + kOne) & 0x80008000u;
-                        if (bad & 0x8000u) {
-                            atomicMin(first_bad + piece * 8 + 2 * k, at + row);
-                            word[k] &= 0xFFFF0000u;
-                        }
-                        if (bad & 0x80000000u) {
-                            atomicMin(first_bad + piece * 8 + 2 * k + 1, at + row);
-                            word[k] &= 0xFFFFu;
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t y = word[k] & 0xFFFFu;
+                            if ((y & kInf) == kInf) {
+                                int* first = first_bad + piece * 8 + 2 * k + half;
+                                if (y != (kInf | 0x8000u)) atomicMin(first, at + row);
+                                if (y != kInf) atomicMin(first + D, at + row);
+                                y = 0;
+                            }
+                            word[k] = word[k] >> 16 | y << 16;
                         }
                     }
                     ptx::st_shared_v4(place(row), v.x, v.y, v.z, v.w);
@@ -1215,13 +1218,6 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = 0;
                 }
-                if (bad) {   // values that are not finite
-                    const volatile int* first_bad = reinterpret_cast<const volatile int*>(smem + L::kBadOff) + (n_part & 7) * D + c;
-                    const int seen = x.vis0 + (p.causal ? row_tok + (pair ? tile * p.tok_tile : 0) : 0);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (seen > first_bad[k]) v[k] = 0x7FFFFFFFu;
-                }
                 if (row < rows) {
                     if (whole) {
 #pragma unroll
@@ -1238,6 +1234,25 @@ __device__ __forceinline__ void correction_role(const Params& p, uint32_t tmem, 
                     }
                 }
                 __syncwarp();
+            }
+            // Values that are not finite, added to what is written: rare, so a small loop.
+            if (bad && row < rows && ll != 0.0f) {
+                const volatile int* first_bad = reinterpret_cast<const volatile int*>(smem + L::kBadOff) + (n_part & 7) * (2 * D);
+                const int seen = x.vis0 + row_tok + (pair ? tile * p.tok_tile : 0);   // the guard is for causal rows only
+#pragma unroll 1
+                for (int c = 0; c < D; ++c) {
+                    const bool up = seen > first_bad[c], down = seen > first_bad[D + c];
+                    if (!up && !down) continue;
+                    const float add = up && down ? NAN : up ? INFINITY : -INFINITY;
+                    if (whole) {
+                        uint16_t* y = reinterpret_cast<uint16_t*>(to) + c;
+                        float y0, y1;
+                        ptx::unpack2<kBf16>(*y, y0, y1);
+                        *y = static_cast<uint16_t>(ptx::pack2<kBf16>(y0 + add, 0.0f));
+                    } else {
+                        reinterpret_cast<float*>(to)[c] += add;
+                    }
+                }
             }
             if (row < rows) {
                 if (whole) p.lse[line] = ll != 0.0f ? (mm + ptx::lg2_approx(ll)) * 0.69314718055994530942f : -INFINITY;
@@ -1309,7 +1324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter w{abort_flag, p.wait_limit_ns};
 
     // The roles' loops share an instruction cache that their program does not fit, so their
-    // order counts: a prompt of 4096 tokens takes 139 us in this one, 142 to 175 in others.
+    // order counts: a prompt of 4096 tokens takes 139 us in this one, two with heads of 64
+    // 185; 138 to 155 and 191 to 210 in seven others of the last four.
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<kRegSoft>();
         softmax_role<D, kBf16>(p, tmem, smem, bars, w, gate, warp / 4);
@@ -1318,9 +1334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         correction_role<D, kBf16>(p, tmem, smem, sbase, bars, w);
     } else {
         ptx::setmaxnreg_dec<kRegRest>();
-        if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
+        if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
+        else if (warp == kLoadWarp) producer<D>(&tmQ, &tmKV, p, smem, sbase, bars, w);
         else if (warp == kMmaWarp) mma_issuer<D, kBf16>(p, smem, sbase, tmem, bars, w);
-        else if (warp == kSchedWarp) scheduler<D>(p, smem, bars, w);
         else guard<D, kBf16>(p, smem, sbase, bars, w, gate);
     }
 

@@ -455,8 +455,11 @@ fa2_status fa2_kv16_append(const void* q, const void* k, const void* v, const in
  * the softmax's weights are rounded to the cache's type (bf16 2^-8, fp16 2^-11);
  * scores, sums and partial results are fp32. What lies in a request's pages behind
  * its last token has no effect, whatever it is. A key or value that is not finite
- * affects the rows that see it, a row of q that is not finite itself alone. A
- * page that is skipped reads as zeros.
+ * affects the rows that see it, a row of q that is not finite itself alone. An infinite
+ * value gives such a row that infinity, whatever the chunk (NaN with one of the
+ * other sign or a NaN beside it; and NaN may stand for an infinity whose weight
+ * rounds to zero). A row whose allowed scores are all -inf is as one without a
+ * key. A page that is skipped reads as zeros.
  * T * H_q < 2^31, num_pages * H_kv < 2^30 - 1, and H_kv times the blocks of 256 query
  * rows (T tokens fill 256 / (H_q / H_kv) of them each, one more a request) times
  * (4 + 3 tiles of 128 keys of a full table) up to 2^30. Two launches.
