@@ -64,7 +64,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 constexpr int kMaxDevices = 64;
 // Kernel slots: 16-bit forward 0-7, backward dK/dV 8-11, FP8 forward 12-13,
 // backward dQ 14-17, d = 64 equal-length forward 18-19, attention over the
-// 4-bit cache 20-43, over the 16-bit cache 44-49.
+// 4-bit cache 20-43, over the 16-bit cache 44-47.
 constexpr int kKernelSlots = 48;
 // Per-device facts, read without a lock: every field is an atomic written
 // with release and read with acquire, and two threads that probe the same
@@ -1147,7 +1147,9 @@ fa2_status kv16_launch(int dev, const CUtensorMap& mq, const CUtensorMap& mkv, c
     using namespace fa2::kv16;
     constexpr int kSmem = Lay<D>::kSmemBytes;
     auto kern = fa2_kv16_fwd_kernel<D, kBf16>;
-    const fa2_status st = set_smem(dev, 44 + (D == 128 ? 0 : 2) + (kBf16 ? 0 : 1), kern, kSmem);
+    constexpr int kSlot = 44 + (D == 128 ? 0 : 2) + (kBf16 ? 0 : 1);
+    static_assert(kSlot < kKernelSlots, "a slot behind the array");
+    const fa2_status st = set_smem(dev, kSlot, kern, kSmem);
     if (st != FA2_OK) return st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
