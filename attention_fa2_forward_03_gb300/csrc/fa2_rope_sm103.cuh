@@ -27,7 +27,7 @@
 namespace fa2 {
 namespace rope {
 
-constexpr int kSiteAxis = 52;   // an entry of `axes` outside 0 .. n_axes - 1
+constexpr int kSiteAxis = 56;   // an entry of `axes` outside 0 .. n_axes - 1
 constexpr int kThreads = 256;
 // Tokens of a block where there are many, items (32 bytes) of a thread in flight
 // and blocks an SM. 8191 tokens of 48 heads take 38.9 us; 45.1 with 8, 4 and 3
