@@ -216,27 +216,19 @@ __device__ __forceinline__ Request request(const Params& p, int b) { return requ
 
 __device__ __forceinline__ int tiles_in(int keys) { return keys <= 0 ? 0 : (keys + kBN - 1) / kBN; }
 
-// The sum of floor((a i + b) / m) over i < n, by Euclid's algorithm on (a, m).
-__device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-    unsigned sum = 0;
-    while (n > 0) {
-        if (a >= m) {
-            sum += n * (n - 1) / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
-        }
-        const unsigned y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const unsigned t = m;
-        m = a;
-        a = t;
-    }
-    return sum;
+// Tiles of keys of n row blocks, where the first sees `keys` keys (1 or more) and each
+// next one `step` more (even, up to 256). A block of x keys has (x + r) / kBN tiles with r = -x
+// mod kBN, the places of its last tile that it leaves empty, so the sum is that of the
+// keys (an arithmetic series) and of the r. These repeat: with g, the largest
+// power of two in step and kBN, a period is kBN / g blocks, and its r are e, e + g, ..
+// (e below g), kBN (period - 1) / 2 + period e together.
+__device__ __forceinline__ int tiles_of_blocks(int n, int keys, int step) {
+    const int g = min(step & -step, kBN), e = -keys & (g - 1);
+    const int periods = n >> __popc(kBN / g - 1), whole = periods * (kBN / g);
+    long long sum = static_cast<long long>(n) * keys + static_cast<long long>(n) * (n - 1) / 2 * step;
+    sum += static_cast<long long>(whole) * e + static_cast<long long>(whole - periods) * (kBN / 2);
+    for (int i = whole, r = -keys & (kBN - 1); i < n; ++i, r = (r - step) & (kBN - 1)) sum += r;
+    return static_cast<int>(sum / kBN);
 }
 
 // The first row block in which some row sees a key (len > 0).
@@ -256,7 +248,7 @@ __device__ __forceinline__ int units_before(const Params& p, const Request& r, i
     if (full > k0) {
         int tiles = (full - k0) * tiles_in(r.len);
         // block k's last row sees len - n + (k + 1) step keys
-        if (p.causal) tiles = floor_sum(full - k0, kBN, step, static_cast<unsigned>(r.len - r.n + (k0 + 1) * step) + kBN - 1);
+        if (p.causal) tiles = tiles_of_blocks(full - k0, r.len - r.n + (k0 + 1) * step, step);
         sum = (full - k0) * kStart + kPairUnits * tiles;
     }
     if (x >= r.blocks) sum += block_units(tiles_in(r.len), weight(p, r.n - (r.blocks - 1) * step));   // its last row sees every key
