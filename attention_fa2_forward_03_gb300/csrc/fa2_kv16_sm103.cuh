@@ -46,16 +46,18 @@ enum Site : int { kSiteRows = 53, kSitePart = 54, kSiteGuard = 55 };
 constexpr int kMaxCtas = 160;
 constexpr int kSchedWarp = 14, kGuardWarp = 15;
 // Units. A tile of keys counts kPairUnits for two query tiles and kSingleUnits
-// for one, and every row block kStart more for its start and its end. A step of 24
-// decoding requests and 3 chunks up to 512 tokens, contexts up to 8192, takes 167 us
-// (218 with pages of 16); with 4, 3 and 5 units 174 (215), with 2, 1 and 2 175 (259). A
-// prompt of 4096 tokens, whose row blocks are of all lengths, takes 139 us; 146 with
-// kStart = 2, 136 with 8, which costs two such prompts with heads of 64 189 us instead of 185.
+// for one, and every row block kStart more for its start and its end. Single calls with
+// caches cold (32 / 8 heads of 128): a step of 24 decoding requests and 3 chunks up to 512
+// tokens, contexts up to 8192, takes 166 us (218 with pages of 16); with 4, 3 and 5 units
+// 172 (214), with 2, 1 and 2 173 (253). A prompt of 4096 tokens, whose row blocks are of
+// all lengths, takes 136 us; 144 with kStart = 2, 134 with 8, which costs two such prompts
+// with 32 / 32 heads of 64 190 us instead of 187.
 constexpr int kPairUnits = 3, kSingleUnits = 2, kStart = 4;
 constexpr int kMinRun = 4;        // units of a run at least
 // Registers a thread. What spills is waited for as long as keys are: the cache
 // that shared memory leaves is small. With 176 and 104 for the softmax and the
-// epilogue the prompt takes 142 us instead of 139, with 184 and 88 150.
+// epilogue the prompt takes 140 us instead of 136, with 184 and 88 141, and a chunk of 2048
+// tokens over 32768 713 and 718 instead of 704.
 constexpr uint32_t kRegSoft = 168, kRegOut = 120, kRegRest = 56;
 static_assert(2 * kRegSoft + kRegOut + kRegRest == 65536 / 128 && kRegSoft >= 128 && kRegOut <= 128 && kRegRest <= 128,
               "shares of the 128 registers a thread that the launch has");
@@ -760,7 +762,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, uint8_t* smem, uint3
     // The same in loops of four products, for one query tile, where copies bound the
     // time: what is executed now and then has to fit the instruction cache beside the
     // rest. (For two, whose products are waited for, these are slower: a chunk of 2048
-    // tokens over 32768 takes 785 us instead of 705.)
+    // tokens over 32768 takes 782 us instead of 704.)
     auto issue_qk_single = [&](int t, uint64_t qd, uint64_t kd) {
 #pragma unroll 1
         for (int blk = 0; blk < D / 64; ++blk)
@@ -1000,6 +1002,9 @@ __device__ __forceinline__ void softmax_role(const Params& p, uint32_t tmem, uin
             const float m_use = m == -INFINITY ? 0.0f : m;
             const uint64_t nm2 = ptx::f2_pack(-m_use, -m_use);
             uint64_t acc[4] = {0, 0, 0, 0};
+            // The products take 16-bit operands, so a weight is rounded to the cache's type, half a step
+            // of it (bf16 2^-8, fp16 2^-11): O is off by 0.0021 to 0.0023 in bf16, with fp32 weights by
+            // 0.0017, in fp16 by 0.00026 to 0.00028 instead of 0.0002. The sum is of the unrounded ones.
             auto weights = [&](const uint32_t (&v)[kBN / 2], uint32_t (&pk)[32], int k0) {   // of v's scores k0 .. k0 + 32
 #pragma unroll
                 for (int k = k0 / 2; k < k0 / 2 + 16; ++k) {
@@ -1316,8 +1321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Waiter w{abort_flag, p.wait_limit_ns};
 
     // The roles' loops share an instruction cache that their program does not fit, so their
-    // order counts: a prompt of 4096 tokens takes 139 us in this one, two with heads of 64
-    // 185; 138 to 155 and 191 to 210 in seven others of the last four.
+    // order counts: a prompt of 4096 tokens takes 136 us in this one, two with heads of 64
+    // 186; 136 to 157 and 191 to 206 in eight others of the last four.
     if (warp < kCorrWarp0) {
         ptx::setmaxnreg_inc<kRegSoft>();
         softmax_role<D, kBf16>(p, tmem, smem, bars, w, gate, warp / 4);

@@ -30,9 +30,9 @@ namespace rope {
 constexpr int kSiteAxis = 56;   // an entry of `axes` outside 0 .. n_axes - 1
 constexpr int kThreads = 256;
 // Tokens of a block where there are many, items (32 bytes) of a thread in flight
-// and blocks an SM. 8191 tokens of 48 heads take 38.9 us; 45.1 with 8, 4 and 3
-// (what 80 registers allow), 41.0 with 2, 2 and 5; 4, 3 and 4 take as long, but 18.4 us
-// for 2000 tokens instead of 16.4.
+// and blocks an SM. 8191 tokens of 48 heads, one call behind another, take 33 us; 36 with
+// 8, 4 and 3 (what 80 registers allow), 34.7 with 2, 2 and 5; 4, 3 and 4 take as long, but 9.2
+// us for 2000 tokens instead of 8.5 (2, 2 and 5: 7.7).
 constexpr int kTokens = 4, kBatch = 2, kBlocks = 5;
 
 struct Params {
